@@ -342,7 +342,7 @@ def _plain(s):
 def _plan(s, cl):
     """The descriptors and workspaces a program keeps beside its buffers."""
     c, op = s["case"], s["case"]["op"]
-    q8 = lambda k, fmt: cl.q8(fmt, s[k], s[k + "_exps"])  # noqa: E731
+    ckpt = lambda k, fmt: cl.ckpt(fmt, s[k], s[k + "_exps"])  # noqa: E731
     p = {}
     need = 0
     if op in ("join_fwd", "join_bwd"):
@@ -355,10 +355,10 @@ def _plan(s, cl):
                                                                   "pre_b")})
         if op == "join_bwd":
             eight = c["saved"] != "same"
-            fmt = cl.Q8_INT8 if c["saved"] == "int8" else cl.Q8_E4M3
+            fmt = cl.CKPT_INT8 if c["saved"] == "int8" else cl.CKPT_E4M3
             p["saved"] = cl.residual_norm_saved(
                 x=s["x"] if s["res_w"] is not None else None, y=None if eight else s["y"], h=None if eight else s["h"],
-                y_q8=q8("y", fmt) if eight else None, h_q8=q8("h", fmt) if eight else None,
+                y_ckpt=ckpt("y", fmt) if eight else None, h_ckpt=ckpt("h", fmt) if eight else None,
                 mean_y=s.get("mean_y"), rstd_y=s["rstd_y"], mean_h=s.get("mean_h"), rstd_h=s["rstd_h"])
             p["grads"] = cl.residual_norm_grads(**{k: s[k] for k in ("dx", "dy", "dpost_w", "dpost_b", "dgate", "dres_w",
                                                                     "dpre_w", "dpre_b")})
@@ -366,12 +366,12 @@ def _plan(s, cl):
         else:
             p["out"] = cl.residual_norm_out(**{k: s.get(k) for k in ("h", "a", "mean_y", "rstd_y", "mean_h", "rstd_h")})
     elif op == "pack":
-        p["q8"] = cl.q8(cl.Q8_INT8 if c["fmt"] == "int8" else cl.Q8_E4M3, s["code"], s["exps"])
+        p["ckpt"] = cl.ckpt(cl.CKPT_INT8 if c["fmt"] == "int8" else cl.CKPT_E4M3, s["code"], s["exps"])
     elif op == "unpack":
-        p["q8"] = q8("code", cl.Q8_INT8 if c["fmt"] == "int8" else cl.Q8_E4M3)
+        p["ckpt"] = ckpt("code", cl.CKPT_INT8 if c["fmt"] == "int8" else cl.CKPT_E4M3)
     else:
-        p["q8"] = q8("x", cl.Q8_INT8 if c["fmt"] == "int8" else cl.Q8_E4M3)
-        need = cl.collider_linear_q8_workspace_size(s["M"], c["K"], c["N"])
+        p["ckpt"] = ckpt("x", cl.CKPT_INT8 if c["fmt"] == "int8" else cl.CKPT_E4M3)
+        need = cl.collider_linear_ckpt_workspace_size(s["M"], c["K"], c["N"])
     p["ws"] = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
     return p
 
@@ -395,12 +395,12 @@ def _own(s):
     dt = cl.F32 if c.get("dtype") == "f32" else cl.BF16
     side = lambda k: cl.ROWS_FULL if c[k] == "full" else cl.ROWS_COMPACT  # noqa: E731
     if op == "pack":
-        cl.collider_q8_pack(dt, s["v"], c["N"], M, c["N"], idx, nk, p["q8"])
+        cl.collider_ckpt_pack(dt, s["v"], c["N"], M, c["N"], idx, nk, p["ckpt"])
         return _codes(s["code"][:n], s["exps"][:n], c["fmt"])
     if op == "unpack":
-        cl.collider_q8_unpack(dt, p["q8"], side("src"), M, c["N"], idx, nk, s["out"], c["N"], side("dst"))
+        cl.collider_ckpt_unpack(dt, p["ckpt"], side("src"), M, c["N"], idx, nk, s["out"], c["N"], side("dst"))
         return s["out"] if c["dst"] == "full" else s["out"][:n]
-    cl.collider_linear_bwd_q8(M, c["K"], c["N"], p["q8"], side("src"), s["w"], s["dy"], cl.ROWS_FULL, s["idx"], s["nk"],
+    cl.collider_linear_bwd_ckpt(M, c["K"], c["N"], p["ckpt"], side("src"), s["w"], s["dy"], cl.ROWS_FULL, s["idx"], s["nk"],
                               s["dx"], cl.ROWS_FULL, s["dw"], s["db"], p["ws"])
     return {k: s[k] for k in ("dx", "dw", "db") if s[k] is not None}
 
