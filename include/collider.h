@@ -65,6 +65,7 @@ typedef enum { COLLIDER_ROWS_FULL = 0, COLLIDER_ROWS_COMPACT = 1 } collider_rows
 typedef enum { COLLIDER_ARCH_LLAMA = 0, COLLIDER_ARCH_PHI = 1 } collider_arch;
 typedef enum { COLLIDER_NORM_RMS = 0, COLLIDER_NORM_LAYER = 1 } collider_norm;
 typedef enum { COLLIDER_ACT_SWIGLU = 0, COLLIDER_ACT_GELU_TANH = 1 } collider_act;
+typedef enum { COLLIDER_CKPT_E4M3 = 0, COLLIDER_CKPT_INT8 = 1 } collider_ckpt_format;
 
 /* ------------------------------------------------------------------------ */
 /* Status                                                                    */
@@ -202,6 +203,165 @@ collider_status collider_linear_bwd(collider_dtype dtype, int M, int K, int N,
                                     const int32_t* idx, const int32_t* n_kept,
                                     void* dX, collider_rows dx_rows, float* dW, float* db,
                                     void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit activation checkpoints (the pages have no counterpart: what a       */
+/* training step keeps of its forward, at half the bytes)                    */
+/* ------------------------------------------------------------------------ */
+
+/* A checkpoint of rows of N values, N a multiple of 32: a code of 8 bits for
+ * each value and an exponent byte for each 32 consecutive values of a row.
+ *   value = code * 2^(byte - 127), byte 255: NaN.
+ * format COLLIDER_CKPT_E4M3: codes are e4m3 floats (4 exponent bits, 3 mantissa
+ * bits, no infinity); COLLIDER_CKPT_INT8: two's complement whole numbers.
+ * Packing takes for each group the smallest exponent e >= -120 for which
+ * max|v| <= L 2^e (L = 448 for e4m3, 127 for int8), rounds each v 2^-e to the
+ * nearest code, ties to even, and stores e + 127; a group that holds a NaN or
+ * an infinity gets byte 255 and codes 0, and decodes to NaN everywhere.  So a
+ * value v is kept to within 2^-4 |v| or 2^(e-10) (e4m3), 2^(e-1) (int8),
+ * whichever is larger, and decoding is exact in bf16 and f32.
+ * code and exps are device memory, or pinned host memory that the device
+ * addresses at the same pointer (an offloaded checkpoint).  Rows are code_ld
+ * and exp_ld bytes apart: code 16-byte aligned, code_ld a multiple of 16. */
+typedef struct {
+  int format;      /* collider_ckpt_format */
+  void* code;      /* u8 [rows, code_ld], N used */
+  void* exps;      /* u8 [rows, exp_ld], N / 32 used */
+  size_t code_ld;
+  size_t exp_ld;
+} collider_ckpt;
+
+/* Packs rows of src ([M, N] of dtype COLLIDER_BF16 or COLLIDER_F32, row
+ * stride src_ld elements): with idx and n_kept the kept rows, COMPACT (row r
+ * of the checkpoint is row idx[r] of src, r < n_kept; the checkpoint needs
+ * room for n_kept rows, and rows beyond are left as they were); both NULL:
+ * every row.  1 <= M <= 2^30. */
+collider_status collider_ckpt_pack(collider_dtype dtype, const void* src, size_t src_ld, int M, int N,
+                                 const int32_t* idx, const int32_t* n_kept, const collider_ckpt* out,
+                                 void* stream);
+
+/* Decodes the kept rows of a checkpoint into dst ([M, N] of dtype, row stride
+ * dst_ld elements).  src_rows: the checkpoint holds FULL rows (read through
+ * idx) or COMPACT ones.  dst_rows FULL: kept row r goes to row idx[r], every
+ * other row is written 0; COMPACT: to row r, with zero rows up to the next
+ * multiple of 128.  idx and n_kept NULL: all M rows, in order. */
+collider_status collider_ckpt_unpack(collider_dtype dtype, const collider_ckpt* src, collider_rows src_rows,
+                                   int M, int N, const int32_t* idx, const int32_t* n_kept, void* dst,
+                                   size_t dst_ld, collider_rows dst_rows, void* stream);
+
+/* collider_linear_bwd (bf16) with X [M, K] saved as an 8-bit checkpoint of
+ * FULL or COMPACT rows: dW = X_k^T . dY_k of the decoded values, dX and db as
+ * there.  The products of each 2048 kept rows accumulate on the tensor cores
+ * and are added in f32.  K % 32 == 0 (K % 8 == 0 when dW is NULL, and X may
+ * be NULL then), N % 8 == 0, 1 <= M <= 2^30.  Workspace:
+ * collider_linear_ckpt_workspace_size(). */
+size_t collider_linear_ckpt_workspace_size(int M, int K, int N);
+collider_status collider_linear_bwd_ckpt(int M, int K, int N, const collider_ckpt* X, collider_rows x_rows,
+                                       const void* W, const void* dY, collider_rows dy_rows,
+                                       const int32_t* idx, const int32_t* n_kept, void* dX,
+                                       collider_rows dx_rows, float* dW, float* db, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Residual join: the norms after and before a block's branch, with its gate */
+/* and residual scale (the pages have no counterpart: the step between two   */
+/* branches of a sandwich-normed decoder, as the norm entry of a block)      */
+/* ------------------------------------------------------------------------ */
+
+/* For token t of sequence b, x the residual stream, y the branch's output:
+ *   h = res_scale * res_w . x + gate_b . post(y)       (. element-wise)
+ *   a = pre(h)                                         (of h as it is stored)
+ * post and pre are RMSNorm (w v r) or LayerNorm (w (v - m) r + b) over the D
+ * values of a row, r = (mean square, or variance, + eps)^(-1/2); either may be
+ * left out (post: y itself; pre: no a).  gate and res_w may be left out (1).
+ * Without y (NULL) only a = pre(x) is computed: a block's first norm. */
+typedef struct {
+  int dtype;          /* collider_dtype of x, y, h, a, their gradients and the parameters */
+  int B, T;           /* tokens: B * T <= 2^30 */
+  int D;              /* values a row: a multiple of 8, at most 8192 */
+  int norm;           /* collider_norm of both norms */
+  int post, pre;      /* nonzero: the norm is there */
+  float eps;          /* > 0 */
+  float res_scale;
+  int gate_rows;      /* rows of gate: 0 (no gate), 1 (all tokens), B (one a sequence) */
+  int x_ld, y_ld, h_ld, a_ld; /* row strides in elements of x, y, h, a and of their
+                                 gradients dx, dy, dh, da; 0 means D */
+} collider_residual_norm_desc;
+
+/* Parameters, dtype [D] (gate [gate_rows, D]).  NULL where the desc has none;
+ * post_b and pre_b (LayerNorm) may be NULL: no bias. */
+typedef struct {
+  const void* post_w;
+  const void* post_b;
+  const void* gate;
+  const void* res_w;
+  const void* pre_w;
+  const void* pre_b;
+} collider_residual_norm_params;
+
+/* What the forward writes: h [M, D] (with y), a [M, D] (with pre), and the
+ * f32 row statistics [M] of the norms there are (means: LayerNorm only). */
+typedef struct {
+  void* h;
+  void* a;
+  float* mean_y;
+  float* rstd_y;
+  float* mean_h;
+  float* rstd_h;
+} collider_residual_norm_out;
+
+/* All M = B*T rows (the forward stays dense).  h may be x or y (in place,
+ * same stride); a aliases nothing.  No workspace. */
+collider_status collider_residual_norm_fwd(const collider_residual_norm_desc* desc,
+                                           const collider_residual_norm_params* params, const void* x,
+                                           const void* y, const collider_residual_norm_out* out,
+                                           void* stream);
+
+/* What the backward reads: y and h (x in the place of h when the forward had
+ * no y) as rows of dtype or as 8-bit checkpoints (both in the same form, D a
+ * multiple of 32; device memory), x only for dres_w; FULL or COMPACT rows.
+ * The statistics are FULL [M]. */
+typedef struct {
+  const void* x;
+  const void* y;
+  const void* h;
+  const collider_ckpt* y_ckpt;
+  const collider_ckpt* h_ckpt;
+  const float* mean_y;
+  const float* rstd_y;
+  const float* mean_h;
+  const float* rstd_h;
+} collider_residual_norm_saved;
+
+/* dx and dy (with y) of dtype; the parameters' gradients f32, [D], dgate
+ * [gate_rows, D], overwritten; NULL ones are not computed. */
+typedef struct {
+  void* dx;
+  void* dy;
+  float* dpost_w;
+  float* dpost_b;
+  float* dgate;
+  float* dres_w;
+  float* dpre_w;
+  float* dpre_b;
+} collider_residual_norm_grads;
+
+/* Backward on the kept rows.  da is the gradient of a (with pre; else NULL),
+ * dh that of h along the residual stream (NULL: none; required without pre);
+ * both FULL or COMPACT rows (in_rows).  dx and dy are FULL (filtered rows 0) or
+ * COMPACT (zero rows up to the next multiple of 128).  idx, cu_kept and n_kept
+ * all NULL: every token is kept.  dx may be dh (same rows and stride); no other
+ * output may alias an input.  Sums are f32 in a fixed order: bit-identical
+ * from run to run.  A kept index outside the tokens is skipped and reported
+ * by collider_check. */
+size_t collider_residual_norm_bwd_workspace_size(const collider_residual_norm_desc* desc);
+collider_status collider_residual_norm_bwd(const collider_residual_norm_desc* desc,
+                                           const collider_residual_norm_params* params,
+                                           const collider_residual_norm_saved* saved, collider_rows saved_rows,
+                                           const void* da, const void* dh, collider_rows in_rows,
+                                           const int32_t* idx, const int32_t* cu_kept, const int32_t* n_kept,
+                                           const collider_residual_norm_grads* grads, collider_rows out_rows,
+                                           void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* a7/a8. Attention backward over the compacted sequences (Figs. 3 and 5)    */

@@ -17,6 +17,10 @@ __all__ = [
     "ColliderError", "lib", "LIB_PATH", "ROWS_FULL", "ROWS_COMPACT", "F32", "BF16",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_CUDA", "ERR_TIMEOUT",
     "ARCH_LLAMA", "ARCH_PHI", "NORM_RMS", "NORM_LAYER", "ACT_SWIGLU", "ACT_GELU_TANH",
+    "CKPT_E4M3", "CKPT_INT8", "Ckpt", "ckpt", "ResidualNormDesc", "ResidualNormParams", "ResidualNormOut", "ResidualNormSaved",
+    "ResidualNormGrads", "residual_norm_params", "residual_norm_out", "residual_norm_saved", "residual_norm_grads",
+    "collider_ckpt_pack", "collider_ckpt_unpack", "collider_linear_ckpt_workspace_size", "collider_linear_bwd_ckpt",
+    "collider_residual_norm_fwd", "collider_residual_norm_bwd_workspace_size", "collider_residual_norm_bwd",
     "LayerDesc", "LayerWeights", "LayerSaved", "LayerGrads", "LayerParams", "LayerActs", "EXPORTED",
     "collider_last_error", "collider_check", "collider_selftest_wait_timeout", "collider_launch_count",
     "collider_profile_enable", "collider_profile_count", "collider_profile_get", "collider_profile_get_span",
@@ -37,6 +41,7 @@ ROWS_FULL, ROWS_COMPACT = 0, 1
 ARCH_LLAMA, ARCH_PHI = 0, 1
 NORM_RMS, NORM_LAYER = 0, 1
 ACT_SWIGLU, ACT_GELU_TANH = 0, 1
+CKPT_E4M3, CKPT_INT8 = 0, 1
 
 
 class ColliderError(RuntimeError):
@@ -76,6 +81,36 @@ class LayerActs(C.Structure):
                                           "s")]
 
 
+class Ckpt(C.Structure):
+    """An 8-bit checkpoint (``collider_ckpt``); see :func:`ckpt`."""
+    _fields_ = [("format", C.c_int), ("code", C.c_void_p), ("exps", C.c_void_p), ("code_ld", C.c_size_t),
+                ("exp_ld", C.c_size_t)]
+
+
+class ResidualNormDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("B", C.c_int), ("T", C.c_int), ("D", C.c_int), ("norm", C.c_int),
+                ("post", C.c_int), ("pre", C.c_int), ("eps", C.c_float), ("res_scale", C.c_float),
+                ("gate_rows", C.c_int), ("x_ld", C.c_int), ("y_ld", C.c_int), ("h_ld", C.c_int), ("a_ld", C.c_int)]
+
+
+class ResidualNormParams(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("post_w", "post_b", "gate", "res_w", "pre_w", "pre_b")]
+
+
+class ResidualNormOut(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("h", "a", "mean_y", "rstd_y", "mean_h", "rstd_h")]
+
+
+class ResidualNormSaved(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("h", C.c_void_p), ("y_ckpt", C.POINTER(Ckpt)),
+                ("h_ckpt", C.POINTER(Ckpt)), ("mean_y", C.c_void_p), ("rstd_y", C.c_void_p), ("mean_h", C.c_void_p),
+                ("rstd_h", C.c_void_p)]
+
+
+class ResidualNormGrads(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("dx", "dy", "dpost_w", "dpost_b", "dgate", "dres_w", "dpre_w", "dpre_b")]
+
+
 P = C.c_void_p
 I = C.c_int
 SZ = C.c_size_t
@@ -97,6 +132,16 @@ _SIGS = {
     "collider_scatter_rows": (I, [P, SZ, P, SZ, SZ, I, P, P, P]),
     "collider_linear_workspace_size": (SZ, [I, I, I, I]),
     "collider_linear_bwd": (I, [I, I, I, I, P, I, P, P, I, P, P, P, I, P, P, P, SZ, P]),
+    "collider_ckpt_pack": (I, [I, P, SZ, I, I, P, P, C.POINTER(Ckpt), P]),
+    "collider_ckpt_unpack": (I, [I, C.POINTER(Ckpt), I, I, I, P, P, P, SZ, I, P]),
+    "collider_linear_ckpt_workspace_size": (SZ, [I, I, I]),
+    "collider_linear_bwd_ckpt": (I, [I, I, I, C.POINTER(Ckpt), I, P, P, I, P, P, P, I, P, P, P, SZ, P]),
+    "collider_residual_norm_fwd": (I, [C.POINTER(ResidualNormDesc), C.POINTER(ResidualNormParams), P, P,
+                                       C.POINTER(ResidualNormOut), P]),
+    "collider_residual_norm_bwd_workspace_size": (SZ, [C.POINTER(ResidualNormDesc)]),
+    "collider_residual_norm_bwd": (I, [C.POINTER(ResidualNormDesc), C.POINTER(ResidualNormParams),
+                                       C.POINTER(ResidualNormSaved), I, P, P, I, P, P, P,
+                                       C.POINTER(ResidualNormGrads), I, P, SZ, P]),
     "collider_attn_workspace_size": (SZ, [I, I, I, I, I]),
     "collider_attn_bwd": (I, [I, I, I, I, I, I, C.c_float, I, C.c_float, P, P, P, P, P, I, I, I, I, P,
                               P, P, P, P, P, P, I, P, SZ, P]),
@@ -245,6 +290,87 @@ def collider_linear_bwd(dtype, M, K, N, X, x_rows, W, dY, dy_rows, idx, n_kept, 
     _check(lib().collider_linear_bwd(dtype, M, K, N, _ptr(X), x_rows, _ptr(W), _ptr(dY), dy_rows, _ptr(idx),
                                      _ptr(n_kept), _ptr(dX), dx_rows, _ptr(dW), _ptr(db), _ptr(ws), _nbytes(ws),
                                      _stream(stream)))
+
+
+def _filled(struct, tensors):
+    """The struct with these buffers' addresses; it keeps the buffers alive."""
+    unknown = set(tensors) - {f[0] for f in struct._fields_}
+    if unknown:
+        raise TypeError(f"{struct.__name__} has no field {sorted(unknown)[0]}")
+    s = struct()
+    s.buffers = tensors
+    for k, v in tensors.items():
+        if isinstance(v, Ckpt):
+            setattr(s, k, C.pointer(v))
+        elif v is not None:
+            setattr(s, k, _ptr(v))
+    return s
+
+
+def ckpt(format, code, exps) -> Ckpt:
+    """The 8-bit checkpoint whose codes and exponent bytes are the rows of two uint8 tensors ``[rows, N]`` and
+    ``[rows, N // 32]`` (a row's bytes adjacent)."""
+    for t in (code, exps):
+        if t.dim() != 2 or t.element_size() != 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise TypeError("codes and exponents are 2-D tensors of bytes, a row's bytes adjacent")
+    q = Ckpt(format=format, code=code.data_ptr(), exps=exps.data_ptr(), code_ld=code.stride(0), exp_ld=exps.stride(0))
+    q.buffers = (code, exps)
+    return q
+
+
+def residual_norm_params(**tensors) -> ResidualNormParams:
+    """ResidualNormParams from tensors by field name (None or absent: NULL)."""
+    return _filled(ResidualNormParams, tensors)
+
+
+def residual_norm_out(**tensors) -> ResidualNormOut:
+    return _filled(ResidualNormOut, tensors)
+
+
+def residual_norm_saved(**tensors) -> ResidualNormSaved:
+    """ResidualNormSaved from tensors and :func:`ckpt` checkpoints (y_ckpt, h_ckpt) by field name."""
+    return _filled(ResidualNormSaved, tensors)
+
+
+def residual_norm_grads(**tensors) -> ResidualNormGrads:
+    return _filled(ResidualNormGrads, tensors)
+
+
+def collider_ckpt_pack(dtype, src, src_ld, M, N, idx, n_kept, out, stream=None) -> None:
+    _check(lib().collider_ckpt_pack(dtype, _ptr(src), src_ld, M, N, _ptr(idx), _ptr(n_kept), C.byref(out),
+                                  _stream(stream)))
+
+
+def collider_ckpt_unpack(dtype, src, src_rows, M, N, idx, n_kept, dst, dst_ld, dst_rows, stream=None) -> None:
+    _check(lib().collider_ckpt_unpack(dtype, C.byref(src), src_rows, M, N, _ptr(idx), _ptr(n_kept), _ptr(dst), dst_ld,
+                                    dst_rows, _stream(stream)))
+
+
+def collider_linear_ckpt_workspace_size(M, K, N) -> int:
+    return lib().collider_linear_ckpt_workspace_size(M, K, N)
+
+
+def collider_linear_bwd_ckpt(M, K, N, X, x_rows, W, dY, dy_rows, idx, n_kept, dX, dx_rows, dW, db, ws,
+                           stream=None) -> None:
+    _check(lib().collider_linear_bwd_ckpt(M, K, N, None if X is None else C.byref(X), x_rows, _ptr(W), _ptr(dY), dy_rows,
+                                        _ptr(idx), _ptr(n_kept), _ptr(dX), dx_rows, _ptr(dW), _ptr(db), _ptr(ws),
+                                        _nbytes(ws), _stream(stream)))
+
+
+def collider_residual_norm_fwd(desc, params, x, y, out, stream=None) -> None:
+    _check(lib().collider_residual_norm_fwd(C.byref(desc), C.byref(params), _ptr(x), _ptr(y), C.byref(out),
+                                            _stream(stream)))
+
+
+def collider_residual_norm_bwd_workspace_size(desc) -> int:
+    return lib().collider_residual_norm_bwd_workspace_size(C.byref(desc))
+
+
+def collider_residual_norm_bwd(desc, params, saved, saved_rows, da, dh, in_rows, idx, cu_kept, n_kept, grads, out_rows,
+                               ws, stream=None) -> None:
+    _check(lib().collider_residual_norm_bwd(C.byref(desc), C.byref(params), C.byref(saved), saved_rows, _ptr(da),
+                                            _ptr(dh), in_rows, _ptr(idx), _ptr(cu_kept), _ptr(n_kept), C.byref(grads),
+                                            out_rows, _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def collider_attn_workspace_size(B, T, H, Hkv, dh) -> int:

@@ -10,12 +10,14 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
 
 #include "../../include/collider.h"
 #include "internal.h"
+#include "q8.cuh"
 #include "tc_ptx.cuh"
 
 namespace collider {
@@ -99,6 +101,29 @@ collider_status make_ctx(void* stream, Ctx* c) {
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 long long pad128(long long m) { return (m + 127) & ~127ll; }
+
+// Every pointer given must be memory of the current device (or managed);
+// host_ok: or pinned host memory that the device addresses at the same pointer.
+collider_status check_memory(const char* fn, std::initializer_list<const void*> ps, bool host_ok = false) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  for (const void* p : ps) {
+    if (!p) continue;
+    cudaPointerAttributes a{};
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+      cudaGetLastError();
+      return fail(COLLIDER_ERR_INVALID_ARG, "%s: a pointer the CUDA runtime does not know", fn);
+    }
+    if (a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == dev)) continue;
+    if (host_ok && a.type == cudaMemoryTypeHost && a.devicePointer == p) continue;
+    return fail(COLLIDER_ERR_INVALID_ARG, a.type == cudaMemoryTypeDevice
+                                              ? "%s: a buffer lives on another device than the current one"
+                                              : "%s: a buffer is not memory this call may use (device memory needed%s)",
+                fn, host_ok ? ", or pinned host memory" : "");
+  }
+  return COLLIDER_OK;
+}
 
 // bump allocator over the caller's workspace
 struct Carver {
@@ -323,6 +348,73 @@ extern "C" collider_status collider_scatter_rows(const void* compact, size_t com
 }
 
 // ===========================================================================
+// 8-bit activation checkpoints
+// ===========================================================================
+namespace {
+Q8View view(const collider_ckpt* q) {
+  return Q8View{static_cast<uint8_t*>(q->code), static_cast<uint8_t*>(q->exps), (long long)q->code_ld,
+                (long long)q->exp_ld};
+}
+// a checkpoint of rows of N values
+collider_status check_ckpt(const char* fn, const collider_ckpt* q, int N) {
+  if (!q || !q->code || !q->exps) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null checkpoint", fn);
+  if (q->format != COLLIDER_CKPT_E4M3 && q->format != COLLIDER_CKPT_INT8)
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: checkpoint format %d", fn, q->format);
+  if (N < 32 || N % 32) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: checkpoint rows need N %% 32 == 0", fn);
+  if (!al16(q->code) || q->code_ld % 16 || q->code_ld < (size_t)N || q->exp_ld < (size_t)N / 32 ||
+      q->code_ld > (1u << 30) || q->exp_ld > (1u << 30))
+    return fail(COLLIDER_ERR_INVALID_ARG,
+                "%s: checkpoint codes must be 16-byte aligned rows of >= N bytes, exponents rows of >= N / 32", fn);
+  return COLLIDER_OK;
+}
+// rows of N values of `dtype` with a stride of ld elements
+collider_status check_rows(const char* fn, int dtype, const void* p, long long ld, int N) {
+  if (!al16(p) || ld < N || ld % (dtype == COLLIDER_F32 ? 4 : 8))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned, with a stride of at least their length", fn);
+  return COLLIDER_OK;
+}
+bool is_rows(collider_rows r) { return r == COLLIDER_ROWS_FULL || r == COLLIDER_ROWS_COMPACT; }
+}  // namespace
+
+extern "C" collider_status collider_ckpt_pack(collider_dtype dtype, const void* src, size_t src_ld, int M, int N,
+                                            const int32_t* idx, const int32_t* n_kept, const collider_ckpt* out,
+                                            void* stream) {
+  static const char* fn = "collider_ckpt_pack";
+  if (dtype != COLLIDER_F32 && dtype != COLLIDER_BF16) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: dtype %d", fn, (int)dtype);
+  if (!src || !idx != !n_kept) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null src, or only one of idx and n_kept", fn);
+  if (M < 1 || M > (1 << 30)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need 1 <= M <= 2^30", fn);
+  collider_status s = check_ckpt(fn, out, N);
+  if (s == COLLIDER_OK) s = check_rows(fn, dtype, src, (long long)src_ld, N);
+  Ctx c;
+  if (s == COLLIDER_OK) s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_memory(fn, {src, idx, n_kept});
+  if (s == COLLIDER_OK) s = check_memory(fn, {out->code, out->exps}, true);
+  if (s != COLLIDER_OK) return s;
+  CK(launch_q8_pack(c, dtype == COLLIDER_F32, src, (long long)src_ld, M, N, idx, n_kept, out->format, view(out)));
+  return COLLIDER_OK;
+}
+
+extern "C" collider_status collider_ckpt_unpack(collider_dtype dtype, const collider_ckpt* src, collider_rows src_rows, int M,
+                                              int N, const int32_t* idx, const int32_t* n_kept, void* dst,
+                                              size_t dst_ld, collider_rows dst_rows, void* stream) {
+  static const char* fn = "collider_ckpt_unpack";
+  if (dtype != COLLIDER_F32 && dtype != COLLIDER_BF16) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: dtype %d", fn, (int)dtype);
+  if (!dst || !idx != !n_kept) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null dst, or only one of idx and n_kept", fn);
+  if (M < 1 || M > (1 << 30)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need 1 <= M <= 2^30", fn);
+  if (!is_rows(src_rows) || !is_rows(dst_rows)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
+  collider_status s = check_ckpt(fn, src, N);
+  if (s == COLLIDER_OK) s = check_rows(fn, dtype, dst, (long long)dst_ld, N);
+  Ctx c;
+  if (s == COLLIDER_OK) s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_memory(fn, {dst, idx, n_kept});
+  if (s == COLLIDER_OK) s = check_memory(fn, {src->code, src->exps}, true);
+  if (s != COLLIDER_OK) return s;
+  CK(launch_q8_unpack(c, dtype == COLLIDER_F32, src->format, view(src), src_rows == COLLIDER_ROWS_FULL, M, N, idx,
+                      n_kept, dst, (long long)dst_ld, dst_rows == COLLIDER_ROWS_FULL, M));
+  return COLLIDER_OK;
+}
+
+// ===========================================================================
 // a3/a4 linear backward
 // ===========================================================================
 namespace {
@@ -347,6 +439,63 @@ size_t linear_carve(Carver& cv, collider_dtype dt, int M, int K, int N, bool x_f
     cv.take<int>(sk_counter_cap(std::max<long long>(M, K), std::max(K, N)));
   }
   return cv.used;
+}
+
+// The bf16 linear backward: compact operands (zero-padded to 128 rows),
+// tcgen05 GEMMs.  X is bf16 rows, or (ck) an 8-bit checkpoint decoded into the
+// compact copy.  xk, dyk, dxk, part: the workspace's buffers.
+struct LinearBufs {
+  void *xk, *dyk, *dxk;
+  float* part;
+  float* sk_partial;
+  int* sk_counters;
+  long long sk_cap;
+};
+collider_status linear_bf16(const Ctx& c, int M, int K, int N, const void* X, const collider_ckpt* ck, bool x_full,
+                            const void* W, const void* dY, bool dy_full, const int32_t* idx, const int32_t* n_kept,
+                            void* dX, bool dx_full, float* dW, float* db, const LinearBufs& L) {
+  const __nv_bfloat16* Xk = static_cast<const __nv_bfloat16*>(L.xk);
+  const __nv_bfloat16* dYk = static_cast<const __nv_bfloat16*>(L.dyk);
+  {
+    const GatherJob jx{static_cast<const char*>(X), static_cast<char*>(L.xk), (long long)K * 2, (long long)K * 2,
+                       K * 2, 0};
+    const GatherJob jy{static_cast<const char*>(dY), static_cast<char*>(L.dyk), (long long)N * 2, (long long)N * 2,
+                       N * 2, 0};
+    if (dW && ck)
+      CK(launch_q8_unpack(c, 0, ck->format, view(ck), x_full, M, K, idx, n_kept, L.xk, K, 0, pad128(M)));
+    else if (dW)
+      CK(launch_gather(c, &jx, 1, M, pad128(M), x_full ? idx : nullptr, n_kept));
+    CK(launch_gather(c, &jy, 1, M, pad128(M), dy_full ? idx : nullptr, n_kept));
+  }
+  if (dX) {
+    TcGemm g{};
+    g.M = M; g.N = K; g.K = N;
+    g.A = dYk; g.lda = N; g.a_mn_major = 0; g.a_rows = M;
+    g.B = W; g.ldb = N; g.b_mn_major = 0; g.b_rows = K;
+    g.C = dx_full ? L.dxk : dX; g.ldc = K; g.c_bf16 = 1; g.zero_pad = 1; g.c_rows = dx_full ? pad128(M) : M;
+    g.n_kept = n_kept; g.dyn = 1;
+    g.partial = L.sk_partial; g.counters = L.sk_counters; g.counter_cap = L.sk_cap;
+    CK(launch_tc_gemm(c, g));
+    if (dx_full) CK(launch_scatter(c, static_cast<const char*>(L.dxk), (long long)K * 2, static_cast<char*>(dX),
+                                   (long long)K * 2, K * 2, M, idx, n_kept));
+  }
+  if (dW) {
+    TcGemm g{};
+    g.M = K; g.N = N; g.K = M;
+    g.A = Xk; g.lda = K; g.a_mn_major = 1; g.a_rows = M;
+    g.B = dYk; g.ldb = N; g.b_mn_major = 1; g.b_rows = M;
+    g.C = dW; g.ldc = N; g.c_bf16 = 0;
+    g.n_kept = n_kept; g.dyn = 2;
+    // the tensor core's running sum drops bits below its last place at every
+    // step, so its error grows with the reduction: 2048 rows at a time (at
+    // most 5e-7 of the result's norm on normal inputs, against 1.3e-6 at 4096
+    // rows and 3.5e-6 at 16384), added in f32
+    if (ck) g.k_piece = 32;
+    g.partial = L.sk_partial; g.counters = L.sk_counters; g.counter_cap = L.sk_cap;
+    CK(launch_tc_gemm(c, g));
+  }
+  if (db) CK(launch_colsum(c, dYk, 1, N, M, N, nullptr, n_kept, L.part, db));
+  return COLLIDER_OK;
 }
 }  // namespace
 
@@ -430,43 +579,47 @@ extern "C" collider_status collider_linear_bwd(collider_dtype dtype, int M, int 
     return COLLIDER_OK;
   }
 
-  // bf16: compact operands (zero-padded to 128 rows), tcgen05 GEMMs
-  const __nv_bfloat16* Xk = static_cast<const __nv_bfloat16*>(X);
-  const __nv_bfloat16* dYk = static_cast<const __nv_bfloat16*>(dY);
-  {
-    const GatherJob jx{static_cast<const char*>(X), static_cast<char*>(xk), (long long)K * 2, (long long)K * 2,
-                       K * 2, 0};
-    const GatherJob jy{static_cast<const char*>(dY), static_cast<char*>(dyk), (long long)N * 2, (long long)N * 2,
-                       N * 2, 0};
-    if (dW) CK(launch_gather(c, &jx, 1, M, pad128(M), x_full ? idx : nullptr, n_kept));
-    CK(launch_gather(c, &jy, 1, M, pad128(M), dy_full ? idx : nullptr, n_kept));
-    if (dW) Xk = static_cast<const __nv_bfloat16*>(xk);
-    dYk = static_cast<const __nv_bfloat16*>(dyk);
-  }
-  if (dX) {
-    TcGemm g{};
-    g.M = M; g.N = K; g.K = N;
-    g.A = dYk; g.lda = N; g.a_mn_major = 0; g.a_rows = M;
-    g.B = W; g.ldb = N; g.b_mn_major = 0; g.b_rows = K;
-    g.C = dx_full ? dxk : dX; g.ldc = K; g.c_bf16 = 1; g.zero_pad = 1; g.c_rows = dx_full ? pad128(M) : M;
-    g.n_kept = n_kept; g.dyn = 1;
-    g.partial = sk_partial; g.counters = sk_counters; g.counter_cap = sk_cap;
-    CK(launch_tc_gemm(c, g));
-    if (dx_full) CK(launch_scatter(c, static_cast<const char*>(dxk), (long long)K * 2, static_cast<char*>(dX),
-                                   (long long)K * 2, K * 2, M, idx, n_kept));
-  }
-  if (dW) {
-    TcGemm g{};
-    g.M = K; g.N = N; g.K = M;
-    g.A = Xk; g.lda = K; g.a_mn_major = 1; g.a_rows = M;
-    g.B = dYk; g.ldb = N; g.b_mn_major = 1; g.b_rows = M;
-    g.C = dW; g.ldc = N; g.c_bf16 = 0;
-    g.n_kept = n_kept; g.dyn = 2;
-    g.partial = sk_partial; g.counters = sk_counters; g.counter_cap = sk_cap;
-    CK(launch_tc_gemm(c, g));
-  }
-  if (db) CK(launch_colsum(c, dYk, 1, N, M, N, nullptr, n_kept, part, db));
-  return COLLIDER_OK;
+  return linear_bf16(c, M, K, N, X, nullptr, x_full, W, dY, dy_full, idx, n_kept, dX, dx_full, dW, db,
+                     LinearBufs{xk, dyk, dxk, part, sk_partial, sk_counters, sk_cap});
+}
+
+extern "C" size_t collider_linear_ckpt_workspace_size(int M, int K, int N) {
+  return collider_linear_workspace_size(COLLIDER_BF16, M, K, N);
+}
+
+extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const collider_ckpt* X, collider_rows x_rows,
+                                                  const void* W, const void* dY, collider_rows dy_rows,
+                                                  const int32_t* idx, const int32_t* n_kept, void* dX,
+                                                  collider_rows dx_rows, float* dW, float* db, void* ws,
+                                                  size_t ws_bytes, void* stream) {
+  static const char* fn = "collider_linear_bwd_ckpt";
+  if (M < 1 || M > (1 << 30) || K < 1 || N < 1) return fail(COLLIDER_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (!idx || !n_kept || !dY) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null idx/n_kept/dY", fn);
+  if (dX && !W) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dX needs W", fn);
+  if (!is_rows(x_rows) || !is_rows(dy_rows) || !is_rows(dx_rows))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
+  if (K % 8 || N % 8) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: needs K, N %% 8 == 0", fn);
+  if (!al16(W) || !al16(dY) || !al16(dX) || !al16(dW) || !al16(db))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  collider_status s = dW ? check_ckpt(fn, X, K) : COLLIDER_OK;
+  if (s != COLLIDER_OK) return s;
+  const size_t need = collider_linear_ckpt_workspace_size(M, K, N);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
+  Ctx c;
+  s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_memory(fn, {W, dY, idx, n_kept, dX, dW, db, ws});
+  if (s == COLLIDER_OK && dW) s = check_memory(fn, {X->code, X->exps}, true);
+  if (s != COLLIDER_OK) return s;
+  Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
+  LinearBufs L{};
+  linear_carve(cv, COLLIDER_BF16, M, K, N, true, true, true, &L.xk, &L.dyk, &L.dxk, &L.part);
+  L.sk_cap = sk_counter_cap(std::max<long long>(M, K), std::max(K, N));
+  L.sk_counters = reinterpret_cast<int*>(static_cast<char*>(ws) + need - up256(L.sk_cap * sizeof(int)));
+  L.sk_partial = reinterpret_cast<float*>(reinterpret_cast<char*>(L.sk_counters) - up256(kSkPartialFloats * 4));
+  CK(cudaMemsetAsync(L.sk_counters, 0, L.sk_cap * sizeof(int), c.stream));
+  return linear_bf16(c, M, K, N, nullptr, X, x_rows == COLLIDER_ROWS_FULL, W, dY, dy_rows == COLLIDER_ROWS_FULL, idx,
+                     n_kept, dX, dx_rows == COLLIDER_ROWS_FULL, dW, db, L);
 }
 
 // ===========================================================================
@@ -1361,5 +1514,186 @@ extern "C" collider_status collider_stack_bwd(const collider_layer_desc* d, int 
   // embedding gradient
   CK(cudaMemsetAsync(dE, 0, (size_t)V * D * sizeof(float), c.stream));
   CK(launch_embed_bwd(c, cur, D, D, ids, V, M, idx, n_kept, dE));
+  return COLLIDER_OK;
+}
+
+// ===========================================================================
+// residual join
+// ===========================================================================
+namespace {
+struct JoinLd {
+  long long x, y, h, a;
+};
+collider_status check_join_desc(const char* fn, const collider_residual_norm_desc* d, JoinLd* ld) {
+  if (!d) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null desc", fn);
+  if (d->dtype != COLLIDER_F32 && d->dtype != COLLIDER_BF16)
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: dtype %d", fn, d->dtype);
+  if (d->norm != COLLIDER_NORM_RMS && d->norm != COLLIDER_NORM_LAYER)
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: norm %d", fn, d->norm);
+  if (d->B < 1 || d->T < 1 || (long long)d->B * d->T > (1 << 30))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: need B, T >= 1 and B*T <= 2^30", fn);
+  if (d->D < 8 || d->D % 8 || d->D > 8192)
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: D must be a multiple of 8, 8 <= D <= 8192", fn);
+  if (!(d->eps > 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->res_scale))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: need a finite eps > 0 and a finite res_scale", fn);
+  if (d->gate_rows != 0 && d->gate_rows != 1 && d->gate_rows != d->B)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: gate_rows must be 0, 1 or B", fn);
+  if (d->x_ld < 0 || d->y_ld < 0 || d->h_ld < 0 || d->a_ld < 0)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: negative row stride", fn);
+  *ld = JoinLd{d->x_ld ? d->x_ld : d->D, d->y_ld ? d->y_ld : d->D, d->h_ld ? d->h_ld : d->D, d->a_ld ? d->a_ld : d->D};
+  const int per = d->dtype == COLLIDER_F32 ? 4 : 8;
+  for (long long l : {ld->x, ld->y, ld->h, ld->a})
+    if (l < d->D || l % per)
+      return fail(COLLIDER_ERR_INVALID_ARG, "%s: row strides must be >= D and multiples of 16 bytes", fn);
+  return COLLIDER_OK;
+}
+// the parameters a call with these norms reads
+collider_status check_join_params(const char* fn, const collider_residual_norm_desc* d,
+                                  const collider_residual_norm_params* w, bool branch) {
+  if (!w) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null params", fn);
+  const bool ln = d->norm == COLLIDER_NORM_LAYER;
+  if (!branch && (d->post || d->gate_rows || w->res_w || d->res_scale != 1.f))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: without y there is no post norm, gate or residual scale", fn);
+  if (!branch && !d->pre) return fail(COLLIDER_ERR_INVALID_ARG, "%s: without y there is nothing but the pre norm", fn);
+  if ((d->post && !w->post_w) || (d->pre && !w->pre_w) || (d->gate_rows && !w->gate))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: a parameter the desc asks for is null", fn);
+  if ((!d->post && (w->post_w || w->post_b)) || (!d->pre && (w->pre_w || w->pre_b)) || (!d->gate_rows && w->gate) ||
+      (!ln && (w->post_b || w->pre_b)))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: a parameter is given that the desc does not ask for", fn);
+  for (const void* p : {w->post_w, w->post_b, w->gate, w->res_w, w->pre_w, w->pre_b})
+    if (!al16(p)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  return COLLIDER_OK;
+}
+collider_status check_join_memory(const char* fn, const collider_residual_norm_params* w) {
+  return check_memory(fn, {w->post_w, w->post_b, w->gate, w->res_w, w->pre_w, w->pre_b});
+}
+}  // namespace
+
+extern "C" collider_status collider_residual_norm_fwd(const collider_residual_norm_desc* d,
+                                                      const collider_residual_norm_params* w, const void* x,
+                                                      const void* y, const collider_residual_norm_out* o,
+                                                      void* stream) {
+  static const char* fn = "collider_residual_norm_fwd";
+  JoinLd ld;
+  collider_status s = check_join_desc(fn, d, &ld);
+  if (s != COLLIDER_OK) return s;
+  if (!x || !o) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null x or out", fn);
+  s = check_join_params(fn, d, w, y != nullptr);
+  if (s != COLLIDER_OK) return s;
+  const bool ln = d->norm == COLLIDER_NORM_LAYER;
+  if (!y != !o->h) return fail(COLLIDER_ERR_INVALID_ARG, "%s: h is written when y is given, and only then", fn);
+  if (d->pre ? (!o->a || !o->rstd_h || (ln && !o->mean_h)) : o->a != nullptr)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: the pre norm writes a, rstd_h (and mean_h for LayerNorm)", fn);
+  if (d->post && (!o->rstd_y || (ln && !o->mean_y)))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: the post norm writes rstd_y (and mean_y for LayerNorm)", fn);
+  if (o->a && (o->a == x || o->a == y || o->a == o->h))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: a must not alias x, y or h", fn);
+  if ((o->h && o->h == x && ld.h != ld.x) || (o->h && o->h == y && ld.h != ld.y))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: h in the place of x or y needs its row stride", fn);
+  for (const void* p : {x, y, static_cast<const void*>(o->h), static_cast<const void*>(o->a)})
+    if (!al16(p)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  Ctx c;
+  s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_join_memory(fn, w);
+  if (s == COLLIDER_OK) s = check_memory(fn, {x, y, o->h, o->a, o->mean_y, o->rstd_y, o->mean_h, o->rstd_h});
+  if (s != COLLIDER_OK) return s;
+  JoinFwd j{};
+  j.f32 = d->dtype == COLLIDER_F32; j.layer_norm = ln; j.B = d->B; j.T = d->T; j.D = d->D;
+  j.eps = d->eps; j.alpha = d->res_scale; j.gate_rows = d->gate_rows; j.post = d->post != 0; j.pre = d->pre != 0;
+  j.x = x; j.y = y; j.h = o->h; j.a = o->a;
+  j.x_ld = ld.x; j.y_ld = ld.y; j.h_ld = ld.h; j.a_ld = ld.a;
+  j.post_w = w->post_w; j.post_b = w->post_b; j.gate = w->gate; j.res_w = w->res_w; j.pre_w = w->pre_w;
+  j.pre_b = w->pre_b;
+  j.mean_y = o->mean_y; j.rstd_y = o->rstd_y; j.mean_h = o->mean_h; j.rstd_h = o->rstd_h;
+  CK(launch_join_fwd(c, j));
+  return COLLIDER_OK;
+}
+
+extern "C" size_t collider_residual_norm_bwd_workspace_size(const collider_residual_norm_desc* d) {
+  JoinLd ld;
+  if (check_join_desc("collider_residual_norm_bwd_workspace_size", d, &ld) != COLLIDER_OK) return 0;
+  return up256(join_bwd_part_floats(d->B, d->T, d->D, d->gate_rows) * sizeof(float));
+}
+
+extern "C" collider_status collider_residual_norm_bwd(const collider_residual_norm_desc* d,
+                                                      const collider_residual_norm_params* w,
+                                                      const collider_residual_norm_saved* sv, collider_rows saved_rows,
+                                                      const void* da, const void* dh, collider_rows in_rows,
+                                                      const int32_t* idx, const int32_t* cu_kept, const int32_t* n_kept,
+                                                      const collider_residual_norm_grads* g, collider_rows out_rows,
+                                                      void* ws, size_t ws_bytes, void* stream) {
+  static const char* fn = "collider_residual_norm_bwd";
+  JoinLd ld;
+  collider_status s = check_join_desc(fn, d, &ld);
+  if (s != COLLIDER_OK) return s;
+  if (!sv || !g) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null saved or grads", fn);
+  const bool ln = d->norm == COLLIDER_NORM_LAYER, post = d->post != 0, pre = d->pre != 0;
+  const bool branch = sv->y || sv->y_ckpt;
+  if ((sv->y && sv->y_ckpt) || (sv->h && sv->h_ckpt))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: y and h are given as rows or as a checkpoint, not both", fn);
+  s = check_join_params(fn, d, w, branch);
+  if (s != COLLIDER_OK) return s;
+  if (!is_rows(saved_rows) || !is_rows(in_rows) || !is_rows(out_rows))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
+  if (!idx != !n_kept || !idx != !cu_kept)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: only some of idx, cu_kept and n_kept given", fn);
+  if (pre ? !da || !(sv->h || sv->h_ckpt) || !sv->rstd_h || (ln && !sv->mean_h) : da != nullptr)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: the pre norm needs da, h and rstd_h (and mean_h for LayerNorm)", fn);
+  if (!pre && !dh) return fail(COLLIDER_ERR_INVALID_ARG, "%s: without a pre norm dh is needed", fn);
+  if (post && (!sv->rstd_y || (ln && !sv->mean_y)))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: the post norm needs rstd_y (and mean_y for LayerNorm)", fn);
+  if (w->res_w && g->dres_w && !sv->x) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dres_w needs x", fn);
+  if (!g->dx || (branch && !g->dy) || (!branch && g->dy))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: dx is written always, dy with y", fn);
+  const int src = pre && sv->h_ckpt ? sv->h_ckpt->format : branch && sv->y_ckpt ? sv->y_ckpt->format : 2;
+  if (branch && pre && (sv->y_ckpt ? sv->y_ckpt->format : 2) != src)
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: y and h must be saved in the same form", fn);
+  if (branch && sv->y_ckpt) s = check_ckpt(fn, sv->y_ckpt, d->D);
+  if (s == COLLIDER_OK && pre && sv->h_ckpt) s = check_ckpt(fn, sv->h_ckpt, d->D);
+  if (s != COLLIDER_OK) return s;
+  for (const void* p : {da, dh, sv->x, sv->y, sv->h, static_cast<const void*>(g->dx), static_cast<const void*>(g->dy)})
+    if (!al16(p)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  if (g->dx == da || (g->dy && (g->dy == da || g->dy == dh || g->dy == g->dx)) ||
+      (g->dx == dh && (in_rows != out_rows || ld.x != ld.h)))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: of the outputs only dx may alias an input: dh, of the same rows and stride",
+                fn);
+  const size_t need = collider_residual_norm_bwd_workspace_size(d);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
+  Ctx c;
+  s = make_ctx(stream, &c);
+  const bool want_res = w->res_w && g->dres_w;
+  JoinBwd j{};
+  j.f32 = d->dtype == COLLIDER_F32; j.layer_norm = ln; j.B = d->B; j.T = d->T; j.D = d->D;
+  j.alpha = d->res_scale; j.gate_rows = d->gate_rows; j.post = post; j.pre = pre;
+  j.da = da; j.dh = dh; j.x = want_res ? sv->x : nullptr;
+  j.src = src;
+  if (branch) j.y = sv->y_ckpt ? sv->y_ckpt->code : sv->y;
+  if (pre) j.h = sv->h_ckpt ? sv->h_ckpt->code : sv->h;
+  if (branch && sv->y_ckpt) {
+    j.y_exps = static_cast<const uint8_t*>(sv->y_ckpt->exps);
+    j.y_code_ld = (long long)sv->y_ckpt->code_ld; j.y_exp_ld = (long long)sv->y_ckpt->exp_ld;
+  }
+  if (pre && sv->h_ckpt) {
+    j.h_exps = static_cast<const uint8_t*>(sv->h_ckpt->exps);
+    j.h_code_ld = (long long)sv->h_ckpt->code_ld; j.h_exp_ld = (long long)sv->h_ckpt->exp_ld;
+  }
+  j.x_ld = ld.x; j.y_ld = ld.y; j.h_ld = ld.h; j.a_ld = ld.a;
+  j.post_w = w->post_w; j.post_b = w->post_b; j.gate = w->gate; j.res_w = w->res_w; j.pre_w = w->pre_w;
+  j.mean_y = sv->mean_y; j.rstd_y = sv->rstd_y; j.mean_h = sv->mean_h; j.rstd_h = sv->rstd_h;
+  j.saved_full = saved_rows == COLLIDER_ROWS_FULL; j.in_full = in_rows == COLLIDER_ROWS_FULL;
+  j.out_full = out_rows == COLLIDER_ROWS_FULL;
+  j.idx = idx; j.cu = cu_kept; j.nk = n_kept;
+  j.dx = g->dx; j.dy = g->dy;
+  j.dpre_w = pre ? g->dpre_w : nullptr; j.dpre_b = pre && ln ? g->dpre_b : nullptr;
+  j.dpost_w = post ? g->dpost_w : nullptr; j.dpost_b = post && ln ? g->dpost_b : nullptr;
+  j.dgate = d->gate_rows ? g->dgate : nullptr; j.dres_w = want_res ? g->dres_w : nullptr;
+  j.part = static_cast<float*>(ws);
+  if (s == COLLIDER_OK) s = check_join_memory(fn, w);
+  if (s == COLLIDER_OK)
+    s = check_memory(fn, {da, dh, j.x, j.y, j.h, j.y_exps, j.h_exps, j.mean_y, j.rstd_y, j.mean_h, j.rstd_h, idx, cu_kept,
+                          n_kept, j.dx, j.dy, j.dpre_w, j.dpre_b, j.dpost_w, j.dpost_b, j.dgate, j.dres_w, ws});
+  if (s != COLLIDER_OK) return s;
+  CK(launch_join_bwd(c, j));
   return COLLIDER_OK;
 }

@@ -41,6 +41,7 @@ struct TcParams {
   float* partial;    // stream-K: [2 * gridDim.x][BM][BN] f32 partial tiles (null: whole tiles only)
   int* counters;     // stream-K: per-(tile, pair rank) arrival counts, zero on entry and left zero
   int split_mode;    // 0 whole tiles, 1 stream-K, 2 hybrid, 3 auto (see Split)
+  int k_piece;       // whole tiles: k-slices accumulated at a time (0: all)
   DevStatus* st;
 };
 
@@ -92,6 +93,7 @@ struct Split {
   int W, wid;          // workers (CTAs or CTA pairs) and this CTA's worker
   int unit0, ustride;  // whole-tile phase: first tile and stride (per worker)
   int dp_tiles;        // tiles handled whole, round-robin, first
+  int piece;           // k-slices of a whole tile accumulated at a time (num_kb: all at once)
   long long total;     // stream-K iterations (over tiles dp_tiles..num_tiles-1)
   bool sk;
   int G;               // workers sharing the stream-K part: min(W, total), no empty range
@@ -131,10 +133,11 @@ struct Split {
 // Iterates this CTA's segments: (tile, first k-slice, end k-slice).
 struct SegIter {
   const Split& sp;
-  int tile;            // whole-tile phase
+  int tile, kpos;      // whole-tile phase
   long long it, end;   // stream-K phase (relative iterations)
   __device__ SegIter(const Split& s) : sp(s) {
     tile = sp.unit0;
+    kpos = 0;
     if (sp.sk && sp.wid < sp.G) {
       it = sp.begin(sp.wid);
       end = (long long)(sp.wid + 1) * sp.total / sp.G;
@@ -145,9 +148,13 @@ struct SegIter {
   __device__ bool next(int& t, int& k0, int& k1) {
     if (tile < sp.dp_tiles) {
       t = tile;
-      k0 = 0;
-      k1 = sp.num_kb;
-      tile += sp.ustride;
+      k0 = kpos;
+      k1 = sp.num_kb - kpos < sp.piece ? sp.num_kb : kpos + sp.piece;
+      kpos = k1;
+      if (k1 == sp.num_kb) {
+        kpos = 0;
+        tile += sp.ustride;
+      }
       return true;
     }
     if (it >= end) return false;
@@ -162,7 +169,7 @@ struct SegIter {
 
 // Store 32 consecutive columns of one output row (bf16 or f32, optional
 // accumulate into C, zero rows past the kept count up to the padding).
-__device__ __forceinline__ void store32(const TcParams& p, int row, int col, bool row_ok, float* v) {
+__device__ __forceinline__ void store32(const TcParams& p, int row, int col, bool row_ok, float* v, bool add) {
   if (p.c_bf16) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + (long long)row * p.ldc + col;
 #pragma unroll
@@ -174,7 +181,7 @@ __device__ __forceinline__ void store32(const TcParams& p, int row, int col, boo
     for (int g = 0; g < 8; ++g) {
       if (col + 4 * g + 4 <= p.N) {
         float4 o = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-        if (p.accumulate && row_ok) {
+        if (add && row_ok) {
           float4 old = *reinterpret_cast<const float4*>(out + 4 * g);
           o.x += old.x; o.y += old.y; o.z += old.z; o.w += old.w;
         }
@@ -259,6 +266,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   sp.unit0 = sp.wid;
   sp.ustride = sp.W;
   sp.init(p.split_mode, p.partial != nullptr);
+  // (pieces of equal length, so that none is a short tail)
+  const int pieces = p.k_piece > 0 && sp.num_kb > p.k_piece ? (sp.num_kb + p.k_piece - 1) / p.k_piece : 1;
+  sp.piece = (sp.num_kb + pieces - 1) / pieces;
   // partial tile of worker w for tile t: this CTA's 128 rows, stored as
   // [BN / 4][BM][4] f32 so that a warp's 32 rows touch 512 contiguous bytes
   constexpr int R = PAIR ? 2 : 1;
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          store32(p, row, n0 + c, row_ok, v);
+          store32(p, row, n0 + c, row_ok, v, p.accumulate);
         }
       }
     }
@@ -454,8 +464,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool row_ok = row < M;
       const bool row_zero = !row_ok && p.zero_pad && row < padded_rows(M, p.c_rows);
       const uint32_t tcol = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
-      if (k0 == 0 && k1 == sp.num_kb) {
-        // whole tile: straight to the output
+      if ((k0 == 0 && k1 == sp.num_kb) || t < sp.dp_tiles) {
+        // whole tile (or a piece of its reduction, added to the pieces before
+        // it by the thread that stored them): straight to the output
         for (int c = 0; c < BN; c += 32) {
           float v[32];
           tmem_ld32(tcol + c, v);
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
           }
-          store32(p, row, n0 + c, row_ok, v);
+          store32(p, row, n0 + c, row_ok, v, p.accumulate || k0 > 0);
         }
         fence_before();
         release_acc(acc);
@@ -511,7 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0.f;
             }
-            store32(p, row, n0 + c, row_ok, v);
+            store32(p, row, n0 + c, row_ok, v, p.accumulate);
           }
         }
         named_bar(1, 128);   // last_flag is reused by the next segment
@@ -664,7 +675,7 @@ cudaError_t launch_tc_gemm(const Ctx& c, const TcGemm& g) {
   const long long m_tiles = (g.M + BM - 1) / BM, n_tiles = (g.N + bn - 1) / bn;
   const long long max_ctrs = (pair ? 2 * ((m_tiles + 1) / 2) : m_tiles) * n_tiles;
   const int split = split_env >= 0 ? split_env : 3;
-  const bool sk = split != 0 && g.partial && g.counters && max_ctrs <= g.counter_cap;
+  const bool sk = split != 0 && g.k_piece == 0 && g.partial && g.counters && max_ctrs <= g.counter_cap;
   CUtensorMap ma, mb;
   // A: K-major [M rows, K] or MN-major [K rows, M]; B: K-major [N rows, K]
   // (half the tile's rows per box for a pair) or MN-major [K rows, N]
@@ -675,7 +686,7 @@ cudaError_t launch_tc_gemm(const Ctx& c, const TcGemm& g) {
   if (!ok) return cudaErrorInvalidValue;
   TcParams p{g.M, g.N, g.K, g.dyn, g.n_kept, g.C, g.ldc, g.c_bf16, g.accumulate, g.zero_pad,
              g.c_rows > 0 ? g.c_rows : g.M, sk ? g.partial : nullptr, sk ? g.counters : nullptr,
-             split, c.st};
+             split, g.k_piece, c.st};
   prof_begin(c, "tc_gemm", g.M, g.N, g.K, g.dyn);
   cudaError_t e;
   const int key = (bn == 256 ? 100 : 0) + (g.a_mn_major ? 10 : (g.b_mn_major ? 20 : 0)) + mode;

@@ -201,6 +201,9 @@ struct TcGemm {
   long long c_rows;   // row capacity of C (zero padding stops there)
   const int32_t* n_kept; int dyn;
   int bn;             // 128 or 256 (0 = choose)
+  // f32 C, whole tiles: at most this many 64-deep k-slices are accumulated in
+  // TMEM at a time; the pieces of a longer reduction are added in C (0: no limit)
+  int k_piece;
   // stream-K scratch (both null: whole tiles only).  partial holds
   // kSkMaxCtas * 2 tiles of 128 x 256 f32; counters hold counter_cap ints,
   // zero before the launch (the kernel leaves them zero).
@@ -301,5 +304,60 @@ cudaError_t launch_residual_out(const Ctx& c, int M, int D, const __nv_bfloat16*
 cudaError_t launch_iota_cu(const Ctx& c, int B, int T, int32_t* cu);
 // the index of "every token kept": idx[i] = i (i < B*T), cu[b] = b*T, *nk = B*T
 cudaError_t launch_identity_index(const Ctx& c, int B, int T, int32_t* idx, int32_t* cu, int32_t* nk);
+
+// ---- 8-bit activation checkpoints (q8.cu; format: q8.cuh) --------------------
+// codes [rows, code_ld] and exponent bytes [rows, exp_ld], a row's N codes and
+// N / 32 exponents (N % 32 == 0; code_ld % 16 == 0, codes 16-byte aligned)
+struct Q8View {
+  uint8_t* code;
+  uint8_t* exps;
+  long long code_ld, exp_ld;   // bytes
+};
+// row r of q = src[idx[r]] for r < n_kept (idx and n_kept null: every row)
+cudaError_t launch_q8_pack(const Ctx& c, int f32, const void* src, long long src_ld, int M, int N, const int32_t* idx,
+                           const int32_t* n_kept, int format, const Q8View& q);
+// dst row (dst_full ? idx[r] : r) = row (src_full ? idx[r] : r) of q; the other
+// rows of a FULL dst (M) are 0, those of a COMPACT one up to the next multiple of
+// 128 (below cap).
+cudaError_t launch_q8_unpack(const Ctx& c, int f32, int format, const Q8View& q, int src_full, int M, int N,
+                             const int32_t* idx, const int32_t* n_kept, void* dst, long long dst_ld, int dst_full,
+                             long long cap);
+
+// ---- residual join (join_fwd.cu, join_bwd.cu) --------------------------------
+// h = alpha res_w x + gate post(y), a = pre(h); rows of D values (D % 8 == 0,
+// D <= 8192) of bf16, or f32; null parameters are 1 (weights) and 0 (biases).
+struct JoinFwd {
+  int f32, layer_norm, B, T, D;
+  float eps, alpha;
+  int gate_rows;    // 0 no gate, 1 one row for all tokens, B one a sequence
+  int post, pre;    // which norms there are
+  const void *x, *y;   // y null: no branch, h is x
+  void *h, *a;
+  long long x_ld, y_ld, h_ld, a_ld;   // elements
+  const void *post_w, *post_b, *gate, *res_w, *pre_w, *pre_b;
+  float *mean_y, *rstd_y, *mean_h, *rstd_h;
+};
+cudaError_t launch_join_fwd(const Ctx& c, const JoinFwd& j);
+struct JoinBwd {
+  int f32, layer_norm, B, T, D;
+  float alpha;
+  int gate_rows, post, pre;
+  const void *da, *dh;   // gradients of a (with pre) and of h (may be null)
+  const void* x;         // only with res_w
+  int src;               // y and h: kQ8E4m3 or kQ8Int8 codes, or 2: as stored
+  const void *y, *h;
+  const uint8_t *y_exps, *h_exps;
+  long long x_ld, y_ld, h_ld, a_ld;   // elements; the gradients have the strides of their tensors
+  long long y_code_ld, h_code_ld, y_exp_ld, h_exp_ld;
+  const void *post_w, *post_b, *gate, *res_w, *pre_w;
+  const float *mean_y, *rstd_y, *mean_h, *rstd_h;   // FULL [M]
+  int saved_full, in_full, out_full;   // rows of x, y, h; of da, dh; of dx, dy
+  const int32_t *idx, *cu, *nk;        // all null: every token is kept
+  void *dx, *dy;
+  float *dpre_w, *dpre_b, *dpost_w, *dpost_b, *dgate, *dres_w;   // null: not wanted
+  float* part;   // join_bwd_part_floats
+};
+size_t join_bwd_part_floats(int B, int T, int D, int gate_rows);
+cudaError_t launch_join_bwd(const Ctx& c, const JoinBwd& j);
 
 }  // namespace collider

@@ -1,0 +1,259 @@
+"""8-bit activation checkpoints on the GPU: pack and unpack bit for bit against the float64 oracle, and the
+linear backward from a checkpoint."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ckpt as ock
+import workloads
+
+pytestmark = pytest.mark.gpu
+
+gu = pytest.importorskip("gpu_util")
+cl = gu.cl
+FMT = {"e4m3": cl.CKPT_E4M3, "int8": cl.CKPT_INT8}
+DT = {"bf16": (cl.BF16, torch.bfloat16), "f32": (cl.F32, torch.float32)}
+
+
+def values(rows, N, dtype, seed):
+    """Rows over the whole range of exponents, with zero groups, ties, limits, infinities and NaNs among them."""
+    rng = np.random.default_rng(seed)
+    v = rng.normal(size=(rows, N)) * np.exp(rng.uniform(-20, 20, size=(rows, 1)))
+    v[rng.random((rows, N)) < 0.02] = 0.0
+    v *= np.where(rng.random(N) < 0.05, 30.0, 1.0)
+    if rows > 7:
+        v[1] = -0.0
+        v[2, :32] = np.linspace(-448, 448, 32)
+        v[3, :32] = np.arange(32) * 4 - 63.5
+        v[4, 1], v[5, N - 1], v[6, N // 2] = np.nan, np.inf, -np.inf
+        v[7, :] = np.where(np.arange(N) % 32 == 0, 3.0e38, 1e-38)
+    v = v.astype(np.float32)
+    return workloads.bf16_representable(v) if dtype == "bf16" else v
+
+
+def index(M, f, seed):
+    rng = np.random.default_rng(seed)
+    keep = rng.random(M) >= f
+    rows = np.flatnonzero(keep)
+    idx = np.full(M, -1)
+    idx[: rows.size] = rows
+    return rows, gu.i32(idx), gu.i32([rows.size])
+
+
+def dev(v, dtype):
+    return torch.from_numpy(np.ascontiguousarray(v)).to(gu.DEV).to(DT[dtype][1])
+
+
+def strided(rows, cols, dtype, pad, fill=0):
+    """A [rows, cols] view with `pad` more elements a row, filled with a mark."""
+    t = torch.full((rows, cols + pad), fill, dtype=dtype, device=gu.DEV)
+    return t, t[:, :cols]
+
+
+def same(a, b):
+    return np.array_equal(a, b, equal_nan=True)
+
+
+SIZES = [(1, 32), (1, 1056), (8, 96), (130, 64), (257, 2048), (37, 11264), (300, 1536)]
+
+
+@pytest.mark.parametrize("M,N", SIZES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_pack_and_unpack(M, N, dtype, fmt):
+    v = values(M, N, dtype, M + N)
+    cdt, tdt = DT[dtype]
+    src, sv = strided(M, N, tdt, 8)
+    sv.copy_(dev(v, dtype))
+    ct, code = strided(M + 1, N, torch.uint8, 16, 0xAB)
+    et, exps = strided(M + 1, N // 32, torch.uint8, 3, 0xCD)
+    q = cl.ckpt(FMT[fmt], code, exps)
+    want_c, want_e = ock.pack(v, fmt)
+    # every row, then the kept rows; rows and columns beyond are left as they were
+    for f in (None, 0.45):
+        ct.fill_(0xAB)
+        et.fill_(0xCD)
+        rows, idx, nk = (np.arange(M), None, None) if f is None else index(M, f, M)
+        cl.collider_ckpt_pack(cdt, src, src.stride(0), M, N, idx, nk, q)
+        cl.collider_check()
+        n = rows.size
+        assert np.array_equal(code[:n].cpu().numpy(), want_c[rows])
+        assert np.array_equal(exps[:n].cpu().numpy(), want_e[rows])
+        assert bool((ct[n:] == 0xAB).all()) and bool((ct[:, N:] == 0xAB).all())
+        assert bool((et[n:] == 0xCD).all()) and bool((et[:, N // 32:] == 0xCD).all())
+        # back: COMPACT and FULL
+        val = ock.unpack(want_c, want_e, fmt)[rows]
+        for drows in (cl.ROWS_COMPACT, cl.ROWS_FULL):
+            dt, dst = strided(M, N, tdt, 16, 7.0)
+            cl.collider_ckpt_unpack(cdt, q, cl.ROWS_COMPACT, M, N, idx, nk, dst, dt.stride(0), drows)
+            cl.collider_check()
+            got = gu.host(dst)
+            if drows == cl.ROWS_FULL:
+                full = np.zeros((M, N))
+                full[rows] = val
+                assert same(got, full)
+            else:
+                pad = min(-(-n // 128) * 128, M)
+                assert same(got[:n], val) and np.all(got[n:pad] == 0) and np.all(got[pad:] == 7)
+            assert bool((dt[:, N:] == 7).all())
+    # a checkpoint of FULL rows, its kept rows
+    cl.collider_ckpt_pack(cdt, src, src.stride(0), M, N, None, None, q)
+    rows, idx, nk = index(M, 0.5, M + 1)
+    dst = torch.full((M, N), 7.0, dtype=tdt, device=gu.DEV)
+    cl.collider_ckpt_unpack(cdt, q, cl.ROWS_FULL, M, N, idx, nk, dst, N, cl.ROWS_COMPACT)
+    assert same(gu.host(dst)[: rows.size], ock.unpack(want_c, want_e, fmt)[rows])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_every_code_and_exponent_decodes(fmt):
+    """All 256 codes under all 256 exponent bytes (other programs' checkpoints may hold any), exactly in f32."""
+    code = np.repeat(np.arange(256, dtype=np.uint8)[None, :], 256, axis=0)
+    exps = np.repeat(np.arange(256, dtype=np.uint8)[:, None], 8, axis=1)
+    q = cl.ckpt(FMT[fmt], torch.from_numpy(code).to(gu.DEV), torch.from_numpy(exps).to(gu.DEV))
+    dst = torch.empty(256, 256, dtype=torch.float32, device=gu.DEV)
+    cl.collider_ckpt_unpack(cl.F32, q, cl.ROWS_FULL, 256, 256, None, None, dst, 256, cl.ROWS_FULL)
+    with np.errstate(over="ignore"):
+        want = ock.unpack(code, exps, fmt).astype(np.float32)
+    assert same(dst.cpu().numpy(), want)
+
+
+def test_nothing_kept_everything_kept_and_a_bad_index():
+    M, N = 300, 96
+    v = values(M, N, "bf16", 3)
+    src = dev(v, "bf16")
+    code = torch.full((M, N), 0xAB, dtype=torch.uint8, device=gu.DEV)
+    exps = torch.full((M, 3), 0xCD, dtype=torch.uint8, device=gu.DEV)
+    q = cl.ckpt(cl.CKPT_E4M3, code, exps)
+    none, zero = gu.i32(np.full(M, -1)), gu.i32([0])
+    cl.collider_ckpt_pack(cl.BF16, src, N, M, N, none, zero, q)
+    assert bool((code == 0xAB).all()) and bool((exps == 0xCD).all())
+    dst = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=gu.DEV)
+    cl.collider_ckpt_unpack(cl.BF16, q, cl.ROWS_COMPACT, M, N, none, zero, dst, N, cl.ROWS_COMPACT)
+    assert bool((dst == 7).all())
+    cl.collider_ckpt_unpack(cl.BF16, q, cl.ROWS_COMPACT, M, N, none, zero, dst, N, cl.ROWS_FULL)
+    assert bool((dst == 0).all())
+    idx, nk = gu.i32(np.arange(M)), gu.i32([M])
+    cl.collider_ckpt_pack(cl.BF16, src, N, M, N, idx, nk, q)
+    assert np.array_equal(code.cpu().numpy(), ock.pack(v, "e4m3")[0])
+    # an index outside the rows is skipped and reported; the others are there
+    cl.collider_check()
+    code.fill_(0xAB)
+    bad = np.arange(M)
+    bad[17] = M
+    cl.collider_ckpt_pack(cl.BF16, src, N, M, N, gu.i32(bad), nk, q)
+    with pytest.raises(cl.ColliderError) as e:
+        cl.collider_check()
+    assert e.value.status == cl.ERR_INVALID_ARG
+    assert bool((code[17] == 0xAB).all()) and bool((code[16] != 0xAB).any())
+
+
+def test_checkpoint_in_pinned_host_memory():
+    M, N = 513, 1024
+    v = values(M, N, "bf16", 9)
+    src = dev(v, "bf16")
+    code = torch.zeros(M, N, dtype=torch.uint8).pin_memory()
+    exps = torch.zeros(M, N // 32, dtype=torch.uint8).pin_memory()
+    q = cl.ckpt(cl.CKPT_INT8, code, exps)
+    rows, idx, nk = index(M, 0.3, 2)
+    cl.collider_ckpt_pack(cl.BF16, src, N, M, N, idx, nk, q)
+    cl.collider_check()
+    c, e = ock.pack(v, "int8")
+    assert np.array_equal(code.numpy()[: rows.size], c[rows]) and np.array_equal(exps.numpy()[: rows.size], e[rows])
+    dst = torch.empty(M, N, dtype=torch.bfloat16, device=gu.DEV)
+    cl.collider_ckpt_unpack(cl.BF16, q, cl.ROWS_COMPACT, M, N, idx, nk, dst, N, cl.ROWS_COMPACT)
+    assert same(gu.host(dst)[: rows.size], ock.unpack(c[rows], e[rows], "int8"))
+
+
+def test_wrong_memory_is_refused():
+    M, N = 4, 64
+    d = torch.zeros(M, N, dtype=torch.bfloat16, device=gu.DEV)
+    h = torch.zeros(M, N, dtype=torch.bfloat16)
+    code = torch.zeros(M, N, dtype=torch.uint8, device=gu.DEV)
+    exps = torch.zeros(M, 2, dtype=torch.uint8, device=gu.DEV)
+    q = cl.ckpt(cl.CKPT_E4M3, code, exps)
+    for call in (lambda: cl.collider_ckpt_pack(cl.BF16, h, N, M, N, None, None, q),
+                 lambda: cl.collider_ckpt_unpack(cl.BF16, q, 0, M, N, None, None, h, N, 0),
+                 lambda: cl.collider_ckpt_pack(cl.BF16, d, N, M, N, None, None, cl.ckpt(0, code.cpu(), exps))):
+        with pytest.raises(cl.ColliderError) as e:
+            call()
+        assert e.value.status == cl.ERR_INVALID_ARG and "memory" in str(e.value)
+
+
+# --------------------------------------------------------------------------
+# linear backward from a checkpoint
+# --------------------------------------------------------------------------
+def _mma_tol(ref_abs, steps):
+    """f32 accumulation on the tensor core: a step adds 16 products, and may drop up to one unit in the last place
+    (2^-23 of the magnitude, at most the sum of all magnitudes) when it aligns the products and one when it adds."""
+    return 2 * steps * 2.0 ** -23 * ref_abs
+
+
+@pytest.mark.parametrize("M,K,N,f", [(1, 32, 8, 0.0), (77, 96, 40, 0.3), (128, 256, 256, 0.4), (700, 512, 1000, 0.6),
+                                     (4500, 64, 72, 0.05), (300, 2048, 256, 1.0), (640, 1056, 520, 0.0)])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("x_rows,dy_rows,dx_rows", [(0, 0, 0), (1, 0, 1), (0, 1, 0)])
+def test_linear_backward(M, K, N, f, fmt, x_rows, dy_rows, dx_rows):
+    rng = np.random.default_rng(M + K + N)
+    rows, idx, nk = index(M, f, M + 5)
+    n = rows.size
+    X = workloads.bf16_representable(rng.normal(size=(M, K)) + 0.5)
+    code, exps = ock.pack(X, fmt)
+    Xd = ock.unpack(code, exps, fmt)[rows]
+    W = workloads.bf16_representable(rng.normal(size=(K, N)) * 0.02).astype(np.float64)
+    dY = workloads.bf16_representable(rng.normal(size=(M, N))).astype(np.float64)
+    lay = lambda a, r: a if r == 0 else np.concatenate([a[rows], np.full((M - n,) + a.shape[1:], 99)])  # noqa: E731
+    c, e = (torch.from_numpy(np.ascontiguousarray(lay(t, x_rows)).astype(np.uint8)).to(gu.DEV) for t in (code, exps))
+    q = cl.ckpt(FMT[fmt], c, e)
+    dX = torch.full((M, K), 7.0, dtype=torch.bfloat16, device=gu.DEV)
+    dW = torch.full((K, N), 7.0, device=gu.DEV)
+    db = torch.full((N,), 7.0, device=gu.DEV)
+    ws = torch.empty(cl.collider_linear_ckpt_workspace_size(M, K, N), dtype=torch.uint8, device=gu.DEV).fill_(255)
+    cl.collider_linear_bwd_ckpt(M, K, N, q, x_rows, gu.bf16(W), gu.bf16(lay(dY, dy_rows)), dy_rows, idx, nk, dX, dx_rows,
+                                dW, db, ws)
+    cl.collider_check()
+    dYk = dY[rows]
+    rX, aX = dYk @ W.T, np.abs(dYk) @ np.abs(W).T
+    got = gu.host(dX)
+    if dx_rows == 0:
+        assert np.all(np.delete(got, rows, axis=0) == 0)
+        got = got[rows]
+    else:
+        pad = min(-(-n // 128) * 128, M)
+        assert np.all(got[n:pad] == 0) and np.all(got[pad:] == 7)
+        got = got[:n]
+    tol = _mma_tol(aX, N / 16 + 1)
+    assert np.all(np.abs(got - rX) <= tol + 2.0 ** -8 * (np.abs(rX) + tol))
+    rW, aW = Xd.T @ dYk, np.abs(Xd).T @ np.abs(dYk)
+    assert np.all(np.abs(gu.host(dW) - rW) <= _mma_tol(aW, min(n, 2048) / 16 + 1 + n / 2048))
+    # db: f32 sums of at most n terms
+    assert np.all(np.abs(gu.host(db) - dYk.sum(0)) <= (n + 1) * 2.0 ** -24 * np.abs(dYk).sum(0))
+
+
+def test_linear_parts_alone_and_repeat():
+    M, K, N = 500, 256, 128
+    rng = np.random.default_rng(4)
+    rows, idx, nk = index(M, 0.4, 8)
+    code, exps = (torch.from_numpy(t).to(gu.DEV) for t in ock.pack(rng.normal(size=(M, K)), "e4m3"))
+    q = cl.ckpt(cl.CKPT_E4M3, code, exps)
+    W, dY = gu.bf16(rng.normal(size=(K, N))), gu.bf16(rng.normal(size=(M, N)))
+    ws = torch.empty(cl.collider_linear_ckpt_workspace_size(M, K, N), dtype=torch.uint8, device=gu.DEV)
+
+    def run(x=q, want_dx=True, want_dw=True, want_db=True):
+        dX = torch.empty(M, K, dtype=torch.bfloat16, device=gu.DEV) if want_dx else None
+        dW = torch.empty(K, N, device=gu.DEV) if want_dw else None
+        db = torch.empty(N, device=gu.DEV) if want_db else None
+        cl.collider_linear_bwd_ckpt(M, K, N, x, 0, W if want_dx else None, dY, 0, idx, nk, dX, 0, dW, db, ws)
+        return dX, dW, db
+    a, b = run(), run()
+    for s, t in zip(a, b):
+        assert torch.equal(s, t)
+    assert torch.equal(run(x=None, want_dw=False)[0], a[0])
+    assert torch.equal(run(want_dx=False)[1], a[1])
+    assert torch.equal(run(want_dx=False, want_dw=False)[2], a[2])
+    # the decoded rows through collider_linear_bwd: the same operands, so dX and db are the same bits
+    X = torch.empty(M, K, dtype=torch.bfloat16, device=gu.DEV)
+    cl.collider_ckpt_unpack(cl.BF16, q, 0, M, K, None, None, X, K, 0)
+    dX, dW, db = torch.empty_like(a[0]), torch.empty_like(a[1]), torch.empty_like(a[2])
+    cl.collider_linear_bwd(cl.BF16, M, K, N, X, 0, W, dY, 0, idx, nk, dX, 0, dW, db, ws)
+    assert torch.equal(dX, a[0]) and torch.equal(db, a[2])
+    assert gu.rel_err(gu.host(dW), gu.host(a[1])) <= 1e-5
