@@ -440,63 +440,6 @@ size_t linear_carve(Carver& cv, collider_dtype dt, int M, int K, int N, bool x_f
   }
   return cv.used;
 }
-
-// The bf16 linear backward: compact operands (zero-padded to 128 rows),
-// tcgen05 GEMMs.  X is bf16 rows, or (ck) an 8-bit checkpoint decoded into the
-// compact copy.  xk, dyk, dxk, part: the workspace's buffers.
-struct LinearBufs {
-  void *xk, *dyk, *dxk;
-  float* part;
-  float* sk_partial;
-  int* sk_counters;
-  long long sk_cap;
-};
-collider_status linear_bf16(const Ctx& c, int M, int K, int N, const void* X, const collider_ckpt* ck, bool x_full,
-                            const void* W, const void* dY, bool dy_full, const int32_t* idx, const int32_t* n_kept,
-                            void* dX, bool dx_full, float* dW, float* db, const LinearBufs& L) {
-  const __nv_bfloat16* Xk = static_cast<const __nv_bfloat16*>(L.xk);
-  const __nv_bfloat16* dYk = static_cast<const __nv_bfloat16*>(L.dyk);
-  {
-    const GatherJob jx{static_cast<const char*>(X), static_cast<char*>(L.xk), (long long)K * 2, (long long)K * 2,
-                       K * 2, 0};
-    const GatherJob jy{static_cast<const char*>(dY), static_cast<char*>(L.dyk), (long long)N * 2, (long long)N * 2,
-                       N * 2, 0};
-    if (dW && ck)
-      CK(launch_q8_unpack(c, 0, ck->format, view(ck), x_full, M, K, idx, n_kept, L.xk, K, 0, pad128(M)));
-    else if (dW)
-      CK(launch_gather(c, &jx, 1, M, pad128(M), x_full ? idx : nullptr, n_kept));
-    CK(launch_gather(c, &jy, 1, M, pad128(M), dy_full ? idx : nullptr, n_kept));
-  }
-  if (dX) {
-    TcGemm g{};
-    g.M = M; g.N = K; g.K = N;
-    g.A = dYk; g.lda = N; g.a_mn_major = 0; g.a_rows = M;
-    g.B = W; g.ldb = N; g.b_mn_major = 0; g.b_rows = K;
-    g.C = dx_full ? L.dxk : dX; g.ldc = K; g.c_bf16 = 1; g.zero_pad = 1; g.c_rows = dx_full ? pad128(M) : M;
-    g.n_kept = n_kept; g.dyn = 1;
-    g.partial = L.sk_partial; g.counters = L.sk_counters; g.counter_cap = L.sk_cap;
-    CK(launch_tc_gemm(c, g));
-    if (dx_full) CK(launch_scatter(c, static_cast<const char*>(L.dxk), (long long)K * 2, static_cast<char*>(dX),
-                                   (long long)K * 2, K * 2, M, idx, n_kept));
-  }
-  if (dW) {
-    TcGemm g{};
-    g.M = K; g.N = N; g.K = M;
-    g.A = Xk; g.lda = K; g.a_mn_major = 1; g.a_rows = M;
-    g.B = dYk; g.ldb = N; g.b_mn_major = 1; g.b_rows = M;
-    g.C = dW; g.ldc = N; g.c_bf16 = 0;
-    g.n_kept = n_kept; g.dyn = 2;
-    // the tensor core's running sum drops bits below its last place at every
-    // step, so its error grows with the reduction: 2048 rows at a time (at
-    // most 5e-7 of the result's norm on normal inputs, against 1.3e-6 at 4096
-    // rows and 3.5e-6 at 16384), added in f32
-    if (ck) g.k_piece = 32;
-    g.partial = L.sk_partial; g.counters = L.sk_counters; g.counter_cap = L.sk_cap;
-    CK(launch_tc_gemm(c, g));
-  }
-  if (db) CK(launch_colsum(c, dYk, 1, N, M, N, nullptr, n_kept, L.part, db));
-  return COLLIDER_OK;
-}
 }  // namespace
 
 extern "C" size_t collider_linear_workspace_size(collider_dtype dtype, int M, int K, int N) {
@@ -579,47 +522,43 @@ extern "C" collider_status collider_linear_bwd(collider_dtype dtype, int M, int 
     return COLLIDER_OK;
   }
 
-  return linear_bf16(c, M, K, N, X, nullptr, x_full, W, dY, dy_full, idx, n_kept, dX, dx_full, dW, db,
-                     LinearBufs{xk, dyk, dxk, part, sk_partial, sk_counters, sk_cap});
-}
-
-extern "C" size_t collider_linear_ckpt_workspace_size(int M, int K, int N) {
-  return collider_linear_workspace_size(COLLIDER_BF16, M, K, N);
-}
-
-extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const collider_ckpt* X, collider_rows x_rows,
-                                                  const void* W, const void* dY, collider_rows dy_rows,
-                                                  const int32_t* idx, const int32_t* n_kept, void* dX,
-                                                  collider_rows dx_rows, float* dW, float* db, void* ws,
-                                                  size_t ws_bytes, void* stream) {
-  static const char* fn = "collider_linear_bwd_ckpt";
-  if (M < 1 || M > (1 << 30) || K < 1 || N < 1) return fail(COLLIDER_ERR_INVALID_ARG, "%s: bad sizes", fn);
-  if (!idx || !n_kept || !dY) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null idx/n_kept/dY", fn);
-  if (dX && !W) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dX needs W", fn);
-  if (!is_rows(x_rows) || !is_rows(dy_rows) || !is_rows(dx_rows))
-    return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
-  if (K % 8 || N % 8) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: needs K, N %% 8 == 0", fn);
-  if (!al16(W) || !al16(dY) || !al16(dX) || !al16(dW) || !al16(db))
-    return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
-  collider_status s = dW ? check_ckpt(fn, X, K) : COLLIDER_OK;
-  if (s != COLLIDER_OK) return s;
-  const size_t need = collider_linear_ckpt_workspace_size(M, K, N);
-  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
-    return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
-  Ctx c;
-  s = make_ctx(stream, &c);
-  if (s == COLLIDER_OK) s = check_memory(fn, {W, dY, idx, n_kept, dX, dW, db, ws});
-  if (s == COLLIDER_OK && dW) s = check_memory(fn, {X->code, X->exps}, true);
-  if (s != COLLIDER_OK) return s;
-  Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
-  LinearBufs L{};
-  linear_carve(cv, COLLIDER_BF16, M, K, N, true, true, true, &L.xk, &L.dyk, &L.dxk, &L.part);
-  L.sk_cap = sk_counter_cap(std::max<long long>(M, K), std::max(K, N));
-  L.sk_counters = reinterpret_cast<int*>(static_cast<char*>(ws) + need - up256(L.sk_cap * sizeof(int)));
-  L.sk_partial = reinterpret_cast<float*>(reinterpret_cast<char*>(L.sk_counters) - up256(kSkPartialFloats * 4));
-  CK(cudaMemsetAsync(L.sk_counters, 0, L.sk_cap * sizeof(int), c.stream));
-  return linear_bf16(c, M, K, N, nullptr, X, x_rows == COLLIDER_ROWS_FULL, W, dY, dy_rows == COLLIDER_ROWS_FULL, idx,
-                     n_kept, dX, dx_rows == COLLIDER_ROWS_FULL, dW, db, L);
+  // bf16: compact operands (zero-padded to 128 rows), tcgen05 GEMMs
+  const __nv_bfloat16* Xk = static_cast<const __nv_bfloat16*>(X);
+  const __nv_bfloat16* dYk = static_cast<const __nv_bfloat16*>(dY);
+  {
+    const GatherJob jx{static_cast<const char*>(X), static_cast<char*>(xk), (long long)K * 2, (long long)K * 2,
+                       K * 2, 0};
+    const GatherJob jy{static_cast<const char*>(dY), static_cast<char*>(dyk), (long long)N * 2, (long long)N * 2,
+                       N * 2, 0};
+    if (dW) CK(launch_gather(c, &jx, 1, M, pad128(M), x_full ? idx : nullptr, n_kept));
+    CK(launch_gather(c, &jy, 1, M, pad128(M), dy_full ? idx : nullptr, n_kept));
+    if (dW) Xk = static_cast<const __nv_bfloat16*>(xk);
+    dYk = static_cast<const __nv_bfloat16*>(dyk);
+  }
+  if (dX) {
+    TcGemm g{};
+    g.M = M; g.N = K; g.K = N;
+    g.A = dYk; g.lda = N; g.a_mn_major = 0; g.a_rows = M;
+    g.B = W; g.ldb = N; g.b_mn_major = 0; g.b_rows = K;
+    g.C = dx_full ? dxk : dX; g.ldc = K; g.c_bf16 = 1; g.zero_pad = 1; g.c_rows = dx_full ? pad128(M) : M;
+    g.n_kept = n_kept; g.dyn = 1;
+    g.partial = sk_partial; g.counters = sk_counters; g.counter_cap = sk_cap;
+    CK(launch_tc_gemm(c, g));
+    if (dx_full) CK(launch_scatter(c, static_cast<const char*>(dxk), (long long)K * 2, static_cast<char*>(dX),
+                                   (long long)K * 2, K * 2, M, idx, n_kept));
+  }
+  if (dW) {
+    TcGemm g{};
+    g.M = K; g.N = N; g.K = M;
+    g.A = Xk; g.lda = K; g.a_mn_major = 1; g.a_rows = M;
+    g.B = dYk; g.ldb = N; g.b_mn_major = 1; g.b_rows = M;
+    g.C = dW; g.ldc = N; g.c_bf16 = 0;
+    g.n_kept = n_kept; g.dyn = 2;
+    g.partial = sk_partial; g.counters = sk_counters; g.counter_cap = sk_cap;
+    CK(launch_tc_gemm(c, g));
+  }
+  if (db) CK(launch_colsum(c, dYk, 1, N, M, N, nullptr, n_kept, part, db));
+  return COLLIDER_OK;
 }
 
 // ===========================================================================
@@ -888,6 +827,124 @@ cudaError_t join_side(const Ctx& c, Side* S, int k) {
   cudaError_t e = cudaEventRecord(S->ev[k], S->s);
   return e == cudaSuccess ? cudaStreamWaitEvent(c.stream, S->ev[k], 0) : e;
 }
+
+}  // namespace
+
+namespace {
+struct LinearCkptBufs {
+  __nv_bfloat16 *xk, *dyk;   // kept rows of X and dY, zero-padded to 128 rows
+  float* part;               // column sums' partials
+};
+size_t linear_ckpt_carve(Carver& cv, int M, int K, int N, LinearCkptBufs* L) {
+  const size_t Mp = (size_t)pad128(M);
+  L->xk = cv.take<__nv_bfloat16>(Mp * K);
+  L->dyk = cv.take<__nv_bfloat16>(Mp * N);
+  L->part = cv.take<float>(colsum_part_floats(M, N));
+  return cv.used;
+}
+}  // namespace
+
+extern "C" size_t collider_linear_ckpt_workspace_size(int M, int K, int N) {
+  if (M < 1 || K < 1 || N < 1) return 0;
+  Carver cv{nullptr, 0, 0, true};
+  LinearCkptBufs L;
+  return linear_ckpt_carve(cv, M, K, N, &L);
+}
+
+extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const collider_ckpt* X, collider_rows x_rows,
+                                                  const void* W, const void* dY, collider_rows dy_rows,
+                                                  const int32_t* idx, const int32_t* n_kept, void* dX,
+                                                  collider_rows dx_rows, float* dW, float* db, void* ws,
+                                                  size_t ws_bytes, void* stream) {
+  static const char* fn = "collider_linear_bwd_ckpt";
+  if (M < 1 || M > (1 << 30) || K < 1 || N < 1) return fail(COLLIDER_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (!idx || !n_kept || !dY) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null idx/n_kept/dY", fn);
+  if (dX && !W) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dX needs W", fn);
+  if (!is_rows(x_rows) || !is_rows(dy_rows) || !is_rows(dx_rows))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
+  if (K % 8 || N % 8) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: needs K, N %% 8 == 0", fn);
+  if (!al16(W) || !al16(dY) || !al16(dX) || !al16(dW) || !al16(db))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  collider_status s = dW ? check_ckpt(fn, X, K) : COLLIDER_OK;
+  if (s != COLLIDER_OK) return s;
+  const size_t need = collider_linear_ckpt_workspace_size(M, K, N);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
+  Ctx c;
+  s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_memory(fn, {W, dY, idx, n_kept, dX, dW, db, ws});
+  if (s == COLLIDER_OK && dW) s = check_memory(fn, {X->code, X->exps}, true);
+  if (s != COLLIDER_OK) return s;
+  Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
+  LinearCkptBufs L;
+  linear_ckpt_carve(cv, M, K, N, &L);
+  const bool dx_full = dx_rows == COLLIDER_ROWS_FULL;
+  LinearPrep p{};
+  p.M = M; p.K = K; p.N = N; p.cap = pad128(M); p.idx = idx; p.n_kept = n_kept;
+  if (dW) {
+    p.x = view(X); p.format = X->format; p.x_full = x_rows == COLLIDER_ROWS_FULL; p.xk = L.xk;
+  }
+  p.dy = static_cast<const __nv_bfloat16*>(dY); p.dy_full = dy_rows == COLLIDER_ROWS_FULL; p.dyk = L.dyk;
+  if (dX && dx_full) p.dx = static_cast<__nv_bfloat16*>(dX);
+  // The weight gradient's part runs on the side stream: X is decoded and dX's
+  // filtered rows are zeroed beside the dX GEMM, and the dW GEMM's first tiles
+  // take the SMs that the dX GEMM's last wave leaves.  Against one stream, with
+  // the three copies in one launch, 40% filtered: 172 and 179 us at 8192 rows x
+  // 5632 x 2048, 170 and 193 at 8192 x 2048 x 5632, 213 and 209 at 8192 x 1536 x
+  // 8960, 44 and 43 at 2048^3, 16 and 22 at 128 x 256 x 256.
+  Ctx cs = c;
+  Side* side = nullptr;
+  if (dX && dW) {
+    s = side_ctx(c, &cs, &side);
+    if (s != COLLIDER_OK) return s;
+  }
+  if (side) {
+    CK(fork_side(c, side, 0));
+    LinearPrep px = p;
+    px.dyk = nullptr;
+    p.xk = nullptr; p.dx = nullptr;
+    CK(launch_linear_prep(cs, px));
+    CK(launch_linear_prep(c, p));
+    CK(fork_side(c, side, 1));
+  } else {
+    CK(launch_linear_prep(c, p));
+  }
+  Ctx cp = c;
+  cp.pdl = pdl_allowed();
+  // Whole tiles only: on the block shapes and down to 128 x 256 x 256 a
+  // stream-K tail never made these launches faster (2048 x 2048 x 2048, 1229
+  // rows kept: 57 us without, 82 us with; 128 x 256 x 256: 31 and 51 us).
+  if (dX) {
+    TcGemm g{};
+    g.M = M; g.N = K; g.K = N;
+    g.A = L.dyk; g.lda = N; g.a_mn_major = 0; g.a_rows = pad128(M);
+    g.B = W; g.ldb = N; g.b_mn_major = 0; g.b_rows = K;
+    g.C = dX; g.ldc = K; g.c_bf16 = 1; g.c_rows = M;
+    g.zero_pad = dx_full ? 0 : 1;
+    g.c_idx = dx_full ? idx : nullptr;   // a FULL dX's kept rows where they belong
+    g.n_kept = n_kept; g.dyn = 1;
+    CK(launch_tc_gemm(cp, g));
+  }
+  if (dW) {
+    TcGemm g{};
+    g.M = K; g.N = N; g.K = M;
+    g.A = L.xk; g.lda = K; g.a_mn_major = 1; g.a_rows = pad128(M);
+    g.B = L.dyk; g.ldb = N; g.b_mn_major = 1; g.b_rows = pad128(M);
+    g.C = dW; g.ldc = N; g.c_bf16 = 0;
+    g.n_kept = n_kept; g.dyn = 2;
+    // The tensor core's running sum drops bits below its last place at every
+    // step, so its error grows with the reduction: at most 2560 rows at a time
+    // (an error of 8e-7 of the result's norm on normal inputs, against 1.3e-6 at
+    // 4096 rows and 3.5e-6 at 16384), the pieces added in f32.
+    g.k_piece = 2560 / 64;
+    CK(launch_tc_gemm(side ? cs : cp, g));
+  }
+  if (db) CK(launch_colsum(side ? cs : c, L.dyk, 1, N, M, N, nullptr, n_kept, L.part, db));
+  CK(join_side(c, side, 2));
+  return COLLIDER_OK;
+}
+
+namespace {
 
 // stream-K scratch shared by the input-gradient chain's GEMMs of one call
 // (they run in stream order)

@@ -42,6 +42,7 @@ struct TcParams {
   int* counters;     // stream-K: per-(tile, pair rank) arrival counts, zero on entry and left zero
   int split_mode;    // 0 whole tiles, 1 stream-K, 2 hybrid, 3 auto (see Split)
   int k_piece;       // whole tiles: k-slices accumulated at a time (0: all)
+  const int32_t* c_idx;   // output row of each row (null: itself)
   DevStatus* st;
 };
 
@@ -169,19 +170,31 @@ struct SegIter {
 
 // Store 32 consecutive columns of one output row (bf16 or f32, optional
 // accumulate into C, zero rows past the kept count up to the padding).
-__device__ __forceinline__ void store32(const TcParams& p, int row, int col, bool row_ok, float* v, bool add) {
+__device__ __forceinline__ void store32(const TcParams& p, long long row, int col, bool row_ok, float* v, bool piece = false) {
   if (p.c_bf16) {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + (long long)row * p.ldc + col;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + row * p.ldc + col;
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       if (col + 8 * g + 8 <= p.N) *reinterpret_cast<uint4*>(out + 8 * g) = pack8(v + 8 * g);
   } else {
-    float* out = static_cast<float*>(p.C) + (long long)row * p.ldc + col;
+    float* out = static_cast<float*>(p.C) + row * p.ldc + col;
+    if (piece && row_ok) {
+      // a later piece of the reduction is added where C lies, without a round
+      // trip (an f32 add rounded to nearest; subnormal values count as 0), by
+      // the thread that stored the piece before it, so in order
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        if (col + 4 * g + 4 <= p.N)
+          asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(out + 4 * g), "f"(v[4 * g]),
+                       "f"(v[4 * g + 1]), "f"(v[4 * g + 2]), "f"(v[4 * g + 3])
+                       : "memory");
+      return;
+    }
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
       if (col + 4 * g + 4 <= p.N) {
         float4 o = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-        if (add && row_ok) {
+        if (p.accumulate && row_ok) {
           float4 old = *reinterpret_cast<const float4*>(out + 4 * g);
           o.x += old.x; o.y += old.y; o.z += old.z; o.w += old.w;
         }
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          store32(p, row, n0 + c, row_ok, v, p.accumulate);
+          store32(p, row, n0 + c, row_ok, v);
         }
       }
     }
@@ -455,18 +468,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     while (si.next(t, k0, k1)) {
       const int acc = seg & 1;
       const uint32_t aph = (seg >> 1) & 1;
-      if (!mbar_wait(tfull0 + 8 * acc, aph, &no_abort, p.st, 4)) break;
-      fence_after();
       int m0, n0;
       origin(t, m0, n0);
       const int rl = q * 32 + lane;
       const int row = m0 + rl;
-      const bool row_ok = row < M;
-      const bool row_zero = !row_ok && p.zero_pad && row < padded_rows(M, p.c_rows);
+      bool row_ok = row < M;
+      long long out_row = row;
+      if (p.c_idx && row_ok) {
+        out_row = p.c_idx[row];
+        row_ok = out_row >= 0 && out_row < p.c_rows;
+        if (!row_ok) report_error(p.st, kErrBadIndex, 60);
+      }
+      if (!mbar_wait(tfull0 + 8 * acc, aph, &no_abort, p.st, 4)) break;
+      fence_after();
+      const bool row_zero = !row_ok && p.zero_pad && row < padded_rows(M, p.c_rows);   // (never with c_idx)
       const uint32_t tcol = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
       if ((k0 == 0 && k1 == sp.num_kb) || t < sp.dp_tiles) {
-        // whole tile (or a piece of its reduction, added to the pieces before
-        // it by the thread that stored them): straight to the output
+        // whole tile, or a piece of its reduction: straight to the output
         for (int c = 0; c < BN; c += 32) {
           float v[32];
           tmem_ld32(tcol + c, v);
@@ -475,7 +493,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
           }
-          store32(p, row, n0 + c, row_ok, v, p.accumulate || k0 > 0);
+          store32(p, out_row, n0 + c, row_ok, v, k0 > 0);
         }
         fence_before();
         release_acc(acc);
@@ -522,7 +540,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0.f;
             }
-            store32(p, row, n0 + c, row_ok, v, p.accumulate);
+            store32(p, row, n0 + c, row_ok, v);
           }
         }
         named_bar(1, 128);   // last_flag is reused by the next segment
@@ -675,7 +693,7 @@ cudaError_t launch_tc_gemm(const Ctx& c, const TcGemm& g) {
   const long long m_tiles = (g.M + BM - 1) / BM, n_tiles = (g.N + bn - 1) / bn;
   const long long max_ctrs = (pair ? 2 * ((m_tiles + 1) / 2) : m_tiles) * n_tiles;
   const int split = split_env >= 0 ? split_env : 3;
-  const bool sk = split != 0 && g.k_piece == 0 && g.partial && g.counters && max_ctrs <= g.counter_cap;
+  const bool sk = split != 0 && g.k_piece == 0 && !g.c_idx && g.partial && g.counters && max_ctrs <= g.counter_cap;
   CUtensorMap ma, mb;
   // A: K-major [M rows, K] or MN-major [K rows, M]; B: K-major [N rows, K]
   // (half the tile's rows per box for a pair) or MN-major [K rows, N]
@@ -686,7 +704,7 @@ cudaError_t launch_tc_gemm(const Ctx& c, const TcGemm& g) {
   if (!ok) return cudaErrorInvalidValue;
   TcParams p{g.M, g.N, g.K, g.dyn, g.n_kept, g.C, g.ldc, g.c_bf16, g.accumulate, g.zero_pad,
              g.c_rows > 0 ? g.c_rows : g.M, sk ? g.partial : nullptr, sk ? g.counters : nullptr,
-             split, g.k_piece, c.st};
+             split, g.k_piece, g.c_idx, c.st};
   prof_begin(c, "tc_gemm", g.M, g.N, g.K, g.dyn);
   cudaError_t e;
   const int key = (bn == 256 ? 100 : 0) + (g.a_mn_major ? 10 : (g.b_mn_major ? 20 : 0)) + mode;

@@ -201,9 +201,13 @@ struct TcGemm {
   long long c_rows;   // row capacity of C (zero padding stops there)
   const int32_t* n_kept; int dyn;
   int bn;             // 128 or 256 (0 = choose)
-  // f32 C, whole tiles: at most this many 64-deep k-slices are accumulated in
-  // TMEM at a time; the pieces of a longer reduction are added in C (0: no limit)
+  // f32 C, dyn = 2, whole tiles, no accumulate: at most this many 64-deep k-slices
+  // are accumulated in TMEM at a time; the pieces of a longer reduction are added
+  // in C (0: no limit)
   int k_piece;
+  // output row of row m (dyn = 1, zero_pad = 0, whole tiles): c_idx[m], kept
+  // below c_rows (null: m).  Rows it does not name are left as they are.
+  const int32_t* c_idx;
   // stream-K scratch (both null: whole tiles only).  partial holds
   // kSkMaxCtas * 2 tiles of 128 x 256 f32; counters hold counter_cap ints,
   // zero before the launch (the kernel leaves them zero).
@@ -322,6 +326,25 @@ cudaError_t launch_q8_pack(const Ctx& c, int f32, const void* src, long long src
 cudaError_t launch_q8_unpack(const Ctx& c, int f32, int format, const Q8View& q, int src_full, int M, int N,
                              const int32_t* idx, const int32_t* n_kept, void* dst, long long dst_ld, int dst_full,
                              long long cap);
+
+// What the linear backward needs before its GEMMs, in one launch: the kept rows
+// of a checkpoint (x_full: read through idx) decoded into xk, those of dY
+// copied into dyk, both zero-padded to 128 rows (below cap), and the rows of a
+// FULL dx that are not kept zeroed.  Parts left out: xk, dyk, dx null.
+struct LinearPrep {
+  int M, K, N;
+  Q8View x;
+  int format, x_full;
+  __nv_bfloat16* xk;      // [cap, K]
+  const __nv_bfloat16* dy;
+  int dy_full;
+  __nv_bfloat16* dyk;     // [cap, N]
+  __nv_bfloat16* dx;      // [M, K]
+  long long cap;
+  const int32_t* idx;
+  const int32_t* n_kept;
+};
+cudaError_t launch_linear_prep(const Ctx& c, const LinearPrep& p);
 
 // ---- residual join (join_fwd.cu, join_bwd.cu) --------------------------------
 // h = alpha res_w x + gate post(y), a = pre(h); rows of D values (D % 8 == 0,

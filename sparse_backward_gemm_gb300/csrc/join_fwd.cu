@@ -34,7 +34,7 @@ struct FwdArgs {
 };
 
 template <typename T, bool LN, int VPT>
-__global__ void __launch_bounds__(512) join_fwd_kernel(FwdArgs p, DevStatus* st) {
+__global__ void __launch_bounds__(kThreads) join_fwd_kernel(FwdArgs p, DevStatus* st) {
   extern __shared__ __align__(128) uint8_t smem[];
   const Place pl(p.tpr);
   float* red = reinterpret_cast<float*>(smem + pl.group * kRedBytes);
@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(512) join_fwd_kernel(FwdArgs p, DevStatus* st)
     for (int s = 0; s < p.stages; ++s) tc::mbar_init(bar0 + 8 * s, 1);
   for (int i = pl.lane; i < (int)(kRedBytes / 4); i += p.tpr) red[i] = 0.f;
   if (threadIdx.x == 0) *abort_flag = 0;
+  if (threadIdx.x < 8) reinterpret_cast<uint32_t*>(smem + zero_at(p.groups))[threadIdx.x] = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncthreads();
 
@@ -55,92 +56,131 @@ __global__ void __launch_bounds__(512) join_fwd_kernel(FwdArgs p, DevStatus* st)
   const int vecs = p.D / 8;
   const uint32_t row_bytes = p.D * (uint32_t)sizeof(T), total = y ? 2 * row_bytes : row_bytes;
   const int step = gridDim.x * p.groups, r0 = blockIdx.x * p.groups + pl.group;
-  auto issue = [&](int r, int s) {
+  auto issue = [&](long long r, int s) {
     const uint32_t b = bar0 + 8 * s, d = ring0 + s * p.stage_bytes;
     tc::mbar_expect_tx(b, total);
-    copy_row(d, x + (long long)r * p.x_ld, row_bytes, b);
-    if (y) copy_row(d + row_bytes, y + (long long)r * p.y_ld, row_bytes, b);
+    copy_row(d, x + r * p.x_ld, row_bytes, b);
+    if (y) copy_row(d + row_bytes, y + r * p.y_ld, row_bytes, b);
   };
   if (pl.lane == 0)
     for (int s = 0; s < p.stages; ++s)
-      if ((long long)r0 + (long long)s * step < p.M) issue(r0 + s * step, s);
+      if (r0 + (long long)s * step < p.M) issue(r0 + (long long)s * step, s);
 
-  int half = 0, s = 0;
-  uint32_t parity = 0;
-  for (long long r = r0; r < p.M; r += step) {
-    tc::mbar_wait(bar0 + 8 * s, (parity >> s) & 1u, abort_flag, st, 710);
-    const uint8_t* stage = ring + s * p.stage_bytes;
-    float xv[VPT][8], yv[VPT][8];
-    bool on[VPT];
+  // gate times the post norm's weight and bias, for the rows of one sequence
+  // (of all sequences when there is one row of gates); 0 beyond the row
+  Vec8 c1[VPT], c0[LN ? VPT : 1];
+  auto set_gate = [&](int b) {
+    const T* gate = p.gate_rows ? static_cast<const T*>(p.gate) + (p.gate_rows > 1 ? (long long)b * p.D : 0) : nullptr;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = pl.lane + k * p.tpr;
-      on[k] = v < vecs;
+      const bool on = v < vecs;
+      const Vec8 g = param8<T>(gate, v, on, 1.f), w = param8<T>(p.post_w, v, on, 1.f);
+      const Vec8 o = param8<T>(p.post_b, v, on, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xv[k][i] = yv[k][i] = 0.f;
-      if (on[k]) {
-        get8<T>(stage + v * 8 * sizeof(T), xv[k]);
-        if (y) get8<T>(stage + row_bytes + v * 8 * sizeof(T), yv[k]);
+      for (int i = 0; i < 4; ++i) {
+        c1[k].v[i] = mul2(g.v[i], w.v[i]);
+        if (LN) c0[LN ? k : 0].v[i] = mul2(g.v[i], o.v[i]);
       }
     }
-    parity ^= 1u << s;
-    // every thread has its values: the stage is free for a row further on
-    pl.sync();
-    if (pl.lane == 0) {
-      const long long rn = r + (long long)p.stages * step;
-      if (rn < p.M) issue((int)rn, s);
-    }
-    if (++s == p.stages) s = 0;
+  };
+  const int seq_rows = p.gate_rows > 1 ? p.T : p.M;   // rows that share a gate
+  int gate_end = 0;
 
-    // mean and reciprocal deviation of a row held in v
-    auto stats = [&](float (*v)[8], float& mean, float& rstd) {
-      float q[1] = {0.f};
-      mean = 0.f;
-      if (LN) {
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q[0] += v[k][i];
-        group_sum(pl, red, half, q);
-        mean = q[0] * p.inv_d;
-        q[0] = 0.f;
-      }
+  // mean and reciprocal deviation of a row held in v (0 beyond the row), and
+  // the row less its mean
+  int half = 0;
+  auto stats = [&](Vec8 (&v)[VPT], float& mean, float& rstd) {
+    float q[1];
+    mean = 0.f;
+    if (LN) {
+      f2 t = both(0.f);
 #pragma unroll
       for (int k = 0; k < VPT; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float d = on[k] ? v[k][i] - mean : 0.f;
-          q[0] = fmaf(d, d, q[0]);
-        }
+        for (int i = 0; i < 4; ++i) t = add2(t, v[k].v[i]);
+      q[0] = t.x + t.y;
       group_sum(pl, red, half, q);
-      rstd = __frsqrt_rn(fmaf(q[0], p.inv_d, p.eps));
+      mean = q[0] * p.inv_d;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const f2 m = both(pl.lane + k * p.tpr < vecs ? -mean : 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k].v[i] = add2(v[k].v[i], m);
+      }
+    }
+    f2 t = both(0.f);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t = fma2(v[k].v[i], v[k].v[i], t);
+    q[0] = t.x + t.y;
+    group_sum(pl, red, half, q);
+    rstd = __frsqrt_rn(fmaf(q[0], p.inv_d, p.eps));
+  };
+
+  // threads beyond the row read zeros
+  const uint32_t off = pl.lane * 8 * (uint32_t)sizeof(T), hop = p.tpr * 8 * (uint32_t)sizeof(T);
+  const uint8_t* zero = smem + zero_at(p.groups);
+  int s = 0;
+  uint32_t parity = 0;
+  for (int r = r0; r < p.M; r += step) {
+    if (r >= gate_end) {   // the first row, and each first row of a sequence
+      const int b = r / seq_rows;
+      set_gate(b);
+      gate_end = (int)min((long long)p.M, (b + 1ll) * seq_rows);
+    }
+    tc::mbar_wait(bar0 + 8 * s, (parity >> s) & 1u, abort_flag, st, 710);
+    const uint8_t* stage = ring + s * p.stage_bytes + off;
+    Vec8 xv[VPT], yv[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const bool on = pl.lane + k * p.tpr < vecs;
+      xv[k] = get8<T>(on ? stage + k * hop : zero);
+      if (y) yv[k] = get8<T>(on ? stage + row_bytes + k * hop : zero);
+    }
+    parity ^= 1u << s;
+    // once every thread has its values the stage is free for a row further on:
+    // after the first sum over the group (or a barrier where there is none)
+    auto refill = [&] {
+      if (pl.lane == 0) {
+        const long long rn = r + (long long)p.stages * step;
+        if (rn < p.M) issue(rn, s);
+      }
+      if (++s == p.stages) s = 0;
     };
+    if (!p.post) {
+      pl.sync();
+      refill();
+    }
 
     if (y) {
       float mean = 0.f, rstd = 1.f;
       if (p.post) {
         stats(yv, mean, rstd);
+        refill();
         if (pl.lane == 0) {
           p.rstd_y[r] = rstd;
           if (LN) p.mean_y[r] = mean;
         }
       }
-      const T* gate = p.gate_rows ? static_cast<const T*>(p.gate) + (p.gate_rows > 1 ? (r / p.T) * p.D : 0) : nullptr;
+      T* row = h + r * p.h_ld + 8 * pl.lane;
+      const f2 rs = both(rstd), al = both(p.alpha);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        if (!on[k]) continue;
-        const int v = pl.lane + k * p.tpr;
-        float w[8], b[8], g[8], l[8];
-        param8(static_cast<const T*>(p.post_w), v, 1.f, w);
-        param8(static_cast<const T*>(p.post_b), v, 0.f, b);
-        param8(gate, v, 1.f, g);
-        param8(static_cast<const T*>(p.res_w), v, 1.f, l);
+        const bool on = pl.lane + k * p.tpr < vecs;
+        if (p.res_w) {
+          const Vec8 l = param8<T>(p.res_w, pl.lane + k * p.tpr, on, 0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float n = p.post ? norm_affine(yv[k][i], mean, rstd, w[i], b[i]) : yv[k][i];
-          xv[k][i] = stored<T>(fmaf(g[i], n, p.alpha * l[i] * xv[k][i]));
+          for (int i = 0; i < 4; ++i) xv[k].v[i] = mul2(xv[k].v[i], l.v[i]);
         }
-        put8(h + r * p.h_ld + 8 * v, xv[k]);
+        Vec8 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 res = LN ? fma2(al, xv[k].v[i], c0[LN ? k : 0].v[i]) : mul2(al, xv[k].v[i]);
+          o.v[i] = fma2(c1[k].v[i], mul2(yv[k].v[i], rs), res);
+        }
+        xv[k] = put8_stored(row + k * p.tpr * 8, on, o);
       }
     }
     if (p.pre) {
@@ -150,16 +190,20 @@ __global__ void __launch_bounds__(512) join_fwd_kernel(FwdArgs p, DevStatus* st)
         p.rstd_h[r] = rstd;
         if (LN) p.mean_h[r] = mean;
       }
+      T* row = a + r * p.a_ld + 8 * pl.lane;
+      const f2 rs = both(rstd);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        if (!on[k]) continue;
         const int v = pl.lane + k * p.tpr;
-        float w[8], b[8], o[8];
-        param8(static_cast<const T*>(p.pre_w), v, 1.f, w);
-        param8(static_cast<const T*>(p.pre_b), v, 0.f, b);
+        if (v >= vecs) continue;
+        const Vec8 w = get8<T>(static_cast<const T*>(p.pre_w) + 8 * v);
+        const Vec8 o = LN ? param8<T>(p.pre_b, v, true, 0.f) : all8(0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = norm_affine(xv[k][i], mean, rstd, w[i], b[i]);
-        put8(a + r * p.a_ld + 8 * v, o);
+        for (int i = 0; i < 4; ++i) {
+          const f2 n = mul2(xv[k].v[i], rs);
+          xv[k].v[i] = LN ? fma2(n, w.v[i], o.v[i]) : mul2(n, w.v[i]);
+        }
+        put8(row + k * p.tpr * 8, xv[k]);
       }
     }
   }
@@ -179,6 +223,11 @@ cudaError_t launch(const Ctx& c, const FwdArgs& p, const Shape& s) {
   return cudaGetLastError();
 }
 
+template <typename T, bool LN>
+cudaError_t by_vpt(const Ctx& c, const FwdArgs& p, const Shape& s) {
+  return s.vpt == 1 ? launch<T, LN, 1>(c, p, s) : s.vpt == 2 ? launch<T, LN, 2>(c, p, s) : launch<T, LN, 4>(c, p, s);
+}
+
 }  // namespace
 
 cudaError_t launch_join_fwd(const Ctx& c, const JoinFwd& j) {
@@ -191,18 +240,14 @@ cudaError_t launch_join_fwd(const Ctx& c, const JoinFwd& j) {
   p.post_w = j.post_w; p.post_b = j.post_b; p.gate = j.gate; p.res_w = j.res_w; p.pre_w = j.pre_w; p.pre_b = j.pre_b;
   p.mean_y = j.mean_y; p.rstd_y = j.rstd_y; p.mean_h = j.mean_h; p.rstd_h = j.rstd_h;
   const uint32_t row = (uint32_t)j.D * (j.f32 ? 4 : 2) * (j.y ? 2 : 1);
-  const Shape s = make_shape(j.D, row, 0, 100 * 1024);
+  const int vpt = j.D <= 256 ? 1 : j.D <= 4096 ? 2 : 4;
+  const Shape s = make_shape(j.D, vpt, row, 0, 60 * 1024);
   p.tpr = s.tpr; p.groups = s.groups; p.stages = s.stages; p.stage_bytes = s.stage_bytes;
   prof_begin(c, "residual_norm_fwd");
+  using bf = __nv_bfloat16;
   cudaError_t e;
-  if (j.f32) {
-    if (j.layer_norm) e = s.vpt == 1 ? launch<float, true, 1>(c, p, s) : launch<float, true, 2>(c, p, s);
-    else e = s.vpt == 1 ? launch<float, false, 1>(c, p, s) : launch<float, false, 2>(c, p, s);
-  } else {
-    using bf = __nv_bfloat16;
-    if (j.layer_norm) e = s.vpt == 1 ? launch<bf, true, 1>(c, p, s) : launch<bf, true, 2>(c, p, s);
-    else e = s.vpt == 1 ? launch<bf, false, 1>(c, p, s) : launch<bf, false, 2>(c, p, s);
-  }
+  if (j.f32) e = j.layer_norm ? by_vpt<float, true>(c, p, s) : by_vpt<float, false>(c, p, s);
+  else e = j.layer_norm ? by_vpt<bf, true>(c, p, s) : by_vpt<bf, false>(c, p, s);
   prof_end(c);
   count_launch();
   return e;

@@ -93,6 +93,38 @@ __global__ void __launch_bounds__(kThreads) q8_pack_kernel(const T* __restrict__
   }
 }
 
+// decodes this lane's vectors (v0 + 32 k) of row sr of q
+template <typename T, int FMT>
+__device__ __forceinline__ void unpack_segment(const Q8View& q, long long sr, T* d, int v0, int vecs) {
+  uint2 c[kUnroll];
+  unsigned e[kUnroll];
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k) {
+    const int v = v0 + 32 * k;
+    c[k] = make_uint2(0, 0);
+    e[k] = 0;
+    if (v < vecs) {
+      c[k] = *reinterpret_cast<const uint2*>(q.code + sr * q.code_ld + 8 * v);
+      e[k] = q.exps[sr * q.exp_ld + (v >> 2)];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k) {
+    const int v = v0 + 32 * k;
+    float f[8];
+    q8_decode8<FMT>(c[k], q8_scale(e[k]), f);
+    if (v < vecs) store_vec(d + 8 * v, f);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void zero_segment(T* d, int v0, int vecs) {
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k) {
+    const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (v0 + 32 * k < vecs) store_vec(d + 8 * (v0 + 32 * k), z);
+  }
+}
+
 // Row slots: the kept rows first, then the rows that get zeros (the filtered
 // tokens of a FULL output, the padding of a COMPACT one).
 template <typename T, int FMT>
@@ -112,12 +144,7 @@ __global__ void __launch_bounds__(kThreads) q8_unpack_kernel(Q8View q, int src_f
     const int r = (int)(u / segs), v0 = (int)(u % segs) * kSegVecs + lane;
     if (r >= nk) {
       const int t = dst_full ? filtered_token(idx, nk, r - nk) : r;
-      T* d = dst + (long long)t * dst_ld;
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (v0 + 32 * k < vecs) store_vec(d + 8 * (v0 + 32 * k), z);
-      }
+      zero_segment(dst + (long long)t * dst_ld, v0, vecs);
       continue;
     }
     int t = r;
@@ -128,25 +155,52 @@ __global__ void __launch_bounds__(kThreads) q8_unpack_kernel(Q8View q, int src_f
         continue;
       }
     }
-    const long long sr = src_full ? t : r, dr = dst_full ? t : r;
-    uint2 c[kUnroll];
-    unsigned e[kUnroll];
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int v = v0 + 32 * k;
-      c[k] = make_uint2(0, 0);
-      e[k] = 0;
-      if (v < vecs) {
-        c[k] = *reinterpret_cast<const uint2*>(q.code + sr * q.code_ld + 8 * v);
-        e[k] = q.exps[sr * q.exp_ld + (v >> 2)];
-      }
+    unpack_segment<T, FMT>(q, src_full ? t : r, dst + (dst_full ? t : r) * dst_ld, v0, vecs);
+  }
+}
+
+// Units of the three parts one after another: segments of xk's rows, of dyk's,
+// and of dx's filtered rows.
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) linear_prep_kernel(LinearPrep p, DevStatus* st) {
+  const int nk = kept_rows(p.n_kept, p.M);
+  const int lane = threadIdx.x & 31;
+  const int kv = p.K >> 3, ks = (kv + kSegVecs - 1) / kSegVecs, nv = p.N >> 3, ns = (nv + kSegVecs - 1) / kSegVecs;
+  const long long pad = padded_rows(nk, p.cap);
+  const long long ux = p.xk ? pad * ks : 0, uy = ux + (p.dyk ? pad * ns : 0),
+                  units = uy + (p.dx ? (long long)(p.M - nk) * ks : 0);
+  const long long stride = (long long)gridDim.x * (kThreads / 32);
+  for (long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
+    if (u >= uy) {
+      const int j = (int)((u - uy) / ks), v0 = (int)((u - uy) % ks) * kSegVecs + lane;
+      zero_segment(p.dx + (long long)filtered_token(p.idx, nk, j) * p.K, v0, kv);
+      continue;
     }
+    const bool is_x = u < ux;
+    const long long w = is_x ? u : u - ux;
+    const int segs = is_x ? ks : ns, r = (int)(w / segs), v0 = (int)(w % segs) * kSegVecs + lane;
+    if (r >= nk) {
+      if (is_x) zero_segment(p.xk + (long long)r * p.K, v0, kv);
+      else zero_segment(p.dyk + (long long)r * p.N, v0, nv);
+      continue;
+    }
+    const int t = (is_x ? p.x_full : p.dy_full) ? p.idx[r] : r;
+    if ((unsigned)t >= (unsigned)p.M) {
+      if (lane == 0) report_error(st, kErrBadIndex, 702);
+      continue;
+    }
+    if (is_x) {
+      unpack_segment<__nv_bfloat16, FMT>(p.x, t, p.xk + (long long)r * p.K, v0, kv);
+    } else {
+      const uint4* s = reinterpret_cast<const uint4*>(p.dy + (long long)t * p.N);
+      uint4* d = reinterpret_cast<uint4*>(p.dyk + (long long)r * p.N);
+      uint4 c[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int v = v0 + 32 * k;
-      float f[8];
-      q8_decode8<FMT>(c[k], q8_scale(e[k]), f);
-      if (v < vecs) store_vec(dst + dr * dst_ld + 8 * v, f);
+      for (int k = 0; k < kUnroll; ++k)
+        if (v0 + 32 * k < nv) c[k] = s[v0 + 32 * k];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (v0 + 32 * k < nv) d[v0 + 32 * k] = c[k];
     }
   }
 }
@@ -198,6 +252,19 @@ cudaError_t launch_q8_unpack(const Ctx& c, int f32, int format, const Q8View& q,
   prof_end(c);
   count_launch();
   return launched(e);
+}
+
+cudaError_t launch_linear_prep(const Ctx& c, const LinearPrep& p) {
+  prof_begin(c, "linear_prep");
+  const long long ks = (p.K / 8 + kSegVecs - 1) / kSegVecs, ns = (p.N / 8 + kSegVecs - 1) / kSegVecs;
+  const long long units = p.cap * ((p.xk || p.dx ? ks : 0) + (p.dyk ? ns : 0)), fit = (long long)c.num_sms * 8;
+  const long long want = (units + kThreads / 32 - 1) / (kThreads / 32);
+  const int grid = (int)(want < 1 ? 1 : want < fit ? want : fit);
+  if (p.format == kQ8E4m3) linear_prep_kernel<kQ8E4m3><<<grid, kThreads, 0, c.stream>>>(p, c.st);
+  else linear_prep_kernel<kQ8Int8><<<grid, kThreads, 0, c.stream>>>(p, c.st);
+  prof_end(c);
+  count_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace collider

@@ -224,7 +224,7 @@ def test_linear_backward(M, K, N, f, fmt, x_rows, dy_rows, dx_rows):
     tol = _mma_tol(aX, N / 16 + 1)
     assert np.all(np.abs(got - rX) <= tol + 2.0 ** -8 * (np.abs(rX) + tol))
     rW, aW = Xd.T @ dYk, np.abs(Xd).T @ np.abs(dYk)
-    assert np.all(np.abs(gu.host(dW) - rW) <= _mma_tol(aW, min(n, 2048) / 16 + 1 + n / 2048))
+    assert np.all(np.abs(gu.host(dW) - rW) <= _mma_tol(aW, min(n, 2560) / 16 + 1 + n / 1280))
     # db: f32 sums of at most n terms
     assert np.all(np.abs(gu.host(db) - dYk.sum(0)) <= (n + 1) * 2.0 ** -24 * np.abs(dYk).sum(0))
 
@@ -250,10 +250,12 @@ def test_linear_parts_alone_and_repeat():
     assert torch.equal(run(x=None, want_dw=False)[0], a[0])
     assert torch.equal(run(want_dx=False)[1], a[1])
     assert torch.equal(run(want_dx=False, want_dw=False)[2], a[2])
-    # the decoded rows through collider_linear_bwd: the same operands, so dX and db are the same bits
+    # the decoded rows through collider_linear_bwd: the same products; db in the same order, dX and dW perhaps cut elsewhere
+    ws = torch.empty(cl.collider_linear_workspace_size(cl.BF16, M, K, N), dtype=torch.uint8, device=gu.DEV)
     X = torch.empty(M, K, dtype=torch.bfloat16, device=gu.DEV)
     cl.collider_ckpt_unpack(cl.BF16, q, 0, M, K, None, None, X, K, 0)
     dX, dW, db = torch.empty_like(a[0]), torch.empty_like(a[1]), torch.empty_like(a[2])
     cl.collider_linear_bwd(cl.BF16, M, K, N, X, 0, W, dY, 0, idx, nk, dX, 0, dW, db, ws)
-    assert torch.equal(dX, a[0]) and torch.equal(db, a[2])
+    assert torch.equal(db, a[2])
+    assert gu.rel_err(gu.host(dX), gu.host(a[0])) <= 2.0 ** -7      # half a bf16 step each
     assert gu.rel_err(gu.host(dW), gu.host(a[1])) <= 1e-5
