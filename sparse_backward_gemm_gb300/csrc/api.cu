@@ -360,7 +360,8 @@ collider_status check_ckpt(const char* fn, const collider_ckpt* q, int N) {
   if (!q || !q->code || !q->exps) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null checkpoint", fn);
   if (q->format != COLLIDER_CKPT_E4M3 && q->format != COLLIDER_CKPT_INT8)
     return fail(COLLIDER_ERR_UNSUPPORTED, "%s: checkpoint format %d", fn, q->format);
-  if (N < 32 || N % 32) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: checkpoint rows need N %% 32 == 0", fn);
+  if (N < 32 || N % 32 || N > (1 << 24))
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: checkpoint rows need N %% 32 == 0, 32 <= N <= 2^24", fn);
   if (!al16(q->code) || q->code_ld % 16 || q->code_ld < (size_t)N || q->exp_ld < (size_t)N / 32 ||
       q->code_ld > (1u << 30) || q->exp_ld > (1u << 30))
     return fail(COLLIDER_ERR_INVALID_ARG,
@@ -857,7 +858,8 @@ extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const c
                                                   collider_rows dx_rows, float* dW, float* db, void* ws,
                                                   size_t ws_bytes, void* stream) {
   static const char* fn = "collider_linear_bwd_ckpt";
-  if (M < 1 || M > (1 << 30) || K < 1 || N < 1) return fail(COLLIDER_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (M < 1 || M > (1 << 30) || K < 1 || N < 1 || K > (1 << 24) || N > (1 << 24))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: bad sizes", fn);
   if (!idx || !n_kept || !dY) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null idx/n_kept/dY", fn);
   if (dX && !W) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dX needs W", fn);
   if (!is_rows(x_rows) || !is_rows(dy_rows) || !is_rows(dx_rows))

@@ -11,13 +11,17 @@
 // are read.  Collider drops filtered rows in every layer (arXiv 2502.00340,
 // abstract): only kept rows are read, and a FULL output gets zeros elsewhere.
 //
-// Bound by HBM: da, dH, y, h are read and dx, dy written once (12 D bytes a
-// row in bf16, 10 D with 8-bit y and h).  A row's two sums depend on one
-// another, so a row takes some 500 cycles however it is spread; the ring keeps
-// several rows' copies in flight meanwhile.  Each thread owns the same columns
-// of every row it sees and keeps their parameter sums in registers; a CTA's
-// sums are parked in the workspace and added in CTA order by a second kernel,
-// so the results do not change from run to run.
+// Floor: da, dH, y, h are read and dx, dy written once (12 D bytes a kept row in
+// bf16, 10 D with 8-bit y and h) beside the zeros.  What bounds it is the
+// instructions of a row at 16 warps an SM (0.45 issued a cycle and scheduler): at
+// 4 x 2048 tokens of 2048 values, 40% filtered, the whole call takes 38.3 us,
+// 3.9 TB/s of the floor's bytes.  On the way there: both row sums taken one after
+// the other 65 us (a row waited twice for the group), all sums at once and two
+// rows in flight 52, tensors kept in registers from a row's sums to its gradients
+// and no question asked in the row loop 42, the pre norm's weight in registers 38.
+// Each thread owns the same columns of every row it sees and keeps their
+// parameter sums in registers; a CTA's sums are parked in the workspace and added
+// in CTA order by a second kernel, so the results do not change from run to run.
 #include <algorithm>
 
 #include "join.cuh"
@@ -31,7 +35,7 @@ namespace {
 constexpr int kSrcSame = 2;   // y and h as stored (else kQ8E4m3, kQ8Int8)
 // column sums
 enum { kPreW, kPostW, kGate, kResW, kPreB, kPostB, kSums };
-constexpr uint32_t kHeadBytes = 32;   // of a stage
+constexpr uint32_t kHeadBytes = 32;   // a warp's copy of a row's token and statistics
 
 struct BwdArgs {
   int M, T, B, D;
@@ -54,6 +58,9 @@ struct BwdArgs {
   int tpr, groups, stages;
   uint32_t stage_bytes, ring_at;
 };
+
+// a stage's exponent bytes: two a vector, rounded up to whole 16s
+__host__ __device__ constexpr uint32_t exps_bytes(int tpr, int vpt) { return (tpr * vpt * 2 + 15) / 16 * 16; }
 
 __device__ __forceinline__ int kept(const BwdArgs& p) { return p.nk ? min(max(*p.nk, 0), p.M) : p.M; }
 // CTAs that have rows: each at least one
@@ -88,22 +95,14 @@ __device__ __forceinline__ Vec8 saved8(const void* p, unsigned e) {
   }
 }
 
-template <typename T, bool LN, int SRC, int VPT, bool RES, int MINB>
-__global__ void __launch_bounds__(kThreads, MINB) join_bwd_kernel(BwdArgs p, DevStatus* st) {
+template <typename T, bool LN, int SRC, int VPT, bool RES>
+__global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus* st) {
   extern __shared__ __align__(128) uint8_t smem[];
   const Place pl(p.tpr);
   float* red = reinterpret_cast<float*>(smem + pl.group * kRedBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.groups * kRedBytes) + pl.group * kMaxStages;
-  volatile int* abort_flag =
-      reinterpret_cast<volatile int*>(smem + p.groups * (kRedBytes + kMaxStages * sizeof(uint64_t)));
   uint8_t* ring = smem + p.ring_at + (size_t)pl.group * p.stages * p.stage_bytes;
-  const uint32_t bar0 = tc::smem_u32(bars), ring0 = tc::smem_u32(ring);
-  if (pl.lane == 0)
-    for (int s = 0; s < p.stages; ++s) tc::mbar_init(bar0 + 8 * s, 2);   // the copies, and the head
-  for (int i = pl.lane; i < (int)(kRedBytes / 4); i += p.tpr) red[i] = 0.f;
-  if (threadIdx.x == 0) *abort_flag = 0;
-  if (threadIdx.x < 8) reinterpret_cast<uint32_t*>(smem + zero_at(p.groups))[threadIdx.x] = 0;
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  const uint32_t ring0 = tc::smem_u32(ring);
+  for (int i = threadIdx.x; i < (int)(head_bytes(p.groups) / 4); i += blockDim.x) reinterpret_cast<uint32_t*>(smem)[i] = 0;
   __syncthreads();
 
   const T *da = static_cast<const T*>(p.da), *dh = static_cast<const T*>(p.dh), *x = static_cast<const T*>(p.x);
@@ -111,10 +110,14 @@ __global__ void __launch_bounds__(kThreads, MINB) join_bwd_kernel(BwdArgs p, Dev
   T *dx = static_cast<T*>(p.dx), *dy = static_cast<T*>(p.dy);
   const int vecs = p.D / 8;
   const int nk = kept(p);
-  const uint32_t row_bytes = p.D * (uint32_t)sizeof(T), src_bytes = SRC == kSrcSame ? row_bytes : (uint32_t)p.D;
-  // a stage: da | dH | h | y | x, those there are
-  const uint32_t o_dh = da ? row_bytes : 0, o_h = o_dh + (dh ? row_bytes : 0), o_y = o_h + (h ? src_bytes : 0),
-                 o_x = o_y + (y ? src_bytes : 0), total = o_x + (x ? row_bytes : 0);
+  // a stage: each warp's copy of the row's token and statistics, each thread's of
+  // its exponent bytes of h and y, then da | dH | h | y (| x), each with a place
+  // for every thread.  Places that no copy reaches (beyond the row, tensors not
+  // given) hold zeros, which is what their values are, so that the row loop
+  // reads and adds without asking.
+  const uint32_t heads = pl.warps * kHeadBytes + (SRC == kSrcSame ? 0 : exps_bytes(p.tpr, VPT));
+  const uint32_t place = p.tpr * VPT * 8 * (uint32_t)sizeof(T), s_place = SRC == kSrcSame ? place : p.tpr * VPT * 8;
+  const uint32_t o_da = heads, o_dh = o_da + place, o_h = o_dh + place, o_y = o_h + s_place, o_x = o_y + s_place;
   // Rows of this group: first, first + step, ... below r1.  Strided over the
   // grid, or, where gates differ by sequence, from a contiguous share of the
   // rows, so that a CTA sees few sequences.
@@ -124,59 +127,120 @@ __global__ void __launch_bounds__(kThreads, MINB) join_bwd_kernel(BwdArgs p, Dev
   const int r0 = by_seq && mine ? (int)((long long)blockIdx.x * nk / A) : blockIdx.x * p.groups,
             r1 = !mine ? 0 : by_seq ? (int)((long long)(blockIdx.x + 1) * nk / A) : nk;
   const int step = by_seq ? p.groups : gridDim.x * p.groups, first = r0 + pl.group;
-  // A stage of the ring: the row's token and statistics, then its tensors.
-  // Lane s of the group's first warp fills stage s, so that the first rows'
-  // indices and statistics are fetched side by side; later it fetches the next
-  // row's index when it fills the stage, and that row's statistics a row later.
   struct Head {
-    int token;   // -1: an index outside the tokens
     float rh, ry, mh, my;
+    int token;   // -1: an index outside the tokens
   };
   static_assert(sizeof(Head) <= kHeadBytes, "");
-  auto token = [&](int r) {
+  // The tokens of rows j = 32 n .. 32 n + 31 of this group, one a lane: the block
+  // that is being filled, and the one after it.
+  auto tokens = [&](int n) {
+    const long long r = first + (32ll * n + (pl.lane & 31)) * step;
     if (r >= r1) return -1;
-    const int t = p.idx ? p.idx[r] : r;
+    const int t = p.idx ? p.idx[r] : (int)r;
     return (unsigned)t < (unsigned)p.M ? t : -1;
   };
-  auto head = [&](int t) {
-    Head q{t, 1.f, 1.f, 0.f, 0.f};
-    if (t >= 0) {
-      if (p.pre) q.rh = p.rstd_h[t];
-      if (p.post) q.ry = p.rstd_y[t];
-      if (LN && p.pre) q.mh = p.mean_h[t];
-      if (LN && p.post) q.my = p.mean_y[t];
+  int block = 0, t_now = tokens(0), t_after = tokens(1);
+  auto token = [&](int j) {   // of row j >= 32 block, in order
+    if ((j >> 5) != block) {
+      block = j >> 5;
+      t_now = t_after;
+      t_after = tokens(block + 1);
     }
-    return q;
+    return __shfl_sync(0xffffffffu, t_now, j & 31);
   };
-  auto fill = [&](int r, int t, int s) {
-    const uint32_t b = bar0 + 8 * s, d = ring0 + s * p.stage_bytes + kHeadBytes;
-    const long long tt = t < 0 ? 0 : t, sr = p.saved_full ? tt : r, ir = p.in_full ? tt : r;
-    tc::mbar_expect_tx(b, total);
-    if (da) copy_row(d, da + ir * p.a_ld, row_bytes, b);
-    if (dh) copy_row(d + o_dh, dh + ir * p.h_ld, row_bytes, b);
-    if (h) copy_row(d + o_h, h + sr * p.hs_ld, src_bytes, b);
-    if (y) copy_row(d + o_y, y + sr * p.ys_ld, src_bytes, b);
-    if (x) copy_row(d + o_x, x + sr * p.x_ld, row_bytes, b);
+  const uint32_t off = pl.lane * 8 * (uint32_t)sizeof(T), hop = p.tpr * 8 * (uint32_t)sizeof(T);
+  const uint32_t s_off = SRC == kSrcSame ? off : pl.lane * 8, s_hop = SRC == kSrcSame ? hop : p.tpr * 8;
+  const uint32_t my_head = (pl.lane >> 5) * kHeadBytes;
+  // Exponent bytes are loaded when their row is filled, and put where its
+  // columns are a row later: e_h, e_y are on their way to stage e_stage.
+  unsigned e_h[VPT] = {}, e_y[VPT] = {};
+  int e_stage = -1;
+  uint8_t* my_exps = ring + pl.warps * kHeadBytes + pl.lane * 2 * VPT;
+  auto land_exps = [&] {
+    if constexpr (SRC != kSrcSame) {
+      if (e_stage < 0) return;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        my_exps[e_stage * p.stage_bytes + 2 * k] = (uint8_t)e_h[k];
+        my_exps[e_stage * p.stage_bytes + 2 * k + 1] = (uint8_t)e_y[k];
+      }
+      e_stage = -1;
+    }
   };
-  auto set_head = [&](const Head& q, int s) {   // (the arrival makes it visible to who waits)
-    *reinterpret_cast<Head*>(ring + s * p.stage_bytes) = q;
-    tc::mbar_arrive(bar0 + 8 * s);
+  // row j of this group, if there is one, into stage s: this thread's columns,
+  // and a few lanes of each warp its statistics
+  auto fill = [&](int j, int s) {
+    const int t = token(j);
+    const long long r = first + (long long)j * step;
+    if (r < r1) {
+      const uint32_t d = ring0 + s * p.stage_bytes;
+      const int lane = pl.lane & 31;
+      if (lane == 0) reinterpret_cast<Head*>(ring + s * p.stage_bytes + my_head)->token = t;
+      if (t >= 0) {
+        if (lane == 0 && p.pre) copy4(d + my_head, p.rstd_h + t);
+        if (lane == 1 && p.post) copy4(d + my_head + 4, p.rstd_y + t);
+        if (LN && lane == 2 && p.pre) copy4(d + my_head + 8, p.mean_h + t);
+        if (LN && lane == 3 && p.post) copy4(d + my_head + 12, p.mean_y + t);
+        const long long sr = p.saved_full ? t : r, ir = p.in_full ? t : r;
+        const T *s_da = da + ir * p.a_ld + 8 * pl.lane, *s_dh = dh + ir * p.h_ld + 8 * pl.lane,
+                *s_x = x + sr * p.x_ld + 8 * pl.lane;
+        const uint8_t *s_h = h + sr * p.hs_ld + s_off, *s_y = y + sr * p.ys_ld + s_off;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          const int v = pl.lane + k * p.tpr;
+          if (v >= vecs) continue;
+          if (da) copy_vec(d + o_da + off + k * hop, s_da + k * p.tpr * 8);
+          if (dh) copy_vec(d + o_dh + off + k * hop, s_dh + k * p.tpr * 8);
+          if (RES && x) copy_vec(d + o_x + off + k * hop, s_x + k * p.tpr * 8);
+          if constexpr (SRC == kSrcSame) {
+            if (h) copy_vec(d + o_h + off + k * hop, reinterpret_cast<const T*>(s_h) + k * p.tpr * 8);
+            if (y) copy_vec(d + o_y + off + k * hop, reinterpret_cast<const T*>(s_y) + k * p.tpr * 8);
+          } else {
+            if (h) copy8(d + o_h + s_off + k * s_hop, s_h + k * s_hop);
+            if (y) copy8(d + o_y + s_off + k * s_hop, s_y + k * s_hop);
+            e_h[k] = h ? p.h_exps[sr * p.he_ld + (v >> 2)] : 0;
+            e_y[k] = y ? p.y_exps[sr * p.ye_ld + (v >> 2)] : 0;
+          }
+        }
+        e_stage = s;
+      }
+    }
+    copy_commit();
   };
-  // the finishing kernel may be scheduled as blocks of this one exit
+  // the sums' kernel may be scheduled as blocks of this one exit
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Head ahead{};          // lane s: of the row that stage s takes next
-  if (pl.lane < p.stages) {
-    const int r = first + pl.lane * step;
-    const int t = token(r), ta = token(r + p.stages * step);
-    if (r < r1) fill(r, t, pl.lane);
-    const Head q = head(t);
-    ahead = head(ta);
-    if (r < r1) set_head(q, pl.lane);
+  if (!da || !dh || !y || (RES && !x) || vecs < p.tpr * VPT) {
+    for (uint32_t i = threadIdx.x; i < p.groups * p.stages * (p.stage_bytes / 16); i += blockDim.x)
+      reinterpret_cast<uint4*>(smem + p.ring_at)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
+  if ((pl.lane & 31) == 0)   // statistics that are not read: 1, and 0
+    for (int j = 0; j < p.stages; ++j)
+      *reinterpret_cast<Head*>(ring + j * p.stage_bytes + my_head) = Head{1.f, 1.f, 0.f, 0.f, -1};
+  __syncwarp();
+  for (int j = 0; j < p.stages; ++j) {
+    land_exps();
+    fill(j, j);
+  }
+  // While the first rows are on their way: zeros where there is no kept row, the
+  // filtered tokens of FULL outputs or the padding of COMPACT ones, a warp a row.
+  {
+    const int zeros = p.out_full ? p.M - nk : padded_rows(nk, p.M) - nk, lane = threadIdx.x & 31;
+    const int wpb = blockDim.x >> 5;
+    for (int j = blockIdx.x * wpb + (threadIdx.x >> 5); j < zeros; j += gridDim.x * wpb) {
+      const long long row = p.out_full ? filtered_token(p.idx, nk, j) : nk + j;
+      for (int v = lane; v < vecs; v += 32) {
+        put8(dx + row * p.x_ld + 8 * v, all8(0.f));
+        if (p.branch) put8(dy + row * p.y_ld + 8 * v, all8(0.f));
+      }
+    }
   }
 
   // Column sums over this group's rows: of da hh, da (LN), and -- of one
   // sequence while gates differ by sequence -- of dh yh, dh (LN); of dh x.
   constexpr int VL = LN ? VPT : 1, VR = RES ? VPT : 1;
+  constexpr int NS = LN ? 16 : 4;   // sums a row (10 of them used with LayerNorm)
   Vec8 s_pre[VPT], s_da[VL], s_dhy[VPT], s_dh[VL], s_res[VR];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
@@ -206,12 +270,6 @@ __global__ void __launch_bounds__(kThreads, MINB) join_bwd_kernel(BwdArgs p, Dev
     }
   };
   set_gate();
-#pragma unroll
-  for (int k = 0; k < VPT; ++k)   // read first in the row loop
-    if (pl.lane + k * p.tpr < vecs) {
-      prefetch_l1(static_cast<const T*>(p.pre_w) + 8 * (pl.lane + k * p.tpr), p.pre != 0);
-      prefetch_l1(static_cast<const T*>(p.res_w) + 8 * (pl.lane + k * p.tpr), RES);
-    }
   // A sequence's sums become the gradient of its gate, dgate = gamma s_dhy +
   // beta s_dh, and its share of the post norm's gradients, gate s_dhy and gate
   // s_dh.  Of several sequences the shares gather in u, this thread's own line
@@ -246,236 +304,145 @@ __global__ void __launch_bounds__(kThreads, MINB) join_bwd_kernel(BwdArgs p, Dev
 #pragma unroll
     for (int i = 0; i < (LN ? 2 : 1) * VPT; ++i) u[i] = all8(0.f);
 
-  // threads beyond the row read zeros
-  const uint8_t* zero = smem + zero_at(p.groups);
-  const uint32_t off = pl.lane * 8 * (uint32_t)sizeof(T), hop = p.tpr * 8 * (uint32_t)sizeof(T);
-  const uint32_t s_off = SRC == kSrcSame ? off : pl.lane * 8, s_hop = SRC == kSrcSame ? hop : p.tpr * 8;
-  // 8-bit y and h: this thread's exponent bytes, a row ahead
-  struct Exps {
-    unsigned h[VPT], y[VPT];
-  };
-  auto exps = [&](int r, int t) {
-    Exps q;
+  Raw8<T> w_pre[VPT];   // this thread's part of the pre norm's weight (0 where there is none), as stored
+  const T* w_res[VR];   // and its places of res_w
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      q.h[k] = q.y[k] = 0;
-      const int v = pl.lane + k * p.tpr;
-      if (SRC != kSrcSame && t >= 0 && v < vecs) {
-        const long long sr = p.saved_full ? t : r;
-        if (h) q.h[k] = p.h_exps[sr * p.he_ld + (v >> 2)];
-        if (y) q.y[k] = p.y_exps[sr * p.ye_ld + (v >> 2)];
-      }
-    }
-    return q;
-  };
-  int tok_next = SRC == kSrcSame ? 0 : token(first + step);
-  Exps now = exps(first, SRC == kSrcSame ? 0 : token(first));
+  for (int k = 0; k < VPT; ++k) {
+    const int v = pl.lane + k * p.tpr;
+    const T* zero = reinterpret_cast<const T*>(smem + zero_at(p.groups));
+    w_pre[k] = *reinterpret_cast<const Raw8<T>*>(p.pre && v < vecs ? static_cast<const T*>(p.pre_w) + 8 * v : zero);
+    if (RES) w_res[RES ? k : 0] = v < vecs ? static_cast<const T*>(p.res_w) + 8 * v : zero;
+  }
 
-  int half = 0, s = 0, prev = -1;
-  uint32_t parity = 0;
+  // The rows, two at a time: while row i's sums travel through the group, row
+  // i - 1's, which every thread can read by then, become its gradients; so one
+  // barrier a row, which nothing waits for at once.  Of row i - 1 a thread keeps
+  // t = gamma da, hh, yh and dH.
   const f2 al = both(p.alpha);
-  for (int r = first; r < r1; r += step) {
-    Exps next;
-    if (SRC != kSrcSame) {
-      next = exps(r + step, tok_next);
-      tok_next = token(r + 2 * step);
-    }
-    tc::mbar_wait(bar0 + 8 * s, (parity >> s) & 1u, abort_flag, st, 720);
-    parity ^= 1u << s;
-    const uint8_t* stage = ring + s * p.stage_bytes + kHeadBytes;
-    const Head hd = *reinterpret_cast<const Head*>(ring + s * p.stage_bytes);
-    // Once every thread has reached this row the stage before it is free for a
-    // row further on: after this row's first sum over the group, or a barrier.
-    // (A ring of one stage has no such stage: it is filled when the row is done.)
-    auto refill = [&] {
-      if (prev >= 0 && pl.lane < p.stages && p.stages > 1) {
-        if (pl.lane == prev) {
-          const int rn = r + (p.stages - 1) * step;
-          if (rn < r1) {
-            fill(rn, ahead.token, prev);
-            set_head(ahead, prev);
-          }
-          ahead.token = token(rn + p.stages * step);
-        }
-        if (pl.lane == (prev == 0 ? p.stages - 1 : prev - 1)) ahead = head(ahead.token);
+  Vec8 t[VPT], hh[VPT], yh[VPT], d[VPT];
+  f2 rh = both(1.f), ry = rh;
+  int s = 0, prev = 0;    // stages of rows i and i - 1
+  int old_token = -1;     // of row i - 1, -1: there is none to finish
+  for (int r = first, i = 0; r - step < r1; r += step, ++i) {
+    if (old_token >= 0) {
+      // row i - 1: its sums, dh, dx, dy and the columns' sums
+      float q[NS];
+      take_sums(pl, red + ((i - 1) & 1) * kMaxSums * kMaxWarps, q);
+      const float n1 = -q[0] * p.inv_d;   // -mean(t hh)
+      const float n0 = LN ? -q[LN ? 4 : 0] * p.inv_d : 0.f;   // -mean(t)
+      // -mean(w yh) and -mean(w), w = c1 dh = c1 (dH + r_h (t + hh n1 + n0))
+      float o1 = fmaf(n1, q[3], q[2]), o0 = 0.f;
+      if (LN) {
+        o1 = fmaf(n0, q[LN ? 5 : 0], o1);
+        o0 = fmaf(n0, q[LN ? 9 : 0], fmaf(n1, q[LN ? 8 : 0], q[LN ? 7 : 0]));
+        o0 = -fmaf(rh.x, o0, q[LN ? 6 : 0]) * p.inv_d;
       }
-      prev = s;
-      if (++s == p.stages) s = 0;
-    };
-    auto row_done = [&] {
-      now = next;
-      if (p.stages > 1) return;
-      pl.sync();
-      if (pl.lane == 0) {
-        if (r + step < r1) {
-          fill(r + step, ahead.token, 0);
-          set_head(ahead, 0);
-        }
-        ahead = head(token(r + 2 * step));
-      }
-    };
-    if (hd.token < 0 || !(p.pre || p.post)) {
-      pl.sync();
-      refill();
-    }
-    if (hd.token < 0) {   // (the same in every thread of the group)
-      if (pl.lane == 0) report_error(st, kErrBadIndex, 721);
-      row_done();
-      continue;
-    }
-    while (r >= b_end && b < b_last) end_sequence(false);
-    const long long orow = p.out_full ? hd.token : r;
-    const f2 rh = both(hd.rh), ry = both(hd.ry), mh = both(-hd.mh), my = both(-hd.my);
-    // the row's vectors (read from the stage whenever they are used, which
-    // keeps few registers), normalised where they have a norm
-    auto on = [&](int k) { return pl.lane + k * p.tpr < vecs; };
-    auto at_da = [&](int k) { return get8<T>(on(k) ? stage + off + k * hop : zero); };
-    auto at_dh = [&](int k) { return get8<T>(on(k) && dh ? stage + o_dh + off + k * hop : zero); };
-    auto at_h = [&](int k) {
-      Vec8 v = saved8<T, SRC>(on(k) ? stage + o_h + s_off + k * s_hop : zero, now.h[k]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v.v[i] = mul2(LN ? add2(v.v[i], mh) : v.v[i], rh);
-      return v;
-    };
-    auto at_y = [&](int k) {
-      Vec8 v = saved8<T, SRC>(on(k) ? stage + o_y + s_off + k * s_hop : zero, now.y[k]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v.v[i] = mul2(LN ? add2(v.v[i], my) : v.v[i], ry);
-      return v;
-    };
-    auto pre_w = [&](int k) { return param8<T>(p.pre_w, pl.lane + k * p.tpr, on(k), 0.f); };
-
-    // Sums over the row.  RMSNorm takes them all at once: with m1 = mean(t hh),
-    //   sum(w yh) = sum(c1 yh dH) + r_h (sum(c1 yh t) - m1 sum(c1 yh hh)),
-    // so that the post norm's sum need not wait for dh.  LayerNorm, which would
-    // need ten sums, takes the pre norm's first.
-    float n1 = 0.f, n0 = 0.f, o1 = 0.f;   // -mean(t hh), -mean(t), -mean(w yh)
-    if (!LN) {
-      f2 q0 = both(0.f), q1 = both(0.f), q2 = both(0.f), q3 = both(0.f);
+      o1 = -fmaf(rh.x, o1, q[1]) * p.inv_d;
+      if (!p.post) o1 = o0 = 0.f;
+      const long long orow = p.out_full ? old_token : r - step;
+      T* rowx = dx + orow * p.x_ld + 8 * pl.lane;
+      T* rowy = dy + orow * p.y_ld + 8 * pl.lane;
+      const f2 n1b = both(n1), n0b = both(n0), o1b = both(o1), o0b = both(o0);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        Vec8 t = all8(0.f), hh = all8(0.f);
-        if (p.pre) {
-          t = at_da(k);
-          hh = at_h(k);
-          const Vec8 w = pre_w(k);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s_pre[k].v[i] = fma2(t.v[i], hh.v[i], s_pre[k].v[i]);
-            t.v[i] = mul2(t.v[i], w.v[i]);
-            q0 = fma2(t.v[i], hh.v[i], q0);
-          }
-        }
-        if (p.post) {
-          const Vec8 yh = at_y(k), d = at_dh(k);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f2 cy = mul2(c1[k].v[i], yh.v[i]);
-            q1 = fma2(cy, d.v[i], q1);
-            q2 = fma2(cy, t.v[i], q2);
-            q3 = fma2(cy, hh.v[i], q3);
-          }
-        }
-      }
-      if (p.pre || p.post) {
-        float q[4] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y, q3.x + q3.y};
-        group_sum(pl, red, half, q);
-        refill();
-        n1 = -q[0] * p.inv_d;
-        o1 = -fmaf(hd.rh, fmaf(n1, q[3], q[2]), q[1]) * p.inv_d;
-      }
-    } else if (p.pre) {
-      f2 q1 = both(0.f), q0 = both(0.f);
-#pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        Vec8 t = at_da(k);
-        const Vec8 hh = at_h(k), w = pre_w(k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s_pre[k].v[i] = fma2(t.v[i], hh.v[i], s_pre[k].v[i]);
-          s_da[LN ? k : 0].v[i] = add2(s_da[LN ? k : 0].v[i], t.v[i]);
-          t.v[i] = mul2(t.v[i], w.v[i]);
-          q1 = fma2(t.v[i], hh.v[i], q1);
-          q0 = add2(q0, t.v[i]);
-        }
-      }
-      float q[2] = {q1.x + q1.y, q0.x + q0.y};
-      group_sum(pl, red, half, q);
-      refill();
-      n1 = -q[0] * p.inv_d;
-      n0 = -q[1] * p.inv_d;
-    }
-
-    // dh, dx and the sums of dh; dy at once (RMSNorm) or after its sums
-    T* rowx = dx + orow * p.x_ld + 8 * pl.lane;
-    T* rowy = dy + orow * p.y_ld + 8 * pl.lane;
-    const f2 n1b = both(n1), n0b = both(n0);
-    f2 q1 = both(0.f), q0 = both(0.f);
-    Vec8 w2[VL];   // LayerNorm: c1 dh
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      Vec8 d = at_dh(k);
-      if (p.pre) {
-        const Vec8 t = at_da(k), hh = at_h(k), w = pre_w(k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f2 g = LN ? fma2(t.v[i], w.v[i], fma2(hh.v[i], n1b, n0b)) : fma2(t.v[i], w.v[i], mul2(hh.v[i], n1b));
-          d.v[i] = fma2(rh, g, d.v[i]);
-        }
-      }
-      Vec8 o;
-      if (RES) {
-        const Vec8 l = param8<T>(p.res_w, pl.lane + k * p.tpr, on(k), 0.f);
-        const Vec8 xv = get8<T>(on(k) && x ? stage + o_x + off + k * hop : zero);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o.v[i] = mul2(d.v[i], mul2(al, l.v[i]));
-          s_res[RES ? k : 0].v[i] = fma2(d.v[i], xv.v[i], s_res[RES ? k : 0].v[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o.v[i] = mul2(d.v[i], al);
-      }
-      if (on(k)) put8(rowx + k * p.tpr * 8, o);
-      if (!p.branch) continue;
-      // (beyond the row dh and yh need not be 0 with LayerNorm; c1 is, so the
-      // row's sums get nothing from there, and those columns are never stored)
-      const Vec8 yh = at_y(k);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s_dhy[k].v[i] = fma2(d.v[i], yh.v[i], s_dhy[k].v[i]);
-        const f2 w = mul2(c1[k].v[i], d.v[i]);
-        if (LN) {
-          s_dh[LN ? k : 0].v[i] = add2(s_dh[LN ? k : 0].v[i], d.v[i]);
-          q1 = fma2(w, yh.v[i], q1);
-          q0 = add2(q0, w);
-          w2[LN ? k : 0].v[i] = w;
-        } else {
-          o.v[i] = mul2(ry, fma2(yh.v[i], both(o1), w));
-        }
-      }
-      if (!LN && on(k)) put8(rowy + k * p.tpr * 8, o);
-    }
-    if (LN && p.branch) {
-      float m1 = 0.f, m0 = 0.f;
-      if (p.post) {
-        float q[2] = {q1.x + q1.y, q0.x + q0.y};
-        group_sum(pl, red, half, q);
-        if (!p.pre) refill();
-        m1 = -q[0] * p.inv_d;
-        m0 = -q[1] * p.inv_d;
-      }
-#pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        const Vec8 yh = at_y(k);
+        const bool on = pl.lane + k * p.tpr < vecs;
         Vec8 o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o.v[i] = mul2(ry, fma2(yh.v[i], both(m1), add2(w2[LN ? k : 0].v[i], both(m0))));
-        if (on(k)) put8(rowy + k * p.tpr * 8, o);
+        for (int j = 0; j < 4; ++j) {
+          const f2 u = LN ? add2(fma2(hh[k].v[j], n1b, n0b), t[k].v[j]) : fma2(hh[k].v[j], n1b, t[k].v[j]);
+          d[k].v[j] = fma2(rh, u, d[k].v[j]);
+        }
+        if (RES) {
+          const Vec8 l = get8<T>(w_res[RES ? k : 0]);
+          const Vec8 xv = get8<T>(ring + prev * p.stage_bytes + o_x + off + k * hop);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o.v[j] = mul2(d[k].v[j], mul2(al, l.v[j]));
+            s_res[RES ? k : 0].v[j] = fma2(d[k].v[j], xv.v[j], s_res[RES ? k : 0].v[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o.v[j] = mul2(d[k].v[j], al);
+        }
+        if (on) put8(rowx + k * p.tpr * 8, o);
+        // (beyond the row dh and yh need not be 0 with LayerNorm; those columns are never stored)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s_dhy[k].v[j] = fma2(d[k].v[j], yh[k].v[j], s_dhy[k].v[j]);
+          if (LN) s_dh[LN ? k : 0].v[j] = add2(s_dh[LN ? k : 0].v[j], d[k].v[j]);
+          const f2 c = mul2(c1[k].v[j], d[k].v[j]);
+          o.v[j] = mul2(ry, LN ? add2(fma2(yh[k].v[j], o1b, o0b), c) : fma2(yh[k].v[j], o1b, c));
+        }
+        if (on && p.branch) put8(rowy + k * p.tpr * 8, o);
       }
     }
-    row_done();
+    // row i - 1's stage takes the row `stages` further on, once the warp is done with it
+    __syncwarp();
+    land_exps();
+    if (i > 0) {
+      fill(i - 1 + p.stages, prev);
+      if (p.stages == 1) land_exps();
+    } else {
+      copy_commit();
+    }
+    if (r < r1) {
+      while (r >= b_end && b < b_last) end_sequence(false);
+      copy_wait(p.stages - 1);
+      __syncwarp();   // the head was copied by a few lanes
+      const uint8_t* at = ring + s * p.stage_bytes;
+      const Head hd = *reinterpret_cast<const Head*>(at + my_head);
+      old_token = hd.token;
+      if (old_token < 0) {   // (the same in every thread of the group)
+        if (pl.lane == 0) report_error(st, kErrBadIndex, 721);
+      } else {
+        // Row i's sums, all at once: with m1 = mean(t hh) (and m0 = mean(t)),
+        //   sum(w yh) = sum(c1 yh dH) + r_h (sum(c1 yh t) - m1 sum(c1 yh hh) - m0 sum(c1 yh)),
+        // and sum(w) the same without yh, so that the post norm's sums need not wait for dh.
+        rh = both(hd.rh);
+        ry = both(hd.ry);
+        const f2 mh = both(-hd.mh), my = both(-hd.my);
+        const uint8_t* e = my_exps + s * p.stage_bytes;
+        f2 q[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) q[j] = both(0.f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          t[k] = get8<T>(at + o_da + off + k * hop);
+          hh[k] = saved8<T, SRC>(at + o_h + s_off + k * s_hop, SRC == kSrcSame ? 0 : e[2 * k]);
+          yh[k] = saved8<T, SRC>(at + o_y + s_off + k * s_hop, SRC == kSrcSame ? 0 : e[2 * k + 1]);
+          d[k] = get8<T>(at + o_dh + off + k * hop);
+          const Vec8 g = get8<T>(&w_pre[k]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            hh[k].v[j] = mul2(LN ? add2(hh[k].v[j], mh) : hh[k].v[j], rh);
+            yh[k].v[j] = mul2(LN ? add2(yh[k].v[j], my) : yh[k].v[j], ry);
+            s_pre[k].v[j] = fma2(t[k].v[j], hh[k].v[j], s_pre[k].v[j]);
+            if (LN) s_da[LN ? k : 0].v[j] = add2(s_da[LN ? k : 0].v[j], t[k].v[j]);
+            t[k].v[j] = mul2(t[k].v[j], g.v[j]);
+            const f2 c = c1[k].v[j], cy = mul2(c, yh[k].v[j]);
+            q[0] = fma2(t[k].v[j], hh[k].v[j], q[0]);
+            q[1] = fma2(cy, d[k].v[j], q[1]);
+            q[2] = fma2(cy, t[k].v[j], q[2]);
+            q[3] = fma2(cy, hh[k].v[j], q[3]);
+            if (LN) {
+              q[LN ? 4 : 0] = add2(q[LN ? 4 : 0], t[k].v[j]);
+              q[LN ? 5 : 0] = add2(q[LN ? 5 : 0], cy);
+              q[LN ? 6 : 0] = fma2(c, d[k].v[j], q[LN ? 6 : 0]);
+              q[LN ? 7 : 0] = fma2(c, t[k].v[j], q[LN ? 7 : 0]);
+              q[LN ? 8 : 0] = fma2(c, hh[k].v[j], q[LN ? 8 : 0]);
+              q[LN ? 9 : 0] = add2(q[LN ? 9 : 0], c);
+            }
+          }
+        }
+        float v[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) v[j] = q[j].x + q[j].y;
+        leave_sums(pl, red + (i & 1) * kMaxSums * kMaxWarps, v);
+      }
+    }
+    pl.sync();   // row i's sums are left
+    prev = s;
+    if (++s == p.stages) s = 0;
   }
 
   // the column sums: gates of sequences by group (above), the others over the CTA's groups
@@ -483,9 +450,8 @@ __global__ void __launch_bounds__(kThreads, MINB) join_bwd_kernel(BwdArgs p, Dev
     while (b < b_last) end_sequence(false);
     end_sequence(true);
   }
+  if (!mine) return;
   __syncthreads();
-  if (*abort_flag && pl.lane == 0) drain(bar0, p.stages, parity);
-  if (!mine || *abort_flag) return;
   float* line = reinterpret_cast<float*>(smem + p.ring_at);   // the rings are done with
   auto park = [&](int q, auto&& value) {
     if (!p.sums[q]) return;
@@ -532,31 +498,14 @@ __global__ void __launch_bounds__(kThreads, MINB) join_bwd_kernel(BwdArgs p, Dev
   }
 }
 
-// After the rows: zeros where there is no kept row (the first zero_ctas blocks
-// of y), and sums[q][c] = the parked sums added in slot order, 32 columns a
-// block, 32 threads a column, each every 32nd slot, then the 32 in order.
-// blockIdx.y counts the gradients there are, a gate by sequences as B of them.
-// The zero blocks touch only rows that the first kernel does not.
-template <typename T>
-__global__ void __launch_bounds__(1024) join_finish_kernel(BwdArgs p, int zero_ctas) {
+// sums[q][c] = the parked sums added in slot order: 32 columns a block, 32
+// threads a column, each every 32nd slot, then the 32 in order.  blockIdx.y
+// counts the gradients there are, a gate by sequences as B of them.
+__global__ void __launch_bounds__(1024) join_sums_kernel(BwdArgs p) {
   __shared__ float red[32][33];
-  const int nk = kept(p);
-  if ((int)blockIdx.y < zero_ctas) {
-    T *dx = static_cast<T*>(p.dx), *dy = static_cast<T*>(p.dy);
-    const int zeros = p.out_full ? p.M - nk : padded_rows(nk, p.M) - nk, vecs = p.D / 8;
-    const int warps = gridDim.x * zero_ctas * 32, lane = threadIdx.x & 31;
-    for (int j = (blockIdx.y * gridDim.x + blockIdx.x) * 32 + (threadIdx.x >> 5); j < zeros; j += warps) {
-      const long long row = p.out_full ? filtered_token(p.idx, nk, j) : nk + j;
-      for (int v = lane; v < vecs; v += 32) {
-        put8(dx + row * p.x_ld + 8 * v, all8(0.f));
-        if (p.branch) put8(dy + row * p.y_ld + 8 * v, all8(0.f));
-      }
-    }
-    grid_dep_wait();
-    return;
-  }
   grid_dep_wait();
-  int q = 0, b = blockIdx.y - zero_ctas;
+  const int nk = kept(p);
+  int q = 0, b = blockIdx.y;
   for (;; ++q) {
     const int n = !p.sums[q] ? 0 : (q == kGate && p.gate_rows > 1) ? p.B : 1;
     if (b < n) break;
@@ -593,8 +542,7 @@ constexpr int kMaxSms = 256;
 
 template <typename T, bool LN, int SRC, int VPT, bool RES>
 cudaError_t launch(const Ctx& c, const BwdArgs& p, size_t smem) {
-  constexpr int MINB = VPT <= 2 ? 2 : 1;
-  auto k = join_bwd_kernel<T, LN, SRC, VPT, RES, MINB>;
+  auto k = join_bwd_kernel<T, LN, SRC, VPT, RES>;
   static size_t granted[64];   // shared memory opted in to, a device
   const cudaError_t e = grant_smem(reinterpret_cast<const void*>(k), smem, granted);
   if (e != cudaSuccess) return e;
@@ -603,9 +551,7 @@ cudaError_t launch(const Ctx& c, const BwdArgs& p, size_t smem) {
 }
 template <typename T, bool LN, int SRC, bool RES>
 cudaError_t by_vpt(const Ctx& c, const BwdArgs& p, int vpt, size_t smem) {
-  return vpt == 1   ? launch<T, LN, SRC, 1, RES>(c, p, smem)
-         : vpt == 2 ? launch<T, LN, SRC, 2, RES>(c, p, smem)
-                    : launch<T, LN, SRC, 4, RES>(c, p, smem);
+  return vpt == 1 ? launch<T, LN, SRC, 1, RES>(c, p, smem) : launch<T, LN, SRC, 2, RES>(c, p, smem);
 }
 template <typename T, bool LN, int SRC>
 cudaError_t by_res(const Ctx& c, const BwdArgs& p, int vpt, size_t smem) {
@@ -619,30 +565,27 @@ cudaError_t by_src(const Ctx& c, const BwdArgs& p, int src, int vpt, size_t smem
   return by_res<T, LN, kSrcSame>(c, p, vpt, smem);
 }
 
-// Launch shape: one vector of 8 a thread up to 2048 values, more for wider rows;
-// two CTAs an SM where two stages of each fit.
+// Launch shape: one vector of 8 a thread up to 4096 values, two for wider rows;
+// two CTAs an SM up to 2048 values (their registers leave no room for more).
 struct BwdShape {
   Shape s;
   int ctas;        // an SM
   size_t own;      // bytes of the threads' own sums (gates by sequence)
 };
-BwdShape bwd_shape(int D, uint32_t stage, bool layer_norm, bool by_seq) {
-  auto shape = [&](int vpt, int ctas) {
-    BwdShape b{};
-    b.ctas = ctas;
-    const Shape t = make_shape(D, vpt, stage, 0, 0);
-    b.own = by_seq ? (size_t)t.groups * t.tpr * vpt * 8 * 4 * (layer_norm ? 2 : 1) : 0;
-    b.s = make_shape(D, vpt, stage, b.own, (ctas == 2 ? 112 : 224) * 1024);
-    const size_t line = head_bytes(t.groups) + b.own + (t.groups > 1 ? (size_t)kSums * t.groups * D * 4 : 0);
-    if (b.s.smem < line) b.s.smem = line;
-    return b;
-  };
-  if (D > 4096) return shape(4, 1);
-  if (D > 2048) {
-    const BwdShape two = shape(2, 2);
-    return two.s.stages >= 2 ? two : shape(2, 1);
-  }
-  return shape(1, 2);
+// bytes: of the T tensors' values and of the saved ones' in a stage, a value
+BwdShape bwd_shape(int D, uint32_t bytes, bool eight, bool layer_norm, bool by_seq) {
+  BwdShape b{};
+  const int vpt = D <= 4096 ? 1 : 2;
+  b.ctas = D <= 2048 ? 2 : 1;
+  const Shape t = make_shape(D, vpt, 16, 0, 0);
+  const uint32_t stage = t.tpr * vpt * 8 * bytes + t.tpr / 32 * kHeadBytes + (eight ? exps_bytes(t.tpr, vpt) : 0);
+  b.own = by_seq ? (size_t)t.groups * t.tpr * vpt * 8 * 4 * (layer_norm ? 2 : 1) : 0;
+  // (64 KB of ring a CTA: more stages only lengthen the start.  4 x 2048 tokens of 2048 values: 42.4 us, 45.3 at 112 KB)
+  b.s = make_shape(D, vpt, stage, b.own, 64 * 1024 + b.own);
+  if (b.s.stages < 2) b.s = make_shape(D, vpt, stage, b.own, (b.ctas == 2 ? 112 : 224) * 1024);
+  const size_t line = head_bytes(t.groups) + b.own + (t.groups > 1 ? (size_t)kSums * t.groups * D * 4 : 0);
+  if (b.s.smem < line) b.s.smem = line;
+  return b;
 }
 int bwd_grid(int M, int num_sms, int groups, int ctas) {
   const long long want = ((long long)M + groups - 1) / groups, fit = (long long)std::min(num_sms, kMaxSms) * ctas;
@@ -653,7 +596,7 @@ int bwd_grid(int M, int num_sms, int groups, int ctas) {
 
 // partial sums of the widest grid on any GPU of up to kMaxSms SMs
 size_t join_bwd_part_floats(int B, int T, int D, int gate_rows) {
-  const int groups = make_shape(D, D <= 256 ? 1 : D <= 4096 ? 2 : 4, 16, 0, 0).groups;   // the most there are
+  const int groups = make_shape(D, D <= 4096 ? 1 : 2, 16, 0, 0).groups;
   const long long grid = std::min<long long>((long long)B * T, kMaxSms * 2);
   return (size_t)(grid * kSums + (gate_rows > 1 ? (grid + B) * groups : 0)) * D;
 }
@@ -677,9 +620,9 @@ cudaError_t launch_join_bwd(const Ctx& c, const JoinBwd& j) {
   p.dx = j.dx; p.dy = j.dy;
   p.sums[kPreW] = j.dpre_w; p.sums[kPreB] = j.dpre_b; p.sums[kPostW] = j.dpost_w; p.sums[kPostB] = j.dpost_b;
   p.sums[kGate] = j.dgate; p.sums[kResW] = j.dres_w;
-  const uint32_t row = (uint32_t)j.D * es, src = same ? row : (uint32_t)j.D;
-  const uint32_t total = (p.da ? row : 0) + (p.dh ? row : 0) + (p.h ? src : 0) + (p.y ? src : 0) + (p.x ? row : 0);
-  const BwdShape bs = bwd_shape(j.D, kHeadBytes + total, j.layer_norm != 0, j.gate_rows > 1);
+  // da, dH, (x), h and y
+  const uint32_t bytes = (p.res_w ? 3 : 2) * es + 2 * (same ? es : 1);
+  const BwdShape bs = bwd_shape(j.D, bytes, !same, j.layer_norm != 0, j.gate_rows > 1);
   const Shape& s = bs.s;
   p.tpr = s.tpr; p.groups = s.groups; p.stages = s.stages; p.stage_bytes = s.stage_bytes;
   p.ring_at = (uint32_t)(head_bytes(s.groups) + bs.own);
@@ -697,16 +640,9 @@ cudaError_t launch_join_bwd(const Ctx& c, const JoinBwd& j) {
   if (e != cudaSuccess) return e;
   int tasks = 0;
   for (int q = 0; q < kSums; ++q) tasks += !p.sums[q] ? 0 : (q == kGate && j.gate_rows > 1) ? j.B : 1;
-  // blocks that write zeros: a warp for each row there may be, 2 blocks an SM at most
-  const int cols = (j.D + 31) / 32;
-  const bool some = j.nk != nullptr;   // (dense: every row is kept)
-  const long long rows = some ? (j.out_full ? p.M : std::min(p.M, 127)) : 0;
-  const int zero_ctas = (int)((std::min(2LL * c.num_sms, (rows + 31) / 32) + cols - 1) / cols);
-  if (tasks + zero_ctas == 0) return cudaSuccess;
-  prof_begin(c, "residual_norm_finish");
-  const dim3 grid(cols, tasks + zero_ctas);
-  if (j.f32) e = launch_k(c, pdl_allowed(), join_finish_kernel<float>, grid, dim3(1024), 0, 1, p, zero_ctas);
-  else e = launch_k(c, pdl_allowed(), join_finish_kernel<__nv_bfloat16>, grid, dim3(1024), 0, 1, p, zero_ctas);
+  if (tasks == 0) return cudaSuccess;
+  prof_begin(c, "residual_norm_sums");
+  e = launch_k(c, pdl_allowed(), join_sums_kernel, dim3((j.D + 31) / 32, tasks), dim3(1024), 0, 1, p);
   prof_end(c);
   count_launch();
   return launched(e);

@@ -34,37 +34,35 @@ struct FwdArgs {
 };
 
 template <typename T, bool LN, int VPT>
-__global__ void __launch_bounds__(kThreads) join_fwd_kernel(FwdArgs p, DevStatus* st) {
+__global__ void __launch_bounds__(kThreads) join_fwd_kernel(FwdArgs p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const Place pl(p.tpr);
   float* red = reinterpret_cast<float*>(smem + pl.group * kRedBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.groups * kRedBytes) + pl.group * kMaxStages;
-  volatile int* abort_flag =
-      reinterpret_cast<volatile int*>(smem + p.groups * (kRedBytes + kMaxStages * sizeof(uint64_t)));
   uint8_t* ring = smem + head_bytes(p.groups) + (size_t)pl.group * p.stages * p.stage_bytes;
-  const uint32_t bar0 = tc::smem_u32(bars), ring0 = tc::smem_u32(ring);
-  if (pl.lane == 0)
-    for (int s = 0; s < p.stages; ++s) tc::mbar_init(bar0 + 8 * s, 1);
-  for (int i = pl.lane; i < (int)(kRedBytes / 4); i += p.tpr) red[i] = 0.f;
-  if (threadIdx.x == 0) *abort_flag = 0;
-  if (threadIdx.x < 8) reinterpret_cast<uint32_t*>(smem + zero_at(p.groups))[threadIdx.x] = 0;
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  const uint32_t ring0 = tc::smem_u32(ring);
+  for (int i = threadIdx.x; i < (int)(head_bytes(p.groups) / 4); i += blockDim.x) reinterpret_cast<uint32_t*>(smem)[i] = 0;
   __syncthreads();
 
   const T *x = static_cast<const T*>(p.x), *y = static_cast<const T*>(p.y);
   T *h = static_cast<T*>(p.h), *a = static_cast<T*>(p.a);
   const int vecs = p.D / 8;
-  const uint32_t row_bytes = p.D * (uint32_t)sizeof(T), total = y ? 2 * row_bytes : row_bytes;
+  const uint32_t row_bytes = p.D * (uint32_t)sizeof(T);
+  const uint32_t off = pl.lane * 8 * (uint32_t)sizeof(T), hop = p.tpr * 8 * (uint32_t)sizeof(T);
   const int step = gridDim.x * p.groups, r0 = blockIdx.x * p.groups + pl.group;
-  auto issue = [&](long long r, int s) {
-    const uint32_t b = bar0 + 8 * s, d = ring0 + s * p.stage_bytes;
-    tc::mbar_expect_tx(b, total);
-    copy_row(d, x + r * p.x_ld, row_bytes, b);
-    if (y) copy_row(d + row_bytes, y + r * p.y_ld, row_bytes, b);
+  auto fill = [&](long long r, int s) {   // this thread's columns of row r, if there is one, into stage s
+    if (r < p.M) {
+      const uint32_t d = ring0 + s * p.stage_bytes + off;
+      const T *sx = x + r * p.x_ld + 8 * pl.lane, *sy = y + r * p.y_ld + 8 * pl.lane;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+        if (pl.lane + k * p.tpr < vecs) {
+          copy_vec(d + k * hop, sx + k * p.tpr * 8);
+          if (y) copy_vec(d + row_bytes + k * hop, sy + k * p.tpr * 8);
+        }
+    }
+    copy_commit();
   };
-  if (pl.lane == 0)
-    for (int s = 0; s < p.stages; ++s)
-      if (r0 + (long long)s * step < p.M) issue(r0 + (long long)s * step, s);
+  for (int s = 0; s < p.stages; ++s) fill(r0 + (long long)s * step, s);
 
   // gate times the post norm's weight and bias, for the rows of one sequence
   // (of all sequences when there is one row of gates); 0 beyond the row
@@ -120,17 +118,21 @@ __global__ void __launch_bounds__(kThreads) join_fwd_kernel(FwdArgs p, DevStatus
   };
 
   // threads beyond the row read zeros
-  const uint32_t off = pl.lane * 8 * (uint32_t)sizeof(T), hop = p.tpr * 8 * (uint32_t)sizeof(T);
   const uint8_t* zero = smem + zero_at(p.groups);
+  Raw8<T> w_pre[VPT];   // this thread's part of the pre norm's weight, as stored
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+    w_pre[k] = *reinterpret_cast<const Raw8<T>*>(
+        p.pre && pl.lane + k * p.tpr < vecs ? static_cast<const void*>(static_cast<const T*>(p.pre_w) + 8 * (pl.lane + k * p.tpr))
+                                            : static_cast<const void*>(zero));
   int s = 0;
-  uint32_t parity = 0;
   for (int r = r0; r < p.M; r += step) {
     if (r >= gate_end) {   // the first row, and each first row of a sequence
       const int b = r / seq_rows;
       set_gate(b);
       gate_end = (int)min((long long)p.M, (b + 1ll) * seq_rows);
     }
-    tc::mbar_wait(bar0 + 8 * s, (parity >> s) & 1u, abort_flag, st, 710);
+    copy_wait(p.stages - 1);
     const uint8_t* stage = ring + s * p.stage_bytes + off;
     Vec8 xv[VPT], yv[VPT];
 #pragma unroll
@@ -139,26 +141,13 @@ __global__ void __launch_bounds__(kThreads) join_fwd_kernel(FwdArgs p, DevStatus
       xv[k] = get8<T>(on ? stage + k * hop : zero);
       if (y) yv[k] = get8<T>(on ? stage + row_bytes + k * hop : zero);
     }
-    parity ^= 1u << s;
-    // once every thread has its values the stage is free for a row further on:
-    // after the first sum over the group (or a barrier where there is none)
-    auto refill = [&] {
-      if (pl.lane == 0) {
-        const long long rn = r + (long long)p.stages * step;
-        if (rn < p.M) issue(rn, s);
-      }
-      if (++s == p.stages) s = 0;
-    };
-    if (!p.post) {
-      pl.sync();
-      refill();
-    }
+    fill(r + (long long)p.stages * step, s);
+    if (++s == p.stages) s = 0;
 
     if (y) {
       float mean = 0.f, rstd = 1.f;
       if (p.post) {
         stats(yv, mean, rstd);
-        refill();
         if (pl.lane == 0) {
           p.rstd_y[r] = rstd;
           if (LN) p.mean_y[r] = mean;
@@ -196,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) join_fwd_kernel(FwdArgs p, DevStatus
       for (int k = 0; k < VPT; ++k) {
         const int v = pl.lane + k * p.tpr;
         if (v >= vecs) continue;
-        const Vec8 w = get8<T>(static_cast<const T*>(p.pre_w) + 8 * v);
+        const Vec8 w = get8<T>(&w_pre[k]);
         const Vec8 o = LN ? param8<T>(p.pre_b, v, true, 0.f) : all8(0.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -207,9 +196,6 @@ __global__ void __launch_bounds__(kThreads) join_fwd_kernel(FwdArgs p, DevStatus
       }
     }
   }
-  // (every copy issued was waited for, unless a wait gave up)
-  __syncthreads();
-  if (*abort_flag && pl.lane == 0) drain(bar0, p.stages, parity);
 }
 
 template <typename T, bool LN, int VPT>
@@ -219,13 +205,13 @@ cudaError_t launch(const Ctx& c, const FwdArgs& p, const Shape& s) {
   const cudaError_t e = grant_smem(reinterpret_cast<const void*>(k), s.smem, granted);
   if (e != cudaSuccess) return e;
   const long long want = ((long long)p.M + s.groups - 1) / s.groups, fit = (long long)c.num_sms * 2;
-  k<<<(int)(want < fit ? want : fit), s.tpr * s.groups, s.smem, c.stream>>>(p, c.st);
+  k<<<(int)(want < fit ? want : fit), s.tpr * s.groups, s.smem, c.stream>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, bool LN>
 cudaError_t by_vpt(const Ctx& c, const FwdArgs& p, const Shape& s) {
-  return s.vpt == 1 ? launch<T, LN, 1>(c, p, s) : s.vpt == 2 ? launch<T, LN, 2>(c, p, s) : launch<T, LN, 4>(c, p, s);
+  return s.vpt == 1 ? launch<T, LN, 1>(c, p, s) : launch<T, LN, 2>(c, p, s);
 }
 
 }  // namespace
@@ -240,7 +226,7 @@ cudaError_t launch_join_fwd(const Ctx& c, const JoinFwd& j) {
   p.post_w = j.post_w; p.post_b = j.post_b; p.gate = j.gate; p.res_w = j.res_w; p.pre_w = j.pre_w; p.pre_b = j.pre_b;
   p.mean_y = j.mean_y; p.rstd_y = j.rstd_y; p.mean_h = j.mean_h; p.rstd_h = j.rstd_h;
   const uint32_t row = (uint32_t)j.D * (j.f32 ? 4 : 2) * (j.y ? 2 : 1);
-  const int vpt = j.D <= 256 ? 1 : j.D <= 4096 ? 2 : 4;
+  const int vpt = j.D <= 256 ? 1 : 2;
   const Shape s = make_shape(j.D, vpt, row, 0, 60 * 1024);
   p.tpr = s.tpr; p.groups = s.groups; p.stages = s.stages; p.stage_bytes = s.stage_bytes;
   prof_begin(c, "residual_norm_fwd");
