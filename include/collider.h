@@ -512,6 +512,42 @@ collider_status collider_layer_bwd(const collider_layer_desc* desc,
                                    collider_rows dx_rows, void* ws, size_t ws_bytes,
                                    void* stream);
 
+/* A block's saved set in 8 bits (collider_ckpt): the tensors of a
+ * collider_layer_saved that the backward cannot recompute.  x [*, D], qkv
+ * [*, (H+2Hkv)dh], o [*, H*dh], up [*, 2F] (LLAMA) or [*, F] (PHI), and h
+ * [*, D] (LLAMA) or a [*, D] (PHI), each in its own format; FULL rows (read
+ * through idx) or COMPACT ones (rows, for all of them), in device or pinned
+ * host memory.  The row statistics stay f32, FULL: rstd1, lse; rstd2 (LLAMA);
+ * mean1 (PHI). */
+typedef struct {
+  int rows;          /* collider_rows of the checkpoints */
+  collider_ckpt x;
+  collider_ckpt a;   /* PHI */
+  collider_ckpt qkv;
+  collider_ckpt o;
+  collider_ckpt h;   /* LLAMA */
+  collider_ckpt up;
+  const float* mean1;
+  const float* rstd1;
+  const float* lse;
+  const float* rstd2;
+} collider_layer_saved_ckpt;
+
+/* collider_layer_bwd of a saved set in 8 bits: the kept rows are decoded once
+ * (beside the first GEMM) and everything else is that call, so the gradients
+ * are bit-identical to its on the decoded values (LLAMA: with a, b and s
+ * recomputed).  A filtered call: idx, cu_kept and n_kept are given.  B*T <=
+ * 2^30.  Workspace: collider_layer_ckpt_workspace_size. */
+size_t collider_layer_ckpt_workspace_size(const collider_layer_desc* desc);
+collider_status collider_layer_bwd_ckpt(const collider_layer_desc* desc,
+                                        const collider_layer_weights* w,
+                                        const collider_layer_saved_ckpt* saved,
+                                        const void* dOut, collider_rows dout_rows,
+                                        const int32_t* idx, const int32_t* cu_kept,
+                                        const int32_t* n_kept, const collider_layer_grads* grads,
+                                        collider_rows dx_rows, void* ws, size_t ws_bytes,
+                                        void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Dense forward of one block (Fig. 2b: the forward stays dense; it saves    */
 /* what the filtered backward reads)                                         */

@@ -20,6 +20,7 @@ __all__ = [
     "CKPT_E4M3", "CKPT_INT8", "Ckpt", "ckpt", "ResidualNormDesc", "ResidualNormParams", "ResidualNormOut", "ResidualNormSaved",
     "ResidualNormGrads", "residual_norm_params", "residual_norm_out", "residual_norm_saved", "residual_norm_grads",
     "collider_ckpt_pack", "collider_ckpt_unpack", "collider_linear_ckpt_workspace_size", "collider_linear_bwd_ckpt",
+    "LayerSavedCkpt", "layer_saved_ckpt", "collider_layer_ckpt_workspace_size", "collider_layer_bwd_ckpt",
     "collider_residual_norm_fwd", "collider_residual_norm_bwd_workspace_size", "collider_residual_norm_bwd",
     "LayerDesc", "LayerWeights", "LayerSaved", "LayerGrads", "LayerParams", "LayerActs", "EXPORTED",
     "collider_last_error", "collider_check", "collider_selftest_wait_timeout", "collider_launch_count",
@@ -87,6 +88,11 @@ class Ckpt(C.Structure):
                 ("exp_ld", C.c_size_t)]
 
 
+class LayerSavedCkpt(C.Structure):
+    _fields_ = ([("rows", C.c_int)] + [(n, Ckpt) for n in ("x", "a", "qkv", "o", "h", "up")] +
+                [(n, C.c_void_p) for n in ("mean1", "rstd1", "lse", "rstd2")])
+
+
 class ResidualNormDesc(C.Structure):
     _fields_ = [("dtype", C.c_int), ("B", C.c_int), ("T", C.c_int), ("D", C.c_int), ("norm", C.c_int),
                 ("post", C.c_int), ("pre", C.c_int), ("eps", C.c_float), ("res_scale", C.c_float),
@@ -136,6 +142,9 @@ _SIGS = {
     "collider_ckpt_unpack": (I, [I, C.POINTER(Ckpt), I, I, I, P, P, P, SZ, I, P]),
     "collider_linear_ckpt_workspace_size": (SZ, [I, I, I]),
     "collider_linear_bwd_ckpt": (I, [I, I, I, C.POINTER(Ckpt), I, P, P, I, P, P, P, I, P, P, P, SZ, P]),
+    "collider_layer_ckpt_workspace_size": (SZ, [C.POINTER(LayerDesc)]),
+    "collider_layer_bwd_ckpt": (I, [C.POINTER(LayerDesc), C.POINTER(LayerWeights), C.POINTER(LayerSavedCkpt), P, I,
+                                    P, P, P, C.POINTER(LayerGrads), I, P, SZ, P]),
     "collider_residual_norm_fwd": (I, [C.POINTER(ResidualNormDesc), C.POINTER(ResidualNormParams), P, P,
                                        C.POINTER(ResidualNormOut), P]),
     "collider_residual_norm_bwd_workspace_size": (SZ, [C.POINTER(ResidualNormDesc)]),
@@ -318,6 +327,18 @@ def ckpt(format, code, exps) -> Ckpt:
     return q
 
 
+def layer_saved_ckpt(rows, **fields) -> LayerSavedCkpt:
+    """LayerSavedCkpt from :func:`ckpt` checkpoints (x, qkv, o, up, h or a) and f32 tensors (rstd1, lse, ...)."""
+    s = LayerSavedCkpt(rows=rows)
+    s.buffers = fields
+    for k, v in fields.items():
+        if k not in {f[0] for f in LayerSavedCkpt._fields_}:
+            raise TypeError(f"LayerSavedCkpt has no field {k}")
+        if v is not None:
+            setattr(s, k, v if isinstance(v, Ckpt) else _ptr(v))
+    return s
+
+
 def residual_norm_params(**tensors) -> ResidualNormParams:
     """ResidualNormParams from tensors by field name (None or absent: NULL)."""
     return _filled(ResidualNormParams, tensors)
@@ -394,6 +415,17 @@ def collider_layer_bwd(desc, weights, saved, dOut, dout_rows, idx, cu_kept, n_ke
     _check(lib().collider_layer_bwd(C.byref(desc), C.byref(weights), C.byref(saved), _ptr(dOut), dout_rows,
                                     _ptr(idx), _ptr(cu_kept), _ptr(n_kept), C.byref(grads), dx_rows, _ptr(ws),
                                     _nbytes(ws), _stream(stream)))
+
+
+def collider_layer_ckpt_workspace_size(desc: LayerDesc) -> int:
+    return lib().collider_layer_ckpt_workspace_size(C.byref(desc))
+
+
+def collider_layer_bwd_ckpt(desc, weights, saved, dOut, dout_rows, idx, cu_kept, n_kept, grads, dx_rows, ws,
+                            stream=None) -> None:
+    _check(lib().collider_layer_bwd_ckpt(C.byref(desc), C.byref(weights), C.byref(saved), _ptr(dOut), dout_rows,
+                                         _ptr(idx), _ptr(cu_kept), _ptr(n_kept), C.byref(grads), dx_rows, _ptr(ws),
+                                         _nbytes(ws), _stream(stream)))
 
 
 def collider_layer_fwd_workspace_size(desc: LayerDesc) -> int:

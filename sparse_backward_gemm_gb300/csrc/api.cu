@@ -767,7 +767,7 @@ void layer_carve(Carver& cv, const collider_layer_desc* d, LayerBufs* L) {
 struct Side {
   cudaStream_t s = nullptr;    // weight gradients, default priority
   cudaStream_t hi = nullptr;   // input-gradient chain, highest priority
-  cudaEvent_t ev[12] = {};
+  cudaEvent_t ev[13] = {};
 };
 thread_local Side g_side[64];
 
@@ -985,13 +985,22 @@ cudaError_t gemm_dw(const Ctx& c, int M, int Kin, int Nout, const void* Xk, long
   return launch_tc_gemm(c, g);
 }
 
+// A saved set in 8 bits: x, h and up are decoded at their FULL rows (kept rows
+// alone) into buffers of the workspace, which the block's kernels then read as
+// they read a bf16 saved set; qkv, o (and a, PHI) straight into the compact copies.
+struct LayerCkpt {
+  const collider_layer_saved_ckpt* saved;
+  __nv_bfloat16 *x, *h, *up;   // [M, D], [M, D] (LLAMA), [M, Nup]
+};
+
 // dense: every token is kept (idx, cu_kept, n_kept are the identity index the
 // caller made with launch_identity_index into L.id_*): the saved rows and dOut
 // are read where they are, nothing is gathered, and dx is written in place.
 collider_status layer_bwd_impl(const Ctx& c_in, const collider_layer_desc* d, const collider_layer_weights* w,
                                const collider_layer_saved* sv, const void* dOut, bool dout_full,
                                const int32_t* idx, const int32_t* cu_kept, const int32_t* n_kept,
-                               const collider_layer_grads* g, bool dx_full, LayerBufs& L, bool dense = false) {
+                               const collider_layer_grads* g, bool dx_full, LayerBufs& L, bool dense = false,
+                               const LayerCkpt* ck = nullptr) {
   // c: the context of the input-gradient chain (the high-priority stream when
   // the side stream is on, else the caller's)
   Ctx c = c_in;
@@ -1056,7 +1065,18 @@ collider_status layer_bwd_impl(const Ctx& c_in, const collider_layer_desc* d, co
     c.pdl = pdl_allowed();
   }
   CK(fork_side(c, side, 0));   // the side stream starts once dOut's kept rows exist
-  if (!dense) {
+  // a checkpoint's kept rows: FULL where they belong, or COMPACT and zero-padded
+  auto decode = [&](const collider_ckpt& q, int N, void* dst, bool full) {
+    return launch_q8_unpack(cs, 0, q.format, view(&q), ck->saved->rows == COLLIDER_ROWS_FULL, M, N, idx, n_kept, dst, N,
+                            full ? 2 : 0, pad128(M));
+  };
+  if (ck) {
+    CK(decode(ck->saved->up, Nup, ck->up, true));
+    if (llama) CK(decode(ck->saved->h, D, ck->h, true));
+    CK(decode(ck->saved->x, D, ck->x, true));
+    if (side) CK(cudaEventRecord(side->ev[12], cs.stream));
+    CK(decode(ck->saved->qkv, Nqkv, L.qkv_k, false));
+  } else if (!dense) {
     GatherJob j{static_cast<const char*>(sv->qkv), reinterpret_cast<char*>(L.qkv_k), (long long)Nqkv * 2,
                 (long long)Nqkv * 2, Nqkv * 2, 0};
     CK(launch_gather(cs, &j, 1, M, pad128(M), idx, n_kept));
@@ -1089,9 +1109,14 @@ collider_status layer_bwd_impl(const Ctx& c_in, const collider_layer_desc* d, co
       j[n++] = GatherJob{static_cast<const char*>(sv->up), reinterpret_cast<char*>(L.s_k), (long long)F * 2,
                          (long long)F * 2, F * 2, 1};
     }
-    if (!dense) {
+    if (ck) {
+      CK(decode(ck->saved->o, Hd, L.o_k, false));
+      if (!llama) CK(decode(ck->saved->a, D, L.a_k, false));
+    } else if (!dense) {
       j[n++] = GatherJob{static_cast<const char*>(sv->o), reinterpret_cast<char*>(L.o_k), (long long)Hd * 2,
                          (long long)Hd * 2, Hd * 2, 0};
+    }
+    if (!dense && !(ck && !llama)) {
       if (sv->a) {
         j[n++] = GatherJob{static_cast<const char*>(sv->a), reinterpret_cast<char*>(L.a_k), (long long)D * 2,
                            (long long)D * 2, D * 2, 0};
@@ -1112,9 +1137,11 @@ collider_status layer_bwd_impl(const Ctx& c_in, const collider_layer_desc* d, co
     const bool s_re = !dense && !sv->s, b_re = !dense && !sv->b;
     if (!s_re) CK(gemm_dw(cs, M, F, D, L.s_k, F, L.dout_k, D, g->dw_down, n_kept, in_rows));   // dW_down = s^T dOut
     CK(gemm_dx(c, M, F, D, L.dout_k, w->w_down, L.ds_k, 1, 0, n_kept, in_rows));      // ds = dOut W_down^T
-    c.pdl = pdl_allowed();
+    c.pdl = pdl_allowed() && !(ck && side);   // (not behind an event wait)
+    if (ck && side) CK(cudaStreamWaitEvent(c.stream, side->ev[12], 0));   // x, h and up are decoded
     CK(launch_swiglu_bwd(c, L.ds_k, 1, F, static_cast<const __nv_bfloat16*>(sv->up), L.dgu_k, M, pad128(M), idx,
                          n_kept, s_re ? L.s_k : nullptr));
+    c.pdl = pdl_allowed();
     CK(fork_side(c, side, 1));
     if (s_re) CK(gemm_dw(cs, M, F, D, L.s_k, F, L.dout_k, D, g->dw_down, n_kept, in_rows));
     if (!b_re) CK(gemm_dw(cs, M, D, Nup, L.b_k, D, L.dgu_k, Nup, g->dw_up, n_kept, in_rows));  // dW_up = b^T dgu
@@ -1140,10 +1167,15 @@ collider_status layer_bwd_impl(const Ctx& c_in, const collider_layer_desc* d, co
     CK(gemm_dw(cs, M, F, D, L.s_k, F, L.dout_k, D, g->dw_down, n_kept, in_rows));     // dW2 = gelu(f1)^T dOut
     CK(gemm_dx(c, M, F, D, L.dout_k, w->w_down, L.ds_k, 1, 0, n_kept, in_rows));      // df2 = dOut W2^T
     c.pdl = pdl_allowed();
+    if (ck && side) {
+      CK(cudaStreamWaitEvent(c.stream, side->ev[12], 0));   // x and up are decoded
+      c.pdl = false;   // (the next kernel follows the wait)
+    }
     if (d->mlp_bias && g->db_down)
       CK(launch_colsum(c, L.dout_k, 1, D, M, D, nullptr, n_kept, L.col_part, g->db_down));
     CK(launch_gelu_bwd(c, L.ds_k, 1, F, static_cast<const __nv_bfloat16*>(sv->up), L.dgu_k, M, pad128(M), idx,
                        n_kept));
+    c.pdl = pdl_allowed();
     CK(fork_side(c, side, 1));
     CK(gemm_dw(cs, M, D, F, L.a_k, D, L.dgu_k, F, g->dw_up, n_kept, in_rows));        // dW1 = a^T df1
     if (d->mlp_bias && g->db_up)
@@ -1301,6 +1333,81 @@ extern "C" collider_status collider_layer_bwd(const collider_layer_desc* d, cons
   }
   return layer_bwd_impl(c, d, w, sv, dOut, dout_rows == COLLIDER_ROWS_FULL, idx, cu_kept, n_kept, g,
                         dx_rows == COLLIDER_ROWS_FULL, L);
+}
+
+namespace {
+void layer_ckpt_carve(Carver& cv, const collider_layer_desc* d, LayerBufs* L, LayerCkpt* ck) {
+  layer_carve(cv, d, L);
+  const size_t M = (size_t)d->B * d->T;
+  const bool llama = d->arch == COLLIDER_ARCH_LLAMA;
+  ck->x = cv.take<__nv_bfloat16>(M * d->D);
+  ck->h = llama ? cv.take<__nv_bfloat16>(M * d->D) : nullptr;
+  ck->up = cv.take<__nv_bfloat16>(M * (llama ? 2 : 1) * d->F);
+}
+}  // namespace
+
+extern "C" size_t collider_layer_ckpt_workspace_size(const collider_layer_desc* d) {
+  if (check_desc(d) != COLLIDER_OK) return 0;
+  Carver cv{nullptr, 0, 0, true};
+  LayerBufs L;
+  LayerCkpt ck;
+  layer_ckpt_carve(cv, d, &L, &ck);
+  return cv.used;
+}
+
+extern "C" collider_status collider_layer_bwd_ckpt(const collider_layer_desc* d, const collider_layer_weights* w,
+                                                   const collider_layer_saved_ckpt* sc, const void* dOut,
+                                                   collider_rows dout_rows, const int32_t* idx, const int32_t* cu_kept,
+                                                   const int32_t* n_kept, const collider_layer_grads* g,
+                                                   collider_rows dx_rows, void* ws, size_t ws_bytes, void* stream) {
+  static const char* fn = "collider_layer_bwd_ckpt";
+  collider_status s = check_desc(d);
+  if (s != COLLIDER_OK) return s;
+  if ((long long)d->B * d->T > (1 << 30)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need B*T <= 2^30", fn);
+  if (!sc || !dOut || !al16(dOut) || !idx || !cu_kept || !n_kept)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: null saved set or index, or null or misaligned dOut", fn);
+  const bool llama = d->arch == COLLIDER_ARCH_LLAMA;
+  if (sc->rows != COLLIDER_ROWS_FULL && sc->rows != COLLIDER_ROWS_COMPACT)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
+  const int Nqkv = (d->H + 2 * d->Hkv) * d->dh;
+  s = check_ckpt(fn, &sc->x, d->D);
+  if (s == COLLIDER_OK) s = check_ckpt(fn, &sc->qkv, Nqkv);
+  if (s == COLLIDER_OK) s = check_ckpt(fn, &sc->o, d->H * d->dh);
+  if (s == COLLIDER_OK) s = check_ckpt(fn, &sc->up, llama ? 2 * d->F : d->F);
+  if (s == COLLIDER_OK) s = check_ckpt(fn, llama ? &sc->h : &sc->a, d->D);
+  if (s != COLLIDER_OK) return s;
+  const size_t need = collider_layer_ckpt_workspace_size(d);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
+  Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
+  LayerBufs L;
+  LayerCkpt ck;
+  layer_ckpt_carve(cv, d, &L, &ck);
+  ck.saved = sc;
+  // the saved set as the block's kernels see it: decoded rows where they are
+  // read through the index; qkv and o only by their compact copies, which the
+  // pointers here merely stand for
+  collider_layer_saved sv{};
+  sv.x = ck.x; sv.rstd1 = sc->rstd1; sv.mean1 = sc->mean1; sv.lse = sc->lse; sv.up = ck.up;
+  sv.qkv = L.qkv_k; sv.o = L.o_k;
+  if (llama) {
+    sv.h = ck.h; sv.rstd2 = sc->rstd2;
+  } else {
+    sv.a = L.a_k;
+  }
+  s = check_layer_ptrs(d, w, &sv, g, true);
+  if (s != COLLIDER_OK) return s;
+  Ctx c;
+  s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_input_memory(w, &sv, dOut, g, false);
+  if (s == COLLIDER_OK) s = check_memory(fn, {idx, cu_kept, n_kept, ws});
+  if (s == COLLIDER_OK)
+    s = check_memory(fn, {sc->x.code, sc->x.exps, sc->qkv.code, sc->qkv.exps, sc->o.code, sc->o.exps, sc->up.code,
+                          sc->up.exps, llama ? sc->h.code : sc->a.code, llama ? sc->h.exps : sc->a.exps}, true);
+  if (s != COLLIDER_OK) return s;
+  CK(cudaMemsetAsync(L.sk_counters, 0, L.sk_cap * sizeof(int), c.stream));
+  return layer_bwd_impl(c, d, w, &sv, dOut, dout_rows == COLLIDER_ROWS_FULL, idx, cu_kept, n_kept, g,
+                        dx_rows == COLLIDER_ROWS_FULL, L, false, &ck);
 }
 
 // ===========================================================================

@@ -321,8 +321,8 @@ struct Q8View {
 cudaError_t launch_q8_pack(const Ctx& c, int f32, const void* src, long long src_ld, int M, int N, const int32_t* idx,
                            const int32_t* n_kept, int format, const Q8View& q);
 // dst row (dst_full ? idx[r] : r) = row (src_full ? idx[r] : r) of q; the other
-// rows of a FULL dst (M) are 0, those of a COMPACT one up to the next multiple of
-// 128 (below cap).
+// rows of a FULL dst (M) are 0 (dst_full 2: left as they were), those of a COMPACT
+// one up to the next multiple of 128 (below cap).
 cudaError_t launch_q8_unpack(const Ctx& c, int f32, int format, const Q8View& q, int src_full, int M, int N,
                              const int32_t* idx, const int32_t* n_kept, void* dst, long long dst_ld, int dst_full,
                              long long cap);

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) q8_unpack_kernel(Q8View q, int src_f
                                                              long long cap, DevStatus* st) {
   grid_dep_wait();
   const int nk = kept_rows(n_kept, M);
-  const int slots = dst_full ? M : padded_rows(nk, cap);
+  const int slots = dst_full == 2 ? nk : dst_full ? M : padded_rows(nk, cap);
   const int lane = threadIdx.x & 31, vecs = N >> 3, v0 = blockIdx.y * kSegVecs + lane;
   for (int r = first_row(); r < slots; r += row_step()) {
     if (r >= nk) {
