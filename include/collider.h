@@ -285,7 +285,7 @@ typedef struct {
   float res_scale;
   int gate_rows;      /* rows of gate: 0 (no gate), 1 (all tokens), B (one a sequence) */
   int x_ld, y_ld, h_ld, a_ld; /* row strides in elements of x, y, h, a and of their
-                                 gradients dx, dy, dh, da; 0 means D */
+                                 gradients dx, dy, dh, da, at most 2^28; 0 means D */
 } collider_residual_norm_desc;
 
 /* Parameters, dtype [D] (gate [gate_rows, D]).  NULL where the desc has none;

@@ -1709,8 +1709,8 @@ collider_status check_join_desc(const char* fn, const collider_residual_norm_des
   *ld = JoinLd{d->x_ld ? d->x_ld : d->D, d->y_ld ? d->y_ld : d->D, d->h_ld ? d->h_ld : d->D, d->a_ld ? d->a_ld : d->D};
   const int per = d->dtype == COLLIDER_F32 ? 4 : 8;
   for (long long l : {ld->x, ld->y, ld->h, ld->a})
-    if (l < d->D || l % per)
-      return fail(COLLIDER_ERR_INVALID_ARG, "%s: row strides must be >= D and multiples of 16 bytes", fn);
+    if (l < d->D || l % per || l > (1 << 28))
+      return fail(COLLIDER_ERR_INVALID_ARG, "%s: row strides must be >= D, multiples of 16 bytes and at most 2^28", fn);
   return COLLIDER_OK;
 }
 // the parameters a call with these norms reads

@@ -370,7 +370,7 @@ struct JoinBwd {
   int src;               // y and h: kQ8E4m3 or kQ8Int8 codes, or 2: as stored
   const void *y, *h;
   const uint8_t *y_exps, *h_exps;
-  long long x_ld, y_ld, h_ld, a_ld;   // elements; the gradients have the strides of their tensors
+  long long x_ld, y_ld, h_ld, a_ld;   // elements, at most 2^28; the gradients have the strides of their tensors
   long long y_code_ld, h_code_ld, y_exp_ld, h_exp_ld;
   const void *post_w, *post_b, *gate, *res_w, *pre_w;
   const float *mean_y, *rstd_y, *mean_h, *rstd_h;   // FULL [M]

@@ -43,9 +43,9 @@ struct BwdArgs {
   int gate_rows, post, pre, branch;
   const void *da, *dh, *x, *y, *h;     // y, h: T rows, or codes
   const uint8_t *y_exps, *h_exps;
-  long long a_ld, h_ld, x_ld, y_ld;    // elements (strides of the gradients too)
-  long long ys_ld, hs_ld;              // bytes between rows of the saved y, h
-  long long ye_ld, he_ld;
+  // bytes between rows (below 2^32, so that a row's offset is one multiplication)
+  uint32_t a_ld, h_ld, x_ld, y_ld;     // of a, h, x, y and their gradients
+  uint32_t ys_ld, hs_ld, ye_ld, he_ld; // of the saved y, h and of their exponents
   const void *post_w, *post_b, *gate, *res_w, *pre_w;
   const float *mean_y, *rstd_y, *mean_h, *rstd_h;
   const int32_t *idx, *cu, *nk;
@@ -61,6 +61,11 @@ struct BwdArgs {
 
 // a stage's exponent bytes: two a vector, rounded up to whole 16s
 __host__ __device__ constexpr uint32_t exps_bytes(int tpr, int vpt) { return (tpr * vpt * 2 + 15) / 16 * 16; }
+
+template <typename T>
+__device__ __forceinline__ T* row_of(T* base, uint32_t row, uint32_t ld) {
+  return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(base) + (uint64_t)row * ld);
+}
 
 __device__ __forceinline__ int kept(const BwdArgs& p) { return p.nk ? min(max(*p.nk, 0), p.M) : p.M; }
 // CTAs that have rows: each at least one
@@ -171,8 +176,7 @@ __global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus
   // row j of this group, if there is one, into stage s: this thread's columns,
   // and a few lanes of each warp its statistics
   auto fill = [&](int j, int s) {
-    const int t = token(j);
-    const long long r = first + (long long)j * step;
+    const int t = token(j), r = first + j * step;
     if (r < r1) {
       const uint32_t d = ring0 + s * p.stage_bytes;
       const int lane = pl.lane & 31;
@@ -182,10 +186,10 @@ __global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus
         if (lane == 1 && p.post) copy4(d + my_head + 4, p.rstd_y + t);
         if (LN && lane == 2 && p.pre) copy4(d + my_head + 8, p.mean_h + t);
         if (LN && lane == 3 && p.post) copy4(d + my_head + 12, p.mean_y + t);
-        const long long sr = p.saved_full ? t : r, ir = p.in_full ? t : r;
-        const T *s_da = da + ir * p.a_ld + 8 * pl.lane, *s_dh = dh + ir * p.h_ld + 8 * pl.lane,
-                *s_x = x + sr * p.x_ld + 8 * pl.lane;
-        const uint8_t *s_h = h + sr * p.hs_ld + s_off, *s_y = y + sr * p.ys_ld + s_off;
+        const int sr = p.saved_full ? t : r, ir = p.in_full ? t : r;
+        const T *s_da = row_of(da + 8 * pl.lane, ir, p.a_ld), *s_dh = row_of(dh + 8 * pl.lane, ir, p.h_ld),
+                *s_x = row_of(x + 8 * pl.lane, sr, p.x_ld);
+        const uint8_t *s_h = row_of(h + s_off, sr, p.hs_ld), *s_y = row_of(y + s_off, sr, p.ys_ld);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
           const int v = pl.lane + k * p.tpr;
@@ -199,8 +203,8 @@ __global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus
           } else {
             if (h) copy8(d + o_h + s_off + k * s_hop, s_h + k * s_hop);
             if (y) copy8(d + o_y + s_off + k * s_hop, s_y + k * s_hop);
-            e_h[k] = h ? p.h_exps[sr * p.he_ld + (v >> 2)] : 0;
-            e_y[k] = y ? p.y_exps[sr * p.ye_ld + (v >> 2)] : 0;
+            e_h[k] = h ? row_of(p.h_exps, sr, p.he_ld)[v >> 2] : 0;
+            e_y[k] = y ? row_of(p.y_exps, sr, p.ye_ld)[v >> 2] : 0;
           }
         }
         e_stage = s;
@@ -223,19 +227,27 @@ __global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus
     land_exps();
     fill(j, j);
   }
-  // While the first rows are on their way: zeros where there is no kept row, the
-  // filtered tokens of FULL outputs or the padding of COMPACT ones, a warp a row.
-  {
-    const int zeros = p.out_full ? p.M - nk : padded_rows(nk, p.M) - nk, lane = threadIdx.x & 31;
-    const int wpb = blockDim.x >> 5;
-    for (int j = blockIdx.x * wpb + (threadIdx.x >> 5); j < zeros; j += gridDim.x * wpb) {
-      const long long row = p.out_full ? filtered_token(p.idx, nk, j) : nk + j;
-      for (int v = lane; v < vecs; v += 32) {
-        put8(dx + row * p.x_ld + 8 * v, all8(0.f));
-        if (p.branch) put8(dy + row * p.y_ld + 8 * v, all8(0.f));
-      }
+  // Zeros where there is no kept row -- the filtered tokens of FULL outputs, the
+  // padding of COMPACT ones -- are a warp's a row, 32 vectors at a time between
+  // its other work.
+  const int zeros = p.out_full ? p.M - nk : padded_rows(nk, p.M) - nk, z_step = gridDim.x * (blockDim.x >> 5);
+  int z = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), z_vec = 0;
+  auto zero_row = [&] { return z >= zeros ? 0 : p.out_full ? filtered_token(p.idx, nk, z) : nk + z; };
+  int z_row = zero_row();
+  auto zero_some = [&] {
+    if (z >= zeros) return;
+    const int v = z_vec + (threadIdx.x & 31);
+    if (v < vecs) {
+      put8(row_of(dx + 8 * v, z_row, p.x_ld), all8(0.f));
+      if (p.branch) put8(row_of(dy + 8 * v, z_row, p.y_ld), all8(0.f));
     }
-  }
+    z_vec += 32;
+    if (z_vec >= vecs) {
+      z += z_step;
+      z_vec = 0;
+      z_row = zero_row();
+    }
+  };
 
   // Column sums over this group's rows: of da hh, da (LN), and -- of one
   // sequence while gates differ by sequence -- of dh yh, dh (LN); of dh x.
@@ -339,9 +351,8 @@ __global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus
       }
       o1 = -fmaf(rh.x, o1, q[1]) * p.inv_d;
       if (!p.post) o1 = o0 = 0.f;
-      const long long orow = p.out_full ? old_token : r - step;
-      T* rowx = dx + orow * p.x_ld + 8 * pl.lane;
-      T* rowy = dy + orow * p.y_ld + 8 * pl.lane;
+      const int orow = p.out_full ? old_token : r - step;
+      T *rowx = row_of(dx + 8 * pl.lane, orow, p.x_ld), *rowy = row_of(dy + 8 * pl.lane, orow, p.y_ld);
       const f2 n1b = both(n1), n0b = both(n0), o1b = both(o1), o0b = both(o0);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
@@ -440,6 +451,7 @@ __global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus
         leave_sums(pl, red + (i & 1) * kMaxSums * kMaxWarps, v);
       }
     }
+    zero_some();
     pl.sync();   // row i's sums are left
     prev = s;
     if (++s == p.stages) s = 0;
@@ -450,6 +462,7 @@ __global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus
     while (b < b_last) end_sequence(false);
     end_sequence(true);
   }
+  while (z < zeros) zero_some();
   if (!mine) return;
   __syncthreads();
   float* line = reinterpret_cast<float*>(smem + p.ring_at);   // the rings are done with
@@ -608,11 +621,12 @@ cudaError_t launch_join_bwd(const Ctx& c, const JoinBwd& j) {
   p.gate_rows = j.gate_rows; p.post = j.post; p.pre = j.pre; p.branch = j.y != nullptr;
   p.da = j.da; p.dh = j.dh; p.x = j.x; p.y = j.y; p.h = j.pre ? j.h : nullptr;
   p.y_exps = j.y_exps; p.h_exps = j.h_exps;
-  p.a_ld = j.a_ld; p.h_ld = j.h_ld; p.x_ld = j.x_ld; p.y_ld = j.y_ld;
   const bool same = j.src == kSrcSame;
   const int es = j.f32 ? 4 : 2;
-  p.ys_ld = same ? j.y_ld * es : j.y_code_ld; p.hs_ld = same ? j.h_ld * es : j.h_code_ld;
-  p.ye_ld = j.y_exp_ld; p.he_ld = j.h_exp_ld;
+  p.a_ld = (uint32_t)(j.a_ld * es); p.h_ld = (uint32_t)(j.h_ld * es);
+  p.x_ld = (uint32_t)(j.x_ld * es); p.y_ld = (uint32_t)(j.y_ld * es);
+  p.ys_ld = same ? p.y_ld : (uint32_t)j.y_code_ld; p.hs_ld = same ? p.h_ld : (uint32_t)j.h_code_ld;
+  p.ye_ld = (uint32_t)j.y_exp_ld; p.he_ld = (uint32_t)j.h_exp_ld;
   p.post_w = j.post_w; p.post_b = j.post_b; p.gate = j.gate; p.res_w = j.res_w; p.pre_w = j.pre_w;
   p.mean_y = j.mean_y; p.rstd_y = j.rstd_y; p.mean_h = j.mean_h; p.rstd_h = j.rstd_h;
   p.idx = j.idx; p.cu = j.cu; p.nk = j.nk;
