@@ -99,6 +99,11 @@ collider_status make_ctx(void* stream, Ctx* c) {
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool al4(std::initializer_list<const void*> ps) {
+  uintptr_t u = 0;
+  for (const void* p : ps) u |= reinterpret_cast<uintptr_t>(p);
+  return (u & 3) == 0;
+}
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 long long pad128(long long m) { return (m + 127) & ~127ll; }
 
@@ -382,7 +387,8 @@ extern "C" collider_status collider_ckpt_pack(collider_dtype dtype, const void* 
                                             void* stream) {
   static const char* fn = "collider_ckpt_pack";
   if (dtype != COLLIDER_F32 && dtype != COLLIDER_BF16) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: dtype %d", fn, (int)dtype);
-  if (!src || !idx != !n_kept) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null src, or only one of idx and n_kept", fn);
+  if (!src || !idx != !n_kept || !al4({idx, n_kept}))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: null src, only one of idx and n_kept, or these misaligned", fn);
   if (M < 1 || M > (1 << 30)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need 1 <= M <= 2^30", fn);
   collider_status s = check_ckpt(fn, out, N);
   if (s == COLLIDER_OK) s = check_rows(fn, dtype, src, (long long)src_ld, N);
@@ -400,7 +406,8 @@ extern "C" collider_status collider_ckpt_unpack(collider_dtype dtype, const coll
                                               size_t dst_ld, collider_rows dst_rows, void* stream) {
   static const char* fn = "collider_ckpt_unpack";
   if (dtype != COLLIDER_F32 && dtype != COLLIDER_BF16) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: dtype %d", fn, (int)dtype);
-  if (!dst || !idx != !n_kept) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null dst, or only one of idx and n_kept", fn);
+  if (!dst || !idx != !n_kept || !al4({idx, n_kept}))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: null dst, only one of idx and n_kept, or these misaligned", fn);
   if (M < 1 || M > (1 << 30)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need 1 <= M <= 2^30", fn);
   if (!is_rows(src_rows) || !is_rows(dst_rows)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
   collider_status s = check_ckpt(fn, src, N);
@@ -860,7 +867,8 @@ extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const c
   static const char* fn = "collider_linear_bwd_ckpt";
   if (M < 1 || M > (1 << 30) || K < 1 || N < 1 || K > (1 << 24) || N > (1 << 24))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: bad sizes", fn);
-  if (!idx || !n_kept || !dY) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null idx/n_kept/dY", fn);
+  if (!idx || !n_kept || !dY || !al4({idx, n_kept}))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: null idx/n_kept/dY, or a misaligned index", fn);
   if (dX && !W) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dX needs W", fn);
   if (!is_rows(x_rows) || !is_rows(dy_rows) || !is_rows(dx_rows))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
@@ -1364,8 +1372,8 @@ extern "C" collider_status collider_layer_bwd_ckpt(const collider_layer_desc* d,
   collider_status s = check_desc(d);
   if (s != COLLIDER_OK) return s;
   if ((long long)d->B * d->T > (1 << 30)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need B*T <= 2^30", fn);
-  if (!sc || !dOut || !al16(dOut) || !idx || !cu_kept || !n_kept)
-    return fail(COLLIDER_ERR_INVALID_ARG, "%s: null saved set or index, or null or misaligned dOut", fn);
+  if (!sc || !dOut || !al16(dOut) || !idx || !cu_kept || !n_kept || !al4({idx, cu_kept, n_kept, sc->rstd1, sc->lse}))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: null saved set or index, or null or misaligned dOut, index or statistics", fn);
   const bool llama = d->arch == COLLIDER_ARCH_LLAMA;
   if (sc->rows != COLLIDER_ROWS_FULL && sc->rows != COLLIDER_ROWS_COMPACT)
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
@@ -1758,6 +1766,8 @@ extern "C" collider_status collider_residual_norm_fwd(const collider_residual_no
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: h in the place of x or y needs its row stride", fn);
   for (const void* p : {x, y, static_cast<const void*>(o->h), static_cast<const void*>(o->a)})
     if (!al16(p)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  if (!al4({o->mean_y, o->rstd_y, o->mean_h, o->rstd_h}))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: statistics must be 4-byte aligned", fn);
   Ctx c;
   s = make_ctx(stream, &c);
   if (s == COLLIDER_OK) s = check_join_memory(fn, w);
@@ -1819,6 +1829,9 @@ extern "C" collider_status collider_residual_norm_bwd(const collider_residual_no
   if (s != COLLIDER_OK) return s;
   for (const void* p : {da, dh, sv->x, sv->y, sv->h, static_cast<const void*>(g->dx), static_cast<const void*>(g->dy)})
     if (!al16(p)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  if (!al4({sv->mean_y, sv->rstd_y, sv->mean_h, sv->rstd_h, idx, cu_kept, n_kept, g->dpre_w, g->dpre_b, g->dpost_w,
+            g->dpost_b, g->dgate, g->dres_w}))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: statistics, indices and f32 gradients must be 4-byte aligned", fn);
   if (g->dx == da || (g->dy && (g->dy == da || g->dy == dh || g->dy == g->dx)) ||
       (g->dx == dh && (in_rows != out_rows || ld.x != ld.h)))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: of the outputs only dx may alias an input: dh, of the same rows and stride",

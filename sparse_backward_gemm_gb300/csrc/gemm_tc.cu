@@ -170,14 +170,14 @@ struct SegIter {
 
 // Store 32 consecutive columns of one output row (bf16 or f32, optional
 // accumulate into C, zero rows past the kept count up to the padding).
-__device__ __forceinline__ void store32(const TcParams& p, long long row, int col, bool row_ok, float* v, bool piece = false) {
+__device__ __forceinline__ void store32(const TcParams& p, int row, int col, bool row_ok, float* v, bool piece = false) {
   if (p.c_bf16) {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + row * p.ldc + col;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + (long long)row * p.ldc + col;
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       if (col + 8 * g + 8 <= p.N) *reinterpret_cast<uint4*>(out + 8 * g) = pack8(v + 8 * g);
   } else {
-    float* out = static_cast<float*>(p.C) + row * p.ldc + col;
+    float* out = static_cast<float*>(p.C) + (long long)row * p.ldc + col;
     if (piece && row_ok) {
       // a later piece of the reduction is added where C lies, without a round
       // trip (an f32 add rounded to nearest; subnormal values count as 0), by
@@ -215,7 +215,8 @@ __device__ __forceinline__ void store32(const TcParams& p, long long row, int co
 //           TMEM-full barriers, and both epilogues release the accumulator on
 //           the even CTA's TMEM-empty barrier.  No copy is multicast: each CTA
 //           loads only what lands in its own shared memory.
-template <int BN, bool A_MN, bool B_MN, int MODE>
+// IDX: output rows through c_idx (a dX whose kept rows go where they belong).
+template <int BN, bool A_MN, bool B_MN, int MODE, bool IDX>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, TcParams p) {
   using Cfg = TcCfg<BN>;
@@ -280,7 +281,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   sp.ustride = sp.W;
   sp.init(p.split_mode, p.partial != nullptr);
   // (pieces of equal length, so that none is a short tail)
-  const int pieces = p.k_piece > 0 && sp.num_kb > p.k_piece ? (sp.num_kb + p.k_piece - 1) / p.k_piece : 1;
+  constexpr bool PIECES = A_MN && B_MN;   // only weight gradients are cut
+  const int pieces = PIECES && p.k_piece > 0 && sp.num_kb > p.k_piece ? (sp.num_kb + p.k_piece - 1) / p.k_piece : 1;
   sp.piece = (sp.num_kb + pieces - 1) / pieces;
   // partial tile of worker w for tile t: this CTA's 128 rows, stored as
   // [BN / 4][BM][4] f32 so that a warp's 32 rows touch 512 contiguous bytes
@@ -473,8 +475,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int rl = q * 32 + lane;
       const int row = m0 + rl;
       bool row_ok = row < M;
-      long long out_row = row;
-      if (p.c_idx && row_ok) {
+      int out_row = row;
+      if (IDX && row_ok) {
         out_row = p.c_idx[row];
         row_ok = out_row >= 0 && out_row < p.c_rows;
         if (!row_ok) report_error(p.st, kErrBadIndex, 60);
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       fence_after();
       const bool row_zero = !row_ok && p.zero_pad && row < padded_rows(M, p.c_rows);   // (never with c_idx)
       const uint32_t tcol = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
-      if ((k0 == 0 && k1 == sp.num_kb) || t < sp.dp_tiles) {
+      if ((k0 == 0 && k1 == sp.num_kb) || (PIECES && t < sp.dp_tiles)) {
         // whole tile, or a piece of its reduction: straight to the output
         for (int c = 0; c < BN; c += 32) {
           float v[32];
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
           }
-          store32(p, out_row, n0 + c, row_ok, v, k0 > 0);
+          store32(p, out_row, n0 + c, row_ok, v, PIECES && k0 > 0);
         }
         fence_before();
         release_acc(acc);
@@ -578,12 +580,12 @@ bool make_map(CUtensorMap* m, const void* base, long long inner, long long rows,
   return make_tensor_map(m, base, false, inner, rows, ld, 64, box_rows);
 }
 
-template <int BN, bool A_MN, bool B_MN, int MODE>
+template <int BN, bool A_MN, bool B_MN, int MODE, bool IDX = false>
 cudaError_t launch_variant(const Ctx& c, const TcGemm& g, const CUtensorMap& ma, const CUtensorMap& mb,
                            const TcParams& p) {
   constexpr bool PAIR = MODE == 2;
   constexpr size_t kSmemBytes = MODE == 2 ? kTwoSmem : TcCfg<BN>::kSmem;
-  auto kern = tc_gemm_kernel<BN, A_MN, B_MN, MODE>;
+  auto kern = tc_gemm_kernel<BN, A_MN, B_MN, MODE, IDX>;
   // Per-device set-up, the first time each device uses this variant: the
   // shared-memory opt-in (a function attribute), and for the pair variant
   // how many 2-CTA clusters fit on the GPU at once (a persistent grid larger
@@ -669,6 +671,7 @@ cudaError_t launch_tc_gemm(const Ctx& c, const TcGemm& g) {
   }
   // dX: both K-major; dW: both MN-major; the forward's Y = X W: A K-major, B MN-major
   if (g.a_mn_major && !g.b_mn_major) return cudaErrorNotSupported;
+  if (g.c_idx && (g.a_mn_major || g.b_mn_major)) return cudaErrorNotSupported;   // (only dX has row-mapped outputs)
   // Work split (launches given stream-K scratch): the auto rule of Split --
   // whole tiles unless they would fill the waves below 60% (90% on a
   // reduction of 128+ k-slices), then a stream-K tail, decided on the device
@@ -709,11 +712,20 @@ cudaError_t launch_tc_gemm(const Ctx& c, const TcGemm& g) {
   cudaError_t e;
   const int key = (bn == 256 ? 100 : 0) + (g.a_mn_major ? 10 : (g.b_mn_major ? 20 : 0)) + mode;
   switch (key) {
-    case 0: e = launch_variant<128, false, false, 0>(c, g, ma, mb, p); break;
+    case 0:
+      e = g.c_idx ? launch_variant<128, false, false, 0, true>(c, g, ma, mb, p)
+                  : launch_variant<128, false, false, 0>(c, g, ma, mb, p);
+      break;
     case 10: e = launch_variant<128, true, true, 0>(c, g, ma, mb, p); break;
     case 20: e = launch_variant<128, false, true, 0>(c, g, ma, mb, p); break;
-    case 100: e = launch_variant<256, false, false, 0>(c, g, ma, mb, p); break;
-    case 102: e = launch_variant<256, false, false, 2>(c, g, ma, mb, p); break;
+    case 100:
+      e = g.c_idx ? launch_variant<256, false, false, 0, true>(c, g, ma, mb, p)
+                  : launch_variant<256, false, false, 0>(c, g, ma, mb, p);
+      break;
+    case 102:
+      e = g.c_idx ? launch_variant<256, false, false, 2, true>(c, g, ma, mb, p)
+                  : launch_variant<256, false, false, 2>(c, g, ma, mb, p);
+      break;
     case 110: e = launch_variant<256, true, true, 0>(c, g, ma, mb, p); break;
     case 120: e = launch_variant<256, false, true, 0>(c, g, ma, mb, p); break;
     case 122: e = launch_variant<256, false, true, 2>(c, g, ma, mb, p); break;

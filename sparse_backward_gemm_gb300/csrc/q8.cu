@@ -208,8 +208,10 @@ __global__ void __launch_bounds__(kThreads) linear_prep_kernel(LinearPrep p, int
       continue;
     }
     const int t = (part == 0 ? p.x_full : p.dy_full) ? p.idx[r] : r;
-    if ((unsigned)t >= (unsigned)p.M) {
+    if ((unsigned)t >= (unsigned)p.M) {   // reported, and a row of zeros to the GEMMs
       if (lane == 0) report_error(st, kErrBadIndex, 702);
+      if (part == 0) zero_segment(p.xk + (long long)r * p.K, v0, kv);
+      else zero_segment(p.dyk + (long long)r * p.N, v0, nv);
       continue;
     }
     if (part == 0) {

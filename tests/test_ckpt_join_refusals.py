@@ -69,6 +69,7 @@ def test_linear_arguments():
     lin(BAD, "null", idx=None)
     lin(BAD, "dX needs W", W=None)
     lin(BAD, "rows", rows=3)
+    lin(BAD, "misaligned", idx=FAKE + 2)
     lin(NO, "% 8", N=60)
     lin(BAD, "aligned", dX=FAKE + 4)
     lin(BAD, "null checkpoint", X=None)
@@ -129,6 +130,8 @@ def test_join_forward_arguments():
     fwd(BAD, "stride", d=desc(h_ld=128), h=3 * FAKE)              # in place with another stride
     fwd(BAD, "aligned", x=3 * FAKE + 2)
     fwd(BAD, "aligned", p=par(res_w=FAKE + 4))
+    fwd(BAD, "4-byte", rstd_h=FAKE + 2)
+    fwd(BAD, "stride", d=desc(x_ld=(1 << 28) + 8))
 
 
 def test_join_backward_arguments():
@@ -152,6 +155,9 @@ def test_join_backward_arguments():
     bwd(NO, "same form", sv=dict(h=None, h_ckpt=ck()))
     bwd(NO, "same form", sv=dict(h=None, h_ckpt=ck(), y=None, y_ckpt=ck(format=cl.CKPT_INT8)))
     bwd(NO, "32", d=desc(D=72), sv=dict(h=None, h_ckpt=ck(), y=None, y_ckpt=ck()))
+    bwd(BAD, "4-byte", sv=dict(rstd_y=FAKE + 1))
+    bwd(BAD, "4-byte", dgate=FAKE + 3)
+    bwd(BAD, "4-byte", idx=(FAKE + 2, FAKE, FAKE))
     bwd(BAD, "alias", dx=7 * FAKE)
     bwd(BAD, "alias", dy=8 * FAKE)
     bwd(BAD, "alias", dx=8 * FAKE, rows=(0, 1, 0))                # in place needs the same rows

@@ -259,3 +259,26 @@ def test_linear_parts_alone_and_repeat():
     assert torch.equal(db, a[2])
     assert gu.rel_err(gu.host(dX), gu.host(a[0])) <= 2.0 ** -7      # half a bf16 step each
     assert gu.rel_err(gu.host(dW), gu.host(a[1])) <= 1e-5
+
+
+def test_linear_with_a_bad_index():
+    """A kept index outside the tokens is reported; its row counts as zeros, and the other rows' results stand."""
+    M, K, N = 200, 64, 64
+    rng = np.random.default_rng(6)
+    code, exps = ock.pack(rng.normal(size=(M, K)), "int8")
+    q = cl.ckpt(cl.CKPT_INT8, torch.from_numpy(code).to(gu.DEV), torch.from_numpy(exps).to(gu.DEV))
+    W, dY = gu.bf16(rng.normal(size=(K, N))), gu.bf16(rng.normal(size=(M, N)))
+    idx = np.arange(M)
+    idx[33] = M + 7
+    ws = torch.full((cl.collider_linear_ckpt_workspace_size(M, K, N),), 255, dtype=torch.uint8, device=gu.DEV)
+    dX = torch.full((M, K), 7.0, dtype=torch.bfloat16, device=gu.DEV)
+    dW, db = torch.empty(K, N, device=gu.DEV), torch.empty(N, device=gu.DEV)
+    cl.collider_linear_bwd_ckpt(M, K, N, q, 0, W, dY, 0, gu.i32(idx), gu.i32([M]), dX, 0, dW, db, ws)
+    with pytest.raises(cl.ColliderError) as e:
+        cl.collider_check()
+    assert e.value.status == cl.ERR_INVALID_ARG
+    X, G = ock.unpack(code, exps, "int8"), gu.host(dY)
+    X[33] = G[33] = 0
+    assert gu.rel_err(gu.host(dW), X.T @ G) <= 1e-5 and gu.rel_err(gu.host(db), G.sum(0)) <= 1e-5
+    rows = [r for r in range(M) if r != 33]
+    assert gu.rel_err(gu.host(dX)[rows], (G @ gu.host(W).T)[rows]) <= 2.0 ** -7 and bool((dX[33] == 7).all())
