@@ -993,12 +993,13 @@ cudaError_t gemm_dw(const Ctx& c, int M, int Kin, int Nout, const void* Xk, long
   return launch_tc_gemm(c, g);
 }
 
-// A saved set in 8 bits: x, h and up are decoded at their FULL rows (kept rows
-// alone) into buffers of the workspace, which the block's kernels then read as
-// they read a bf16 saved set; qkv, o (and a, PHI) straight into the compact copies.
+// A saved set in 8 bits: x and h (PHI: up) are decoded at their FULL rows (kept
+// rows alone) into buffers of the workspace, which the block's kernels then read
+// as they read a bf16 saved set; qkv, o (and a, PHI) straight into the compact
+// copies; LLAMA's up by the SwiGLU backward itself.
 struct LayerCkpt {
   const collider_layer_saved_ckpt* saved;
-  __nv_bfloat16 *x, *h, *up;   // [M, D], [M, D] (LLAMA), [M, Nup]
+  __nv_bfloat16 *x, *h, *up;   // [M, D], [M, D] (LLAMA), [M, F] (PHI)
 };
 
 // dense: every token is kept (idx, cu_kept, n_kept are the identity index the
@@ -1079,8 +1080,8 @@ collider_status layer_bwd_impl(const Ctx& c_in, const collider_layer_desc* d, co
                             full ? 2 : 0, pad128(M));
   };
   if (ck) {
-    CK(decode(ck->saved->up, Nup, ck->up, true));
     if (llama) CK(decode(ck->saved->h, D, ck->h, true));
+    else CK(decode(ck->saved->up, Nup, ck->up, true));
     CK(decode(ck->saved->x, D, ck->x, true));
     if (side) CK(cudaEventRecord(side->ev[12], cs.stream));
     CK(decode(ck->saved->qkv, Nqkv, L.qkv_k, false));
@@ -1145,11 +1146,13 @@ collider_status layer_bwd_impl(const Ctx& c_in, const collider_layer_desc* d, co
     const bool s_re = !dense && !sv->s, b_re = !dense && !sv->b;
     if (!s_re) CK(gemm_dw(cs, M, F, D, L.s_k, F, L.dout_k, D, g->dw_down, n_kept, in_rows));   // dW_down = s^T dOut
     CK(gemm_dx(c, M, F, D, L.dout_k, w->w_down, L.ds_k, 1, 0, n_kept, in_rows));      // ds = dOut W_down^T
-    c.pdl = pdl_allowed() && !(ck && side);   // (not behind an event wait)
-    if (ck && side) CK(cudaStreamWaitEvent(c.stream, side->ev[12], 0));   // x, h and up are decoded
-    CK(launch_swiglu_bwd(c, L.ds_k, 1, F, static_cast<const __nv_bfloat16*>(sv->up), L.dgu_k, M, pad128(M), idx,
-                         n_kept, s_re ? L.s_k : nullptr));
     c.pdl = pdl_allowed();
+    if (ck)   // g and u straight from their codes
+      CK(launch_swiglu_bwd_ckpt(c, L.ds_k, 1, F, ck->saved->up.format, view(&ck->saved->up),
+                                ck->saved->rows == COLLIDER_ROWS_FULL, L.dgu_k, M, pad128(M), idx, n_kept, L.s_k));
+    else
+      CK(launch_swiglu_bwd(c, L.ds_k, 1, F, static_cast<const __nv_bfloat16*>(sv->up), L.dgu_k, M, pad128(M), idx,
+                           n_kept, s_re ? L.s_k : nullptr));
     CK(fork_side(c, side, 1));
     if (s_re) CK(gemm_dw(cs, M, F, D, L.s_k, F, L.dout_k, D, g->dw_down, n_kept, in_rows));
     if (!b_re) CK(gemm_dw(cs, M, D, Nup, L.b_k, D, L.dgu_k, Nup, g->dw_up, n_kept, in_rows));  // dW_up = b^T dgu
@@ -1163,8 +1166,13 @@ collider_status layer_bwd_impl(const Ctx& c_in, const collider_layer_desc* d, co
     nb.xn_out = b_re ? L.b_k : nullptr;   // b = norm2(h), recomputed
     // the column pass needs only what the row pass reads, so it is forked
     // before it and the two run side by side
+    if (ck && side) {
+      CK(cudaStreamWaitEvent(c.stream, side->ev[12], 0));   // x and h are decoded
+      c.pdl = false;   // (the next kernel follows the wait)
+    }
     CK(fork_side(c, side, 7));
     CK(launch_norm_rows(c, nb));                                                         // dh = dOut + norm2'
+    c.pdl = pdl_allowed();
     CK(launch_norm_cols(cs, nb));                                                        // dnorm2_w, beside the chain
     if (b_re) {
       CK(fork_side(c, side, 11));
@@ -1350,7 +1358,7 @@ void layer_ckpt_carve(Carver& cv, const collider_layer_desc* d, LayerBufs* L, La
   const bool llama = d->arch == COLLIDER_ARCH_LLAMA;
   ck->x = cv.take<__nv_bfloat16>(M * d->D);
   ck->h = llama ? cv.take<__nv_bfloat16>(M * d->D) : nullptr;
-  ck->up = cv.take<__nv_bfloat16>(M * (llama ? 2 : 1) * d->F);
+  ck->up = llama ? nullptr : cv.take<__nv_bfloat16>(M * d->F);
 }
 }  // namespace
 
@@ -1393,10 +1401,10 @@ extern "C" collider_status collider_layer_bwd_ckpt(const collider_layer_desc* d,
   layer_ckpt_carve(cv, d, &L, &ck);
   ck.saved = sc;
   // the saved set as the block's kernels see it: decoded rows where they are
-  // read through the index; qkv and o only by their compact copies, which the
-  // pointers here merely stand for
+  // read through the index; qkv, o and LLAMA's up are not read by these pointers,
+  // which merely stand for them
   collider_layer_saved sv{};
-  sv.x = ck.x; sv.rstd1 = sc->rstd1; sv.mean1 = sc->mean1; sv.lse = sc->lse; sv.up = ck.up;
+  sv.x = ck.x; sv.rstd1 = sc->rstd1; sv.mean1 = sc->mean1; sv.lse = sc->lse; sv.up = llama ? ck.x : ck.up;
   sv.qkv = L.qkv_k; sv.o = L.o_k;
   if (llama) {
     sv.h = ck.h; sv.rstd2 = sc->rstd2;

@@ -80,6 +80,13 @@ cudaError_t launch_compact(const Ctx& c, const uint8_t* mask, int B, int T, int3
                            int32_t* cu_kept, int32_t* n_kept, void* ws);
 
 // ---- row kernels (rows.cu) -------------------------------------------------
+// An 8-bit checkpoint (format: q8.cuh): codes [rows, code_ld] and exponent bytes [rows, exp_ld], a row's N codes and
+// N / 32 exponents (N % 32 == 0; code_ld % 16 == 0, codes 16-byte aligned)
+struct Q8View {
+  uint8_t* code;
+  uint8_t* exps;
+  long long code_ld, exp_ld;   // bytes
+};
 struct GatherJob {
   const char* src;
   char* dst;
@@ -149,6 +156,10 @@ cudaError_t launch_norm_cols(const Ctx& c, const NormBwdArgs& a);
 cudaError_t launch_swiglu_bwd(const Ctx& c, const void* ds, int ds_is_bf16, int F,
                               const __nv_bfloat16* gu, __nv_bfloat16* dgu, int M, long long cap,
                               const int32_t* idx, const int32_t* n_kept, __nv_bfloat16* s_out = nullptr);
+// the same with gu as an 8-bit checkpoint of [*, 2F] rows (q_full: read through idx)
+cudaError_t launch_swiglu_bwd_ckpt(const Ctx& c, const void* ds, int ds_is_bf16, int F, int format, const Q8View& q,
+                                   int q_full, __nv_bfloat16* dgu, int M, long long cap, const int32_t* idx,
+                                   const int32_t* n_kept, __nv_bfloat16* s_out);
 // GELU-tanh backward: df1[r] = df2[r] * gelu'(f1[idx[r]]); df2 COMPACT, f1 FULL.
 cudaError_t launch_gelu_bwd(const Ctx& c, const void* df2, int df2_is_bf16, int F,
                             const __nv_bfloat16* f1, __nv_bfloat16* df1, int M, long long cap,
@@ -310,13 +321,6 @@ cudaError_t launch_iota_cu(const Ctx& c, int B, int T, int32_t* cu);
 cudaError_t launch_identity_index(const Ctx& c, int B, int T, int32_t* idx, int32_t* cu, int32_t* nk);
 
 // ---- 8-bit activation checkpoints (q8.cu; format: q8.cuh) --------------------
-// codes [rows, code_ld] and exponent bytes [rows, exp_ld], a row's N codes and
-// N / 32 exponents (N % 32 == 0; code_ld % 16 == 0, codes 16-byte aligned)
-struct Q8View {
-  uint8_t* code;
-  uint8_t* exps;
-  long long code_ld, exp_ld;   // bytes
-};
 // row r of q = src[idx[r]] for r < n_kept (idx and n_kept null: every row)
 cudaError_t launch_q8_pack(const Ctx& c, int f32, const void* src, long long src_ld, int M, int N, const int32_t* idx,
                            const int32_t* n_kept, int format, const Q8View& q);

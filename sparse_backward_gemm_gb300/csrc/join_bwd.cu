@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(1024) join_sums_kernel(BwdArgs p) {
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
   float sum = 0.f;
   if (c < p.D) {
-#pragma unroll 4
+#pragma unroll 8
     for (long long s = s0 + ty; s < s1; s += 32) sum += part[s * p.D + c];
   }
   red[ty][tx] = sum;

@@ -6,6 +6,7 @@
 // tokens are dropped in every layer, so every kernel here touches kept rows
 // only, and COMPACT outputs are zero-padded to the GEMM tile height.
 #include "internal.h"
+#include "q8.cuh"
 
 namespace collider {
 
@@ -299,8 +300,18 @@ __global__ void __launch_bounds__(256) norm_cols_kernel(NormBwdArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// 8 values at column c of row r of an 8-bit checkpoint
+template <int FMT>
+__device__ __forceinline__ void load_ckpt8(const Q8View& q, long long r, int c, float* f) {
+  const uint2 code = *reinterpret_cast<const uint2*>(q.code + r * q.code_ld + c);
+  q8_decode8<FMT>(code, q8_scale(q.exps[r * q.exp_ld + (c >> 5)]), f);
+}
+
+// SRC: g and u as bf16 rows (kQ8Int8 + 1), or as a checkpoint of that format,
+// whose rows are FULL or COMPACT (decoding is exact in bf16: the same values)
+template <int SRC>
 __global__ void __launch_bounds__(256) swiglu_bwd_kernel(const void* __restrict__ ds, int ds_bf16, int F,
-                                                         const __nv_bfloat16* __restrict__ gu,
+                                                         const __nv_bfloat16* __restrict__ gu, Q8View q, int q_full,
                                                          __nv_bfloat16* __restrict__ dgu, int M, long long cap,
                                                          const int32_t* __restrict__ idx,
                                                          const int32_t* __restrict__ n_kept, DevStatus* st,
@@ -324,8 +335,14 @@ __global__ void __launch_bounds__(256) swiglu_bwd_kernel(const void* __restrict_
     if ((unsigned)t >= (unsigned)M) { report_error(st, kErrBadIndex, 300); continue; }
     float d[8], g[8], u[8], dg[8], du[8];
     load8(ds, ds_bf16, (long long)r * F + c, d);
-    load8(gu, 1, (long long)t * 2 * F + c, g);
-    load8(gu, 1, (long long)t * 2 * F + F + c, u);
+    if constexpr (SRC == kQ8E4m3 || SRC == kQ8Int8) {
+      const long long row = q_full ? t : r;
+      load_ckpt8<SRC>(q, row, c, g);
+      load_ckpt8<SRC>(q, row, F + c, u);
+    } else {
+      load8(gu, 1, (long long)t * 2 * F + c, g);
+      load8(gu, 1, (long long)t * 2 * F + F + c, u);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float sg = sigmoid_f(g[i]);
@@ -567,8 +584,21 @@ cudaError_t launch_swiglu_bwd(const Ctx& c, const void* ds, int ds_is_bf16, int 
                               __nv_bfloat16* dgu, int M, long long cap, const int32_t* idx, const int32_t* n_kept,
                               __nv_bfloat16* s_out) {
   prof_begin(c, "swiglu_bwd");
-  const cudaError_t e = launch_k(c, c.pdl, swiglu_bwd_kernel, dim3(grid_rows(c, cap * (F / 8), 256)), dim3(256), 0,
-                                 1, ds, ds_is_bf16, F, gu, dgu, M, cap, idx, n_kept, c.st, s_out);
+  const cudaError_t e = launch_k(c, c.pdl, swiglu_bwd_kernel<kQ8Int8 + 1>, dim3(grid_rows(c, cap * (F / 8), 256)),
+                                 dim3(256), 0, 1, ds, ds_is_bf16, F, gu, Q8View{}, 0, dgu, M, cap, idx, n_kept, c.st,
+                                 s_out);
+  prof_end(c);
+  count_launch();
+  return launched(e);
+}
+
+cudaError_t launch_swiglu_bwd_ckpt(const Ctx& c, const void* ds, int ds_is_bf16, int F, int format, const Q8View& q,
+                                   int q_full, __nv_bfloat16* dgu, int M, long long cap, const int32_t* idx,
+                                   const int32_t* n_kept, __nv_bfloat16* s_out) {
+  prof_begin(c, "swiglu_bwd");
+  auto k = format == kQ8E4m3 ? swiglu_bwd_kernel<kQ8E4m3> : swiglu_bwd_kernel<kQ8Int8>;
+  const cudaError_t e = launch_k(c, c.pdl, k, dim3(grid_rows(c, cap * (F / 8), 256)), dim3(256), 0, 1, ds, ds_is_bf16,
+                                 F, (const __nv_bfloat16*)nullptr, q, q_full, dgu, M, cap, idx, n_kept, c.st, s_out);
   prof_end(c);
   count_launch();
   return launched(e);
