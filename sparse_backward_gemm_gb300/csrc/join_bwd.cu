@@ -14,11 +14,13 @@
 // Floor: da, dH, y, h are read and dx, dy written once (12 D bytes a kept row in
 // bf16, 10 D with 8-bit y and h) beside the zeros.  What bounds it is the
 // instructions of a row at 16 warps an SM (0.45 issued a cycle and scheduler): at
-// 4 x 2048 tokens of 2048 values, 40% filtered, the whole call takes 38.3 us,
-// 3.9 TB/s of the floor's bytes.  On the way there: both row sums taken one after
+// 4 x 2048 tokens of 2048 values, 40% filtered, the whole call takes 37.4 us,
+// 3.9 TB/s of the floor's bytes (22.0 us).  On the way there: both row sums taken one after
 // the other 65 us (a row waited twice for the group), all sums at once and two
 // rows in flight 52, tensors kept in registers from a row's sums to its gradients
 // and no question asked in the row loop 42, the pre norm's weight in registers 38.
+// More CTAs an SM do not fit: above 102 registers a thread an SM's quarter holds
+// four warps.
 // Each thread owns the same columns of every row it sees and keeps their
 // parameter sums in registers; a CTA's sums are parked in the workspace and added
 // in CTA order by a second kernel, so the results do not change from run to run.
