@@ -2,12 +2,13 @@
 //
 // Collider drops the activations of filtered tokens in the backward (arXiv
 // 2502.00340, abstract), so a checkpoint needs the kept rows only, and at one
-// byte a value (plus 1/32 for the exponents) it is half as large again as in
-// bf16.  Both kernels are bound by HBM: a value moves 2 + 1.03 bytes once (4916 x
-// 11264 values: 168 MB, 25.1 us at the measured copy rate; packing takes 27.0 us,
-// unpacking 28.9).  A warp takes 1024 consecutive values of one row at a time (four 16-byte vectors a
-// lane in flight), so that one long row spreads over warps as many rows do; the
-// maximum over a group's 32 values is two shuffles among four lanes.
+// byte a value (plus 1/32 for the exponents) it is half as large as in bf16.
+// Both kernels are bound by HBM: a value moves 2 + 1.03 bytes once (4916 x 11264
+// values: 168 MB, 25.1 us at the measured copy rate; packing takes 27.0 us,
+// unpacking 28.9).  A warp takes 1024 consecutive values of one row at a time
+// (four 16-byte vectors a lane in flight), so that one long row spreads over
+// warps as many rows do; the maximum over a group's 32 values is two shuffles
+// among four lanes.
 #include "internal.h"
 #include "q8.cuh"
 
