@@ -179,6 +179,23 @@ def test_wrong_memory_is_refused():
         assert e.value.status == cl.ERR_INVALID_ARG and "memory" in str(e.value)
 
 
+def test_offsets_beyond_32_bits():
+    """Rows of values 2^28 elements apart and of codes 2^29 bytes apart: the last row of ten lies beyond 2^32 bytes."""
+    M, N = 10, 96
+    v = values(M, N, "bf16", 12)
+    big = torch.empty(M << 28, dtype=torch.bfloat16, device=gu.DEV).view(M, 1 << 28)
+    src, dst = big[:, :N], big[:, 1024:1024 + N]
+    src.copy_(dev(v, "bf16"))
+    codes = big.view(torch.uint8).view(M, 1 << 29)
+    q = cl.ckpt(cl.CKPT_E4M3, codes[:, 8192:8192 + N], codes[:, 16384:16384 + N // 32])
+    cl.collider_ckpt_pack(cl.BF16, src, 1 << 28, M, N, None, None, q)
+    cl.collider_ckpt_unpack(cl.BF16, q, cl.ROWS_FULL, M, N, None, None, dst, 1 << 28, cl.ROWS_FULL)
+    cl.collider_check()
+    c, e = ock.pack(v, "e4m3")
+    assert np.array_equal(q.buffers[0].cpu().numpy(), c) and np.array_equal(q.buffers[1].cpu().numpy(), e)
+    assert same(gu.host(dst), ock.unpack(c, e, "e4m3"))
+
+
 # --------------------------------------------------------------------------
 # linear backward from a checkpoint
 # --------------------------------------------------------------------------
@@ -282,3 +299,34 @@ def test_linear_with_a_bad_index():
     assert gu.rel_err(gu.host(dW), X.T @ G) <= 1e-5 and gu.rel_err(gu.host(db), G.sum(0)) <= 1e-5
     rows = [r for r in range(M) if r != 33]
     assert gu.rel_err(gu.host(dX)[rows], (G @ gu.host(W).T)[rows]) <= 2.0 ** -7 and bool((dX[33] == 7).all())
+
+
+def test_linear_of_many_rows():
+    """Half a million kept rows: the reduction runs in some two hundred pieces."""
+    M, K, N = 1000003, 32, 8
+    rows, idx, nk = index(M, 0.5, 3)
+    g = torch.Generator(device=gu.DEV).manual_seed(1)
+    x = (torch.randn(M, K, generator=g, device=gu.DEV) + 0.5).to(torch.bfloat16)
+    code = torch.empty(M, K, dtype=torch.uint8, device=gu.DEV)
+    exps = torch.empty(M, 1, dtype=torch.uint8, device=gu.DEV)
+    q = cl.ckpt(cl.CKPT_INT8, code, exps)
+    cl.collider_ckpt_pack(cl.BF16, x, K, M, K, None, None, q)
+    cl.collider_ckpt_unpack(cl.BF16, q, 0, M, K, None, None, x, K, 0)
+    W = torch.randn(K, N, generator=g, device=gu.DEV).to(torch.bfloat16)
+    dY = torch.randn(M, N, generator=g, device=gu.DEV).to(torch.bfloat16)
+    dX = torch.full((M, K), 7.0, dtype=torch.bfloat16, device=gu.DEV)
+    dW, db = torch.empty(K, N, device=gu.DEV), torch.empty(N, device=gu.DEV)
+    ws = torch.empty(cl.collider_linear_ckpt_workspace_size(M, K, N), dtype=torch.uint8, device=gu.DEV)
+    cl.collider_linear_bwd_ckpt(M, K, N, q, 0, W, dY, 0, idx, nk, dX, 0, dW, db, ws)
+    cl.collider_check()
+    at = torch.from_numpy(rows).to(gu.DEV)
+    xk, dk, wd = x[at].double(), dY[at].double(), W.double()
+    mag = xk.abs().T @ dk.abs()
+    # a piece's steps (2 units of 2^-23 of its magnitude each), and an f32 add of the whole for each piece
+    tol = (2 * (2560 / 16 + 1) * 2.0 ** -23 + (rows.size / 2560 + 2) * 2.0 ** -24) * mag
+    assert bool(((dW.double() - xk.T @ dk).abs() <= tol).all())
+    ref = dk @ wd.T
+    off = _mma_tol(1.0, N / 16 + 1) * (dk.abs() @ wd.abs().T)
+    assert bool(((dX[at].double() - ref).abs() <= off + 2.0 ** -8 * (ref.abs() + off)).all())
+    dX[at] = 0
+    assert bool((dX == 0).all())

@@ -332,6 +332,47 @@ def test_bit_identical_on_another_stream():
         assert v is None or torch.equal(v, again[k]), k
 
 
+def test_offsets_beyond_32_bits():
+    """Rows 2^28 elements apart: the last row of nine lies beyond 2^32 bytes.  All tensors are columns of one buffer."""
+    D, ld = 64, 1 << 28
+    c = Case(3, 3, D, gate=3, res=True, f=0.3)
+    want_f, want_b = c.forward(), c.check_backward()
+    big = torch.empty(c.M * ld, dtype=torch.bfloat16, device=gu.DEV).view(c.M, ld)
+    names = ["x", "y", "h", "a", "da", "dh", "dx", "dy"]
+    t = {k: big[:, i * D:(i + 1) * D] for i, k in enumerate(names)}
+    d = cl.ResidualNormDesc.from_buffer_copy(c.desc)
+    d.x_ld = d.y_ld = d.h_ld = d.a_ld = ld
+    for k, v in (("x", c.x), ("y", c.y), ("da", c.da), ("dh", c.dh)):
+        t[k].copy_(c.up(v))
+    ry, rh = torch.empty(c.M, device=gu.DEV), torch.empty(c.M, device=gu.DEV)
+    cl.collider_residual_norm_fwd(d, c.params, t["x"], t["y"], cl.residual_norm_out(h=t["h"], a=t["a"], rstd_y=ry, rstd_h=rh))
+    assert torch.equal(t["h"], want_f["h"]) and torch.equal(t["a"], want_f["a"]) and torch.equal(rh, want_f["rstd_h"])
+    y, h, st, _ = c.saved("rows")
+    t["h"].copy_(c.up(h))
+    km = np.flatnonzero(c.keep.reshape(-1))
+    idx = np.full(c.M, -1)
+    idx[: km.size] = km
+    G = {k: torch.empty_like(want_b[k]) for k in ("dpost_w", "dgate", "dres_w", "dpre_w")}
+    ws = torch.empty(cl.collider_residual_norm_bwd_workspace_size(d), dtype=torch.uint8, device=gu.DEV)
+    sv = cl.residual_norm_saved(x=t["x"], y=t["y"], h=t["h"], rstd_y=gu.f32(st["rstd_y"]), rstd_h=gu.f32(st["rstd_h"]))
+    cl.collider_residual_norm_bwd(d, c.params, sv, 0, t["da"], t["dh"], 0, gu.i32(idx),
+                                  gu.i32(np.concatenate([[0], np.cumsum(c.keep.sum(1))])), gu.i32([km.size]),
+                                  cl.residual_norm_grads(dx=t["dx"], dy=t["dy"], **G), 0, ws)
+    cl.collider_check()
+    for k in ("dx", "dy"):
+        assert torch.equal(t[k], want_b[k]), k
+    for k in G:
+        assert torch.equal(G[k], want_b[k]), k
+
+
+@pytest.mark.parametrize("ln", [False, True])
+def test_many_rows(ln):
+    """A sequence of 300001 tokens: column sums of some 180000 rows."""
+    c = Case(1, 300001, 8, "f32", ln, gate=1, res=True)
+    c.check_forward(c.forward())
+    c.check_backward()
+
+
 # --------------------------------------------------------------------------
 # a sandwich-normed branch: pre norm, linear branch, join; the checkpoints of its forward; its backward
 # --------------------------------------------------------------------------
