@@ -514,13 +514,14 @@ __global__ void __launch_bounds__(kThreads) join_bwd_kernel(BwdArgs p, DevStatus
 }
 
 // sums[q][c] = the parked sums added in slot order: 32 columns a block, 32
-// threads a column, each every 32nd slot, then the 32 in order.  blockIdx.y
-// counts the gradients there are, a gate by sequences as B of them.
+// threads a column, each every 32nd slot, then the 32 in order.  blockIdx.x
+// counts the gradients there are, a gate by sequences as B of them (which may be
+// more than the 65535 blocks of y).
 __global__ void __launch_bounds__(1024) join_sums_kernel(BwdArgs p) {
   __shared__ float red[32][33];
   grid_dep_wait();
   const int nk = kept(p);
-  int q = 0, b = blockIdx.y;
+  int q = 0, b = blockIdx.x;
   for (;; ++q) {
     const int n = !p.sums[q] ? 0 : (q == kGate && p.gate_rows > 1) ? p.B : 1;
     if (b < n) break;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(1024) join_sums_kernel(BwdArgs p) {
     s0 = l > f ? (cta(f) + b) * p.groups : 0;
     s1 = l > f ? (cta(l - 1) + b + 1) * p.groups : 0;
   }
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.y * 32 + tx;
   float sum = 0.f;
   if (c < p.D) {
 #pragma unroll 8
@@ -658,7 +659,7 @@ cudaError_t launch_join_bwd(const Ctx& c, const JoinBwd& j) {
   for (int q = 0; q < kSums; ++q) tasks += !p.sums[q] ? 0 : (q == kGate && j.gate_rows > 1) ? j.B : 1;
   if (tasks == 0) return cudaSuccess;
   prof_begin(c, "residual_norm_sums");
-  e = launch_k(c, pdl_allowed(), join_sums_kernel, dim3((j.D + 31) / 32, tasks), dim3(1024), 0, 1, p);
+  e = launch_k(c, pdl_allowed(), join_sums_kernel, dim3(tasks, (j.D + 31) / 32), dim3(1024), 0, 1, p);
   prof_end(c);
   count_launch();
   return launched(e);

@@ -268,6 +268,12 @@ def test_gates_of_many_sequences(B, T, D):
     c.check_backward()
 
 
+def test_gates_of_more_sequences_than_a_grid_is_high():
+    c = Case(70001, 1, 8, "f32", gate=70001, f=0.3)
+    c.check_forward(c.forward())
+    c.check_backward()
+
+
 def test_nothing_kept():
     c = Case(2, 200, 256, gate=2, res=True)
     c.keep[:] = 0
