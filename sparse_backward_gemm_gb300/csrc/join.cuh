@@ -10,6 +10,8 @@
 // lone lane, 0.2 us for each copy.
 #pragma once
 
+#include <mutex>
+
 #include "internal.h"
 #include "q8.cuh"
 #include "tc_ptx.cuh"
@@ -243,11 +245,15 @@ inline Shape make_shape(int D, int vpt, uint32_t row_bytes, size_t extra, size_t
 }
 
 // Opts kernel k in to `bytes` of dynamic shared memory on the current device,
-// once for each larger amount (`granted`: the kernel's own table).
+// once for each larger amount (`granted`: the kernel's own table).  The lock keeps
+// a second thread's smaller amount from replacing a larger one.
 inline cudaError_t grant_smem(const void* k, size_t bytes, size_t (&granted)[64]) {
+  static std::mutex lock;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || bytes <= 48 * 1024 || granted[dev & 63] >= bytes) return e;
+  if (e != cudaSuccess || bytes <= 48 * 1024) return e;
+  std::lock_guard<std::mutex> hold(lock);
+  if (granted[dev & 63] >= bytes) return e;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e == cudaSuccess) granted[dev & 63] = bytes;
   return e;
