@@ -253,8 +253,8 @@ collider_status collider_ckpt_unpack(collider_dtype dtype, const collider_ckpt* 
  * FULL or COMPACT rows: dW = X_k^T . dY_k of the decoded values, dX and db as
  * there.  The products of up to 2560 kept rows accumulate on the tensor cores
  * and are added in f32.  K % 32 == 0 (K % 8 == 0 when dW is NULL, and X may
- * be NULL then), N % 8 == 0, 1 <= M <= 2^30.  Workspace:
- * collider_linear_ckpt_workspace_size(). */
+ * be NULL then), N % 8 == 0, 1 <= M <= 2^30.  dX may be dY unless dX is FULL
+ * and dY COMPACT.  Workspace: collider_linear_ckpt_workspace_size(). */
 size_t collider_linear_ckpt_workspace_size(int M, int K, int N);
 collider_status collider_linear_bwd_ckpt(int M, int K, int N, const collider_ckpt* X, collider_rows x_rows,
                                        const void* W, const void* dY, collider_rows dy_rows,
@@ -317,10 +317,10 @@ collider_status collider_residual_norm_fwd(const collider_residual_norm_desc* de
                                            const void* y, const collider_residual_norm_out* out,
                                            void* stream);
 
-/* What the backward reads: y and h (x in the place of h when the forward had
- * no y) as rows of dtype or as 8-bit checkpoints (both in the same form, D a
- * multiple of 32; device memory), x only for dres_w; FULL or COMPACT rows.
- * The statistics are FULL [M]. */
+/* What the backward reads: y and h as rows of dtype or as 8-bit checkpoints
+ * (both in the same form, D a multiple of 32; device memory), x only for
+ * dres_w; FULL or COMPACT rows.  When the forward had no y, h is x, and x_ld
+ * and h_ld are the same.  The statistics are FULL [M]. */
 typedef struct {
   const void* x;
   const void* y;

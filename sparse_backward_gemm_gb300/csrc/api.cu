@@ -875,6 +875,8 @@ extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const c
   if (K % 8 || N % 8) return fail(COLLIDER_ERR_UNSUPPORTED, "%s: needs K, N %% 8 == 0", fn);
   if (!al16(W) || !al16(dY) || !al16(dX) || !al16(dW) || !al16(db))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  if (dX && dX == dY && dx_rows == COLLIDER_ROWS_FULL && dy_rows == COLLIDER_ROWS_COMPACT)   // (zeros are written beside dY's gather)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: a FULL dX may not alias a COMPACT dY", fn);
   collider_status s = dW ? check_ckpt(fn, X, K) : COLLIDER_OK;
   if (s != COLLIDER_OK) return s;
   const size_t need = collider_linear_ckpt_workspace_size(M, K, N);
@@ -1380,10 +1382,10 @@ extern "C" collider_status collider_layer_bwd_ckpt(const collider_layer_desc* d,
   collider_status s = check_desc(d);
   if (s != COLLIDER_OK) return s;
   if ((long long)d->B * d->T > (1 << 30)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need B*T <= 2^30", fn);
-  if (!sc || !dOut || !al16(dOut) || !idx || !cu_kept || !n_kept || !al4({idx, cu_kept, n_kept, sc->rstd1, sc->lse}))
+  if (!sc || !dOut || !al16(dOut) || !idx || !cu_kept || !n_kept || !al4({idx, cu_kept, n_kept, sc->mean1, sc->rstd1, sc->lse, sc->rstd2}))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: null saved set or index, or null or misaligned dOut, index or statistics", fn);
   const bool llama = d->arch == COLLIDER_ARCH_LLAMA;
-  if (sc->rows != COLLIDER_ROWS_FULL && sc->rows != COLLIDER_ROWS_COMPACT)
+  if (!is_rows((collider_rows)sc->rows) || !is_rows(dout_rows) || !is_rows(dx_rows))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
   const int Nqkv = (d->H + 2 * d->Hkv) * d->dh;
   s = check_ckpt(fn, &sc->x, d->D);
@@ -1826,6 +1828,8 @@ extern "C" collider_status collider_residual_norm_bwd(const collider_residual_no
   if (!pre && !dh) return fail(COLLIDER_ERR_INVALID_ARG, "%s: without a pre norm dh is needed", fn);
   if (post && (!sv->rstd_y || (ln && !sv->mean_y)))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: the post norm needs rstd_y (and mean_y for LayerNorm)", fn);
+  if (!branch && sv->h && ld.x != ld.h)
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: without y, x stands for h and needs h's row stride", fn);
   if (w->res_w && g->dres_w && !sv->x) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dres_w needs x", fn);
   if (!g->dx || (branch && !g->dy) || (!branch && g->dy))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: dx is written always, dy with y", fn);

@@ -78,6 +78,43 @@ def test_linear_arguments():
     assert cl.collider_linear_ckpt_workspace_size(8192, 2048, 5632) > 0
 
 
+def test_linear_in_place_of_compact_rows():
+    """A FULL dX gets its zeros while dY is still read: not over a COMPACT dY."""
+    for dy_rows, dx_rows, text in ((cl.ROWS_COMPACT, cl.ROWS_FULL, "alias"), (cl.ROWS_FULL, cl.ROWS_FULL, "workspace"),
+                                   (cl.ROWS_COMPACT, cl.ROWS_COMPACT, "workspace")):
+        refused(BAD, text, cl.collider_linear_bwd_ckpt, 4, 256, 256, ck(), cl.ROWS_FULL, FAKE, 2 * FAKE, dy_rows, FAKE, FAKE,
+                2 * FAKE, dx_rows, FAKE, None, None)
+
+
+def layer(arch):
+    d = cl.LayerDesc(B=1, T=64, D=256, H=4, Hkv=4, dh=64, F=256, rotary_dim=32, rope_base=1e4, eps=1e-5, arch=arch,
+                     norm=cl.NORM_RMS if arch == cl.ARCH_LLAMA else cl.NORM_LAYER,
+                     act=cl.ACT_SWIGLU if arch == cl.ARCH_LLAMA else cl.ACT_GELU_TANH)
+    q = lambda n: ck(code_ld=n, exp_ld=n // 32)  # noqa: E731
+    return d, dict(x=q(256), a=q(256), qkv=q(768), o=q(256), h=q(256), up=q(512), rstd1=FAKE, lse=FAKE, rstd2=FAKE, mean1=FAKE)
+
+
+@pytest.mark.parametrize("arch", [cl.ARCH_LLAMA, cl.ARCH_PHI])
+def test_layer_arguments(arch):
+    d, saved = layer(arch)
+
+    def run(status, text, dout_rows=cl.ROWS_FULL, dx_rows=cl.ROWS_FULL, idx=FAKE, **kw):
+        sc = cl.LayerSavedCkpt(rows=cl.ROWS_FULL)
+        for k, v in dict(saved, **kw).items():
+            setattr(sc, k, v)
+        refused(status, text, cl.collider_layer_bwd_ckpt, d, cl.LayerWeights(), sc, FAKE, dout_rows, idx, FAKE, FAKE,
+                cl.LayerGrads(), dx_rows, None)
+    run(BAD, "workspace")
+    run(BAD, "rows", rows=2)
+    run(BAD, "rows", dout_rows=2)
+    run(BAD, "rows", dx_rows=-1)
+    run(BAD, "null", idx=None)
+    run(NO, "format", x=ck(format=3))
+    run(BAD, "codes", qkv=ck())
+    for k in ("mean1", "rstd1", "lse", "rstd2"):
+        run(BAD, "misaligned", **{k: FAKE + 2})
+
+
 def desc(**kw):
     return cl.ResidualNormDesc(**dict(dict(dtype=cl.BF16, B=2, T=8, D=64, norm=cl.NORM_RMS, post=1, pre=1, eps=1e-5,
                                            res_scale=1.0, gate_rows=1), **kw))
@@ -162,6 +199,9 @@ def test_join_backward_arguments():
     bwd(BAD, "alias", dy=8 * FAKE)
     bwd(BAD, "alias", dx=8 * FAKE, rows=(0, 1, 0))                # in place needs the same rows
     bwd(BAD, "workspace", dx=8 * FAKE)
+    first = dict(p=par(post_w=None, gate=None), sv=dict(y=None, rstd_y=None), dy=None)   # without y, x stands for h
+    bwd(BAD, "workspace", d=desc(post=0, gate_rows=0, x_ld=128, h_ld=128), **first)
+    bwd(BAD, "row stride", d=desc(post=0, gate_rows=0, x_ld=128), **first)
 
 
 def test_binding_helpers():
