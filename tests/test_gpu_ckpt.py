@@ -330,3 +330,84 @@ def test_linear_of_many_rows():
     assert bool(((dX[at].double() - ref).abs() <= off + 2.0 ** -8 * (ref.abs() + off)).all())
     dX[at] = 0
     assert bool((dX == 0).all())
+
+
+@pytest.mark.parametrize("dy_rows,dx_rows", [(0, 0), (1, 1), (0, 1)])
+def test_linear_dx_in_the_place_of_dy(dy_rows, dx_rows):
+    """dX over dY, in the layouts that may: the same bits as apart from it."""
+    M, K = 700, 512
+    rng = np.random.default_rng(9)
+    rows, idx, nk = index(M, 0.4, 2)
+    code, exps = (torch.from_numpy(t).to(gu.DEV) for t in ock.pack(rng.normal(size=(M, K)), "e4m3"))
+    q = cl.ckpt(cl.CKPT_E4M3, code, exps)
+    W, dY = gu.bf16(rng.normal(size=(K, K))), gu.bf16(rng.normal(size=(M, K)))
+    ws = torch.empty(cl.collider_linear_ckpt_workspace_size(M, K, K), dtype=torch.uint8, device=gu.DEV)
+    got = []
+    for apart in (True, False):
+        g = dY.clone()
+        dX = torch.empty_like(g) if apart else g
+        dW, db = torch.empty(K, K, device=gu.DEV), torch.empty(K, device=gu.DEV)
+        cl.collider_linear_bwd_ckpt(M, K, K, q, 0, W, g, dy_rows, idx, nk, dX, dx_rows, dW, db, ws)
+        cl.collider_check()
+        n = M if dx_rows == 0 else min(-(-rows.size // 128) * 128, M)
+        got.append((dX[:n], dW, db))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_calls_of_two_threads():
+    """Two host threads, each with its own stream, buffers and workspace, issue the linear backward and the join's
+    together, the wider one's first calls among them; both get the bits that calls one after the other give."""
+    import threading
+
+    def work(D, seed):
+        M, K, N = 600, D, 256
+        rng = np.random.default_rng(seed)
+        rows, idx, nk = index(M, 0.4, seed)
+        cu = gu.i32([0, rows.size])
+        code, exps = (torch.from_numpy(t).to(gu.DEV) for t in ock.pack(rng.normal(size=(M, K)), "int8"))
+        q = cl.ckpt(cl.CKPT_INT8, code, exps)
+        W, dY = gu.bf16(rng.normal(size=(K, N))), gu.bf16(rng.normal(size=(M, N)))
+        y, da, dh = (gu.bf16(rng.normal(size=(M, D))) for _ in range(3))
+        w, rstd = gu.bf16(np.ones(D)), torch.ones(M, device=gu.DEV)
+        d = cl.ResidualNormDesc(dtype=cl.BF16, B=1, T=M, D=D, norm=cl.NORM_RMS, post=1, pre=1, eps=1e-5, res_scale=1.0)
+        p = cl.residual_norm_params(post_w=w, pre_w=w)
+        sv = cl.residual_norm_saved(y=y, h=da, rstd_y=rstd, rstd_h=rstd)
+        ws = torch.empty(cl.collider_linear_ckpt_workspace_size(M, K, N), dtype=torch.uint8, device=gu.DEV)
+        wj = torch.empty(cl.collider_residual_norm_bwd_workspace_size(d), dtype=torch.uint8, device=gu.DEV)
+
+        def run(stream):
+            outs = []
+            for _ in range(20):
+                dX, dx, dy = (torch.empty(M, D, dtype=torch.bfloat16, device=gu.DEV) for _ in range(3))
+                dW, db, dw = (torch.empty(s, device=gu.DEV) for s in ((K, N), (N,), (D,)))
+                g = cl.residual_norm_grads(dx=dx, dy=dy, dpre_w=dw)
+                cl.collider_linear_bwd_ckpt(M, K, N, q, 0, W, dY, 0, idx, nk, dX, 0, dW, db, ws, stream=stream)
+                cl.collider_residual_norm_bwd(d, p, sv, 0, da, dh, 0, idx, cu, nk, g, 0, wj, stream=stream)
+                outs.append((dX, dW, db, dx, dy, dw))
+            return outs
+        return run
+    runs = [work(1024, 1), work(6144, 2)]
+    streams = [torch.cuda.Stream() for _ in runs]
+    got = [None, None]
+    gate = threading.Barrier(2, timeout=60)
+
+    def body(i):
+        with torch.cuda.stream(streams[i]):
+            gate.wait()
+            got[i] = runs[i](streams[i].cuda_stream)
+            streams[i].synchronize()
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    cl.collider_check()
+    for i, run in enumerate(runs):
+        assert got[i] is not None
+        want = run(0)[0]
+        torch.cuda.synchronize()
+        for outs in got[i]:
+            for a, b in zip(outs, want):
+                assert torch.equal(a, b)
