@@ -1833,9 +1833,11 @@ extern "C" collider_status collider_residual_norm_bwd(const collider_residual_no
   if (w->res_w && g->dres_w && !sv->x) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dres_w needs x", fn);
   if (!g->dx || (branch && !g->dy) || (!branch && g->dy))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: dx is written always, dy with y", fn);
-  const int src = pre && sv->h_ckpt ? sv->h_ckpt->format : branch && sv->y_ckpt ? sv->y_ckpt->format : 2;
-  if (branch && pre && (sv->y_ckpt ? sv->y_ckpt->format : 2) != src)
+  // of each tensor that is read: its checkpoint's format, or 2 for rows
+  const int y_form = sv->y_ckpt ? sv->y_ckpt->format : 2, h_form = sv->h_ckpt ? sv->h_ckpt->format : 2;
+  if (branch && pre && y_form != h_form)
     return fail(COLLIDER_ERR_UNSUPPORTED, "%s: y and h must be saved in the same form", fn);
+  const int src = branch ? y_form : h_form;
   if (branch && sv->y_ckpt) s = check_ckpt(fn, sv->y_ckpt, d->D);
   if (s == COLLIDER_OK && pre && sv->h_ckpt) s = check_ckpt(fn, sv->h_ckpt, d->D);
   if (s != COLLIDER_OK) return s;
