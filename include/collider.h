@@ -253,8 +253,9 @@ collider_status collider_ckpt_unpack(collider_dtype dtype, const collider_ckpt* 
  * FULL or COMPACT rows: dW = X_k^T . dY_k of the decoded values, dX and db as
  * there.  The products of up to 2560 kept rows accumulate on the tensor cores
  * and are added in f32.  K % 32 == 0 (K % 8 == 0 when dW is NULL, and X may
- * be NULL then), N % 8 == 0, 1 <= M <= 2^30.  dX may be dY unless dX is FULL
- * and dY COMPACT.  Workspace: collider_linear_ckpt_workspace_size(). */
+ * be NULL then), N % 8 == 0, 1 <= M <= 2^30.  dX may be dY, a FULL dX only a
+ * FULL dY with K == N; it may not overlap X.  Workspace:
+ * collider_linear_ckpt_workspace_size(). */
 size_t collider_linear_ckpt_workspace_size(int M, int K, int N);
 collider_status collider_linear_bwd_ckpt(int M, int K, int N, const collider_ckpt* X, collider_rows x_rows,
                                        const void* W, const void* dY, collider_rows dy_rows,

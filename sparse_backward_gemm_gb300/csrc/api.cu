@@ -104,6 +104,11 @@ bool al4(std::initializer_list<const void*> ps) {
   for (const void* p : ps) u |= reinterpret_cast<uintptr_t>(p);
   return (u & 3) == 0;
 }
+// whether [a, a + an) and [b, b + bn) share a byte
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + bn && q < p + an;
+}
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 long long pad128(long long m) { return (m + 127) & ~127ll; }
 
@@ -882,6 +887,17 @@ extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const c
   const size_t need = collider_linear_ckpt_workspace_size(M, K, N);
   if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
+  // A FULL dX is zeroed while dY is gathered: over a FULL dY only row for row
+  // (the zeroed rows are then none that is read).  Either dX is written while X
+  // is decoded.  Of COMPACT rows, whose number the host does not know, the first.
+  if (dX) {
+    const size_t dx_bytes = (dx_rows == COLLIDER_ROWS_FULL ? (size_t)M : 1) * K * 2,
+                 dy_bytes = (dy_rows == COLLIDER_ROWS_FULL ? (size_t)M : 1) * N * 2;
+    if (dx_rows == COLLIDER_ROWS_FULL && !(dX == dY && K == N) && overlap(dX, dx_bytes, dY, dy_bytes))
+      return fail(COLLIDER_ERR_INVALID_ARG, "%s: a FULL dX may alias dY only as the same rows (K == N)", fn);
+    if (dW && (overlap(dX, dx_bytes, X->code, K) || overlap(dX, dx_bytes, X->exps, K / 32)))
+      return fail(COLLIDER_ERR_INVALID_ARG, "%s: dX may not alias X", fn);
+  }
   Ctx c;
   s = make_ctx(stream, &c);
   if (s == COLLIDER_OK) s = check_memory(fn, {W, dY, idx, n_kept, dX, dW, db, ws});
