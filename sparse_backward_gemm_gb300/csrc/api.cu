@@ -1866,12 +1866,18 @@ extern "C" collider_status collider_residual_norm_bwd(const collider_residual_no
       (g->dx == dh && (in_rows != out_rows || ld.x != ld.h)))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: of the outputs only dx may alias an input: dh, of the same rows and stride",
                 fn);
+  // (a saved row may be read after a row of an output is written)
+  const bool want_res = w->res_w && g->dres_w;
+  const collider_ckpt *yq = branch ? sv->y_ckpt : nullptr, *hq = pre ? sv->h_ckpt : nullptr;
+  for (const void* p : {static_cast<const void*>(g->dx), static_cast<const void*>(g->dy)})
+    if (p && ((want_res && p == sv->x) || p == sv->y || (pre && p == sv->h) || (yq && (p == yq->code || p == yq->exps)) ||
+              (hq && (p == hq->code || p == hq->exps))))
+      return fail(COLLIDER_ERR_INVALID_ARG, "%s: dx and dy may not alias the saved tensors", fn);
   const size_t need = collider_residual_norm_bwd_workspace_size(d);
   if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
   Ctx c;
   s = make_ctx(stream, &c);
-  const bool want_res = w->res_w && g->dres_w;
   JoinBwd j{};
   j.f32 = d->dtype == COLLIDER_F32; j.layer_norm = ln; j.B = d->B; j.T = d->T; j.D = d->D;
   j.alpha = d->res_scale; j.gate_rows = d->gate_rows; j.post = post; j.pre = pre;
