@@ -335,7 +335,8 @@ typedef struct {
 } collider_residual_norm_saved;
 
 /* dx and dy (with y) of dtype; the parameters' gradients f32, [D], dgate
- * [gate_rows, D], overwritten; NULL ones are not computed. */
+ * [gate_rows, D], overwritten; NULL ones are not computed, and those of
+ * parameters that the call does not have (biases: LayerNorm's) must be NULL. */
 typedef struct {
   void* dx;
   void* dy;

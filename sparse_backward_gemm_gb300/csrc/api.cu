@@ -1847,6 +1847,9 @@ extern "C" collider_status collider_residual_norm_bwd(const collider_residual_no
   if (!branch && sv->h && ld.x != ld.h)
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: without y, x stands for h and needs h's row stride", fn);
   if (w->res_w && g->dres_w && !sv->x) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dres_w needs x", fn);
+  if ((!post && (g->dpost_w || g->dpost_b)) || (!pre && (g->dpre_w || g->dpre_b)) || (!d->gate_rows && g->dgate) ||
+      (!w->res_w && g->dres_w) || (!ln && (g->dpost_b || g->dpre_b)))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: a gradient is given of a parameter that the call does not ask for", fn);
   if (!g->dx || (branch && !g->dy) || (!branch && g->dy))
     return fail(COLLIDER_ERR_INVALID_ARG, "%s: dx is written always, dy with y", fn);
   // of each tensor that is read: its checkpoint's format, or 2 for rows
@@ -1900,9 +1903,8 @@ extern "C" collider_status collider_residual_norm_bwd(const collider_residual_no
   j.out_full = out_rows == COLLIDER_ROWS_FULL;
   j.idx = idx; j.cu = cu_kept; j.nk = n_kept;
   j.dx = g->dx; j.dy = g->dy;
-  j.dpre_w = pre ? g->dpre_w : nullptr; j.dpre_b = pre && ln ? g->dpre_b : nullptr;
-  j.dpost_w = post ? g->dpost_w : nullptr; j.dpost_b = post && ln ? g->dpost_b : nullptr;
-  j.dgate = d->gate_rows ? g->dgate : nullptr; j.dres_w = want_res ? g->dres_w : nullptr;
+  j.dpre_w = g->dpre_w; j.dpre_b = g->dpre_b; j.dpost_w = g->dpost_w; j.dpost_b = g->dpost_b;
+  j.dgate = g->dgate; j.dres_w = g->dres_w;
   j.part = static_cast<float*>(ws);
   if (s == COLLIDER_OK) s = check_join_memory(fn, w);
   if (s == COLLIDER_OK)
