@@ -219,7 +219,9 @@ collider_status collider_linear_bwd(collider_dtype dtype, int M, int K, int N,
  * nearest code, ties to even, and stores e + 127; a group that holds a NaN or
  * an infinity gets byte 255 and codes 0, and decodes to NaN everywhere.  So a
  * value v is kept to within 2^-4 |v| or 2^(e-10) (e4m3), 2^(e-1) (int8),
- * whichever is larger, and decoding is exact in bf16 and f32.
+ * whichever is larger, and decoding is exact in bf16 and f32.  Next to 2^128
+ * values are kept finite: e4m3 codes end at 240 where e = 120 (within 2^-4 |v|
+ * still), int8 has e <= 121, and |v| > 127.5 2^121 is kept as 127 2^121.
  * code and exps are device memory, or pinned host memory that the device
  * addresses at the same pointer (an offloaded checkpoint).  Rows are code_ld
  * and exp_ld bytes apart: code 16-byte aligned, code_ld a multiple of 16. */

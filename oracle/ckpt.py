@@ -2,8 +2,10 @@
 with explicit arithmetic (test infrastructure only).
 
 A group is 32 consecutive values of a row.  Its exponent is the smallest e >= -120 with max|v| <= L 2^e (L = 448
-for e4m3, 127 for int8); a code is v 2^-e rounded to the nearest representable value, ties to even; the byte is
-e + 127.  A group with a NaN or an infinity: byte 255, codes 0, decodes to NaN.
+for e4m3, 127 for int8), for int8 121 at most; a code is v 2^-e rounded to the nearest representable value, ties to
+even, but none whose value would be 2^128: there the largest that decodes to a finite value (240 under e = 120 for
+e4m3, 127 under e = 121 for int8).  The byte is e + 127.  A group with a NaN or an infinity: byte 255, codes 0,
+decodes to NaN.
 """
 from __future__ import annotations
 
@@ -12,6 +14,8 @@ import numpy as np
 GROUP = 32
 E_MIN = -120
 LIMIT = {"e4m3": 448.0, "int8": 127.0}
+E_TOP = {"e4m3": 120, "int8": 121}       # the largest exponent, and
+TOP_CODE = {"e4m3": 240.0, "int8": 127.0}   # the largest code under it
 
 
 def e4m3_round(q):
@@ -52,8 +56,10 @@ def pack(v, fmt):
     big = np.where(fine, big, 0.0)
     m, e = np.frexp(big / LIMIT[fmt])                    # the quotient is m 2^e: a power of two exactly when m = 1/2
     e = np.maximum(np.where(m > 0.5, e, e - 1), E_MIN)
-    e = np.where(big > 0, e, E_MIN)
+    e = np.minimum(np.where(big > 0, e, E_MIN), E_TOP[fmt])
     q = np.where(fine[..., None], g, 0.0) * np.ldexp(1.0, -e)[..., None]
+    lim = np.where(e == E_TOP[fmt], TOP_CODE[fmt], np.inf)[..., None]
+    q = np.clip(q, -lim, lim)
     code = e4m3_code(e4m3_round(q)) if fmt == "e4m3" else np.rint(q).astype(np.int8).view(np.uint8)
     return code.reshape(rows, N), np.where(fine, e + 127, 255).astype(np.uint8)
 

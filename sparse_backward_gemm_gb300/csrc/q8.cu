@@ -118,6 +118,10 @@ __global__ void __launch_bounds__(kThreads) q8_pack_kernel(const T* __restrict__
       raw[k].values(f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] *= inv;
+      if (byte == kQ8TopByte<FMT>) {   // values next to 2^128
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i], -kQ8TopCode<FMT>), kQ8TopCode<FMT>);
+      }
       uint2 c = q8_encode8<FMT>(f);
       if (byte == 255) c = make_uint2(0, 0);
       if (v0 + 32 * k < vecs) {

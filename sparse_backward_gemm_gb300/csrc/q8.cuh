@@ -5,7 +5,9 @@
 // 8-bit value (448 for e4m3, 127 for int8); a code is v * 2^-e rounded to the
 // nearest 8-bit value, ties to even, and the exponent is kept as the byte
 // e + 127.  A group that holds a NaN or an infinity gets the byte 255 and
-// decodes to NaN everywhere.
+// decodes to NaN everywhere.  At the top of the range no code stands for 2^128,
+// which is no bf16 or f32 number: int8 exponents end at 121, and the codes under
+// the largest exponent at 240 (e4m3) and 127.
 //
 // Why a power of two and not max|v| / L: scaling by it is exact, so a code is
 // one rounding of v with no case that depends on how a division rounds, and
@@ -24,6 +26,11 @@ namespace collider {
 constexpr int kQ8Group = 32;
 constexpr int kQ8E4m3 = 0, kQ8Int8 = 1;
 
+// the largest exponent byte (but 255), and the largest code value under it
+template <int FMT>
+constexpr int kQ8TopByte = FMT == kQ8E4m3 ? 247 : 248;
+template <int FMT>
+constexpr float kQ8TopCode = FMT == kQ8E4m3 ? 240.f : 127.f;
 // exponent byte of a group whose largest magnitude is amax >= 0 (NaN or
 // infinite: 255).  amax = 1.f * 2^(E-127): L = 1.75 * 2^8 or 1.984375 * 2^6.
 template <int FMT>
@@ -31,9 +38,9 @@ __device__ __forceinline__ int q8_exp_byte(float amax) {
   const unsigned u = __float_as_uint(amax) & 0x7fffffffu;
   if (u >= 0x7f800000u) return 255;
   const int E = (int)(u >> 23), over = (u & 0x7fffffu) > (FMT == kQ8E4m3 ? 0x600000u : 0x7e0000u);
-  return max(E + over - (FMT == kQ8E4m3 ? 8 : 6), 7);
+  return min(max(E + over - (FMT == kQ8E4m3 ? 8 : 6), 7), kQ8TopByte<FMT>);
 }
-// 2^-(byte - 127) for a byte q8_exp_byte gave (7..250)
+// 2^-(byte - 127) for a byte q8_exp_byte gave (7..248)
 __device__ __forceinline__ float q8_inv_scale(int byte) { return __uint_as_float((unsigned)(254 - byte) << 23); }
 // 2^(byte - 127) for any byte; 255 is NaN
 __device__ __forceinline__ float q8_scale(unsigned byte) {
