@@ -246,7 +246,9 @@ collider_status collider_ckpt_pack(collider_dtype dtype, const void* src, size_t
  * dst_ld elements).  src_rows: the checkpoint holds FULL rows (read through
  * idx) or COMPACT ones.  dst_rows FULL: kept row r goes to row idx[r], every
  * other row is written 0; COMPACT: to row r, with zero rows up to the next
- * multiple of 128.  idx and n_kept NULL: all M rows, in order. */
+ * multiple of 128.  idx and n_kept NULL: all M rows, in order.  A kept index
+ * outside the M rows is reported by collider_check; packing skips its row, and
+ * a COMPACT dst looked up through it gets a row of zeros. */
 collider_status collider_ckpt_unpack(collider_dtype dtype, const collider_ckpt* src, collider_rows src_rows,
                                    int M, int N, const int32_t* idx, const int32_t* n_kept, void* dst,
                                    size_t dst_ld, collider_rows dst_rows, void* stream);

@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kThreads) q8_unpack_kernel(Q8View q, int src_f
       t = idx[r];
       if ((unsigned)t >= (unsigned)M) {
         if (lane == 0) report_error(st, kErrBadIndex, 701);
+        if (!dst_full) zero_segment(dst + (long long)r * dst_ld, v0, vecs);   // a row of zeros to who reads it next
         continue;
       }
     }
