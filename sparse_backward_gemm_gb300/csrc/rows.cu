@@ -5,6 +5,8 @@
 // multiple of the SM count.  Collider (abstract): the activations of filtered
 // tokens are dropped in every layer, so every kernel here touches kept rows
 // only, and COMPACT outputs are zero-padded to the GEMM tile height.
+#include <algorithm>
+
 #include "internal.h"
 #include "q8.cuh"
 
@@ -135,28 +137,30 @@ __global__ void __launch_bounds__(256) scatter_kernel(const char* __restrict__ c
 // ---------------------------------------------------------------------------
 // column sums: pass 1 over blocks of kColRows rows, pass 2 fixed-order reduce
 constexpr int kColRows = 16;
+constexpr int kMaxGridY = 65535;
 
 __global__ void __launch_bounds__(256) colsum_part_kernel(const void* __restrict__ X, int is_bf16, long long ld,
-                                                          int N, const int32_t* __restrict__ gidx,
+                                                          int M, int N, const int32_t* __restrict__ gidx,
                                                           const int32_t* __restrict__ n_kept,
                                                           float* __restrict__ part) {
-  const int nk = *n_kept;
-  const int r0 = blockIdx.y * kColRows;
-  if (r0 >= nk) return;
+  const int nk = min(*n_kept, M);
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
   if (c >= N) return;
-  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  const int r1 = min(nk, r0 + kColRows);
-  for (int r = r0; r < r1; ++r) {
-    float f[8];
-    const long long row = gidx ? gidx[r] : r;
-    load8(X, is_bf16, row * ld + c, f);
+  // (a grid is at most 65535 blocks high: 1,048,560 rows a round)
+  for (long long b = blockIdx.y; b * kColRows < nk; b += gridDim.y) {
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int r0 = (int)b * kColRows, r1 = min(nk, r0 + kColRows);
+    for (int r = r0; r < r1; ++r) {
+      float f[8];
+      const long long row = gidx ? gidx[r] : r;
+      load8(X, is_bf16, row * ld + c, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += f[i];
+      for (int i = 0; i < 8; ++i) acc[i] += f[i];
+    }
+    float4* p = reinterpret_cast<float4*>(part + b * N + c);
+    p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
   }
-  float4* p = reinterpret_cast<float4*>(part + (long long)blockIdx.y * N + c);
-  p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
 }
 
 // out[c] = sum over partial rows i < ceil(n_kept / rows_per_part) of
@@ -536,9 +540,9 @@ size_t colsum_part_floats(int M, int N) {
 
 cudaError_t launch_colsum(const Ctx& c, const void* X, int x_is_bf16, long long ld, int M, int N,
                           const int32_t* gidx, const int32_t* n_kept, float* part, float* out) {
-  dim3 g1((N / 8 + 255) / 256, (M + kColRows - 1) / kColRows);
+  const dim3 g1((N / 8 + 255) / 256, std::min((M + kColRows - 1) / kColRows, kMaxGridY));
   prof_begin(c, "colsum");
-  colsum_part_kernel<<<g1, 256, 0, c.stream>>>(X, x_is_bf16, ld, N, gidx, n_kept, part);
+  colsum_part_kernel<<<g1, 256, 0, c.stream>>>(X, x_is_bf16, ld, M, N, gidx, n_kept, part);
   colsum_reduce_kernel<<<(N + 31) / 32, 256, 0, c.stream>>>(part, N, N, kColRows, n_kept, out);
   prof_end(c);
   count_launch(2);
