@@ -271,35 +271,36 @@ __global__ void __launch_bounds__(kNormWarps * 32) norm_rows_kernel(NormBwdArgs 
 }
 
 __global__ void __launch_bounds__(256) norm_cols_kernel(NormBwdArgs a) {
-  const int nk = *a.n_kept;
-  const int r0 = blockIdx.y * kNormColRows;
-  if (r0 >= nk) return;
+  const int nk = min(*a.n_kept, a.M);
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
   if (c >= a.D) return;
-  float dg[8] = {0, 0, 0, 0, 0, 0, 0, 0}, db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  const int r1 = min(nk, r0 + kNormColRows);
-  for (int r = r0; r < r1; ++r) {
-    const int t = a.idx[r];
-    if ((unsigned)t >= (unsigned)a.M) continue;   // reported by the row kernel
-    const float rstd = a.rstd[t];
-    const float mu = a.layer_norm ? a.mean[t] : 0.f;
-    float dy[8], xv[8];
-    norm_dy8(a, (long long)r * a.D + c, dy);
-    load8(a.x, 1, (long long)t * a.D + c, xv);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      dg[k] += dy[k] * (xv[k] - mu) * rstd;
-      db[k] += dy[k];
-    }
-  }
   const int nsets = a.layer_norm ? 2 : 1;
-  float4* p = reinterpret_cast<float4*>(a.part + ((long long)blockIdx.y * nsets) * a.D + c);
-  p[0] = make_float4(dg[0], dg[1], dg[2], dg[3]);
-  p[1] = make_float4(dg[4], dg[5], dg[6], dg[7]);
-  if (nsets == 2) {
-    float4* q = reinterpret_cast<float4*>(a.part + ((long long)blockIdx.y * nsets + 1) * a.D + c);
-    q[0] = make_float4(db[0], db[1], db[2], db[3]);
-    q[1] = make_float4(db[4], db[5], db[6], db[7]);
+  // (as in the column sums: rounds of at most 65535 parts)
+  for (long long b = blockIdx.y; b * kNormColRows < nk; b += gridDim.y) {
+    float dg[8] = {0, 0, 0, 0, 0, 0, 0, 0}, db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int r0 = (int)b * kNormColRows, r1 = min(nk, r0 + kNormColRows);
+    for (int r = r0; r < r1; ++r) {
+      const int t = a.idx[r];
+      if ((unsigned)t >= (unsigned)a.M) continue;   // reported by the row kernel
+      const float rstd = a.rstd[t];
+      const float mu = a.layer_norm ? a.mean[t] : 0.f;
+      float dy[8], xv[8];
+      norm_dy8(a, (long long)r * a.D + c, dy);
+      load8(a.x, 1, (long long)t * a.D + c, xv);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dg[k] += dy[k] * (xv[k] - mu) * rstd;
+        db[k] += dy[k];
+      }
+    }
+    float4* p = reinterpret_cast<float4*>(a.part + (b * nsets) * a.D + c);
+    p[0] = make_float4(dg[0], dg[1], dg[2], dg[3]);
+    p[1] = make_float4(dg[4], dg[5], dg[6], dg[7]);
+    if (nsets == 2) {
+      float4* q = reinterpret_cast<float4*>(a.part + (b * nsets + 1) * a.D + c);
+      q[0] = make_float4(db[0], db[1], db[2], db[3]);
+      q[1] = make_float4(db[4], db[5], db[6], db[7]);
+    }
   }
 }
 
@@ -565,8 +566,8 @@ cudaError_t launch_norm_rows(const Ctx& c, const NormBwdArgs& a) {
 cudaError_t launch_norm_cols(const Ctx& c, const NormBwdArgs& a) {
   const int nsets = a.layer_norm ? 2 : 1;
   prof_begin(c, "norm_bwd");
-  norm_cols_kernel<<<dim3((a.D / 8 + 255) / 256, (unsigned)((a.cap + kNormColRows - 1) / kNormColRows)), 256, 0,
-                     c.stream>>>(a);
+  const long long parts = std::min<long long>((a.cap + kNormColRows - 1) / kNormColRows, kMaxGridY);
+  norm_cols_kernel<<<dim3((a.D / 8 + 255) / 256, (unsigned)parts), 256, 0, c.stream>>>(a);
   // partials are laid out [part][set][D] with set 0 = dgamma, set 1 = dbeta
   const int g = (a.D + 31) / 32;
   colsum_reduce_kernel<<<g, 256, 0, c.stream>>>(a.part, a.D, (long long)nsets * a.D, kNormColRows, a.n_kept,
