@@ -543,7 +543,10 @@ typedef struct {
  * (beside the first GEMM) and everything else is that call, so the gradients
  * are bit-identical to its on the decoded values (LLAMA: with a, b and s
  * recomputed).  A filtered call: idx, cu_kept and n_kept are given.  B*T <=
- * 2^30.  Workspace: collider_layer_ckpt_workspace_size. */
+ * 2^30.  After a kept index outside the tokens (collider_check reports it), in
+ * this call and in collider_layer_bwd, dx holds for the sequences without one
+ * alone, and the parameters' gradients are not defined.  Workspace:
+ * collider_layer_ckpt_workspace_size. */
 size_t collider_layer_ckpt_workspace_size(const collider_layer_desc* desc);
 collider_status collider_layer_bwd_ckpt(const collider_layer_desc* desc,
                                         const collider_layer_weights* w,

@@ -84,6 +84,11 @@ __global__ void attn_prep_kernel(AttnK p, int DH, float rope_base, float2* rope)
   for (long long e = tid; e < (long long)p.H * nk; e += stride) {
     const int h = (int)(e / nk), r = (int)(e % nk);
     const int t = p.idx[r];
+    if ((unsigned)t >= (unsigned)p.M) {   // reported; as a query it weighs nothing
+      if (h == 0) report_error(p.st, kErrBadIndex, 600);
+      p.lse2[(long long)h * p.M + r] = INFINITY;
+      continue;
+    }
     const int b = t / p.T, ti = t % p.T;
     p.lse2[(long long)h * p.M + r] = p.lse[((long long)b * p.H + h) * p.T + ti] * kLog2e;
   }
@@ -179,7 +184,8 @@ __global__ void attn_finalize_kernel(AttnK p, int DH) {
     __nv_bfloat16* o = which == 0 ? p.dq + (long long)r * p.dq_ld + h * DH
                                   : (which == 1 ? p.dk : p.dv) + (long long)r * p.dkv_ld + h * DH;
     const int use_rh = which == 2 ? 0 : rh;
-    const float2* rope_row = use_rh ? p.rope + (long long)(p.idx[r] % p.T) * rh : nullptr;
+    const int t = use_rh ? p.idx[r] : 0;   // (an index outside the tokens, reported by the preparation: position 0)
+    const float2* rope_row = use_rh ? p.rope + (long long)((unsigned)t < (unsigned)p.M ? t % p.T : 0) * rh : nullptr;
     finalize_unit(a, o, u, use_rh, rope_row, which == 2 ? 1.f : p.scale);
   }
   // zero padding rows, 16 bytes at a time
