@@ -20,6 +20,15 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(SimtGemm g, DevStatus* s
     if (g.dyn == 1) M = min(M, nk);
     else K = min(K, nk);
   }
+  // the row that position i stands for; -1 (and reported) where the index names
+  // none of the `rows` there are: its values count as zeros, its output is skipped
+  auto token = [&](int through, int i, int rows) -> long long {
+    if (!through) return i;
+    const int t = g.idx[i];
+    if ((unsigned)t < (unsigned)rows) return t;
+    report_error(st, kErrBadIndex, 50);
+    return -1;
+  };
   const int m0 = blockIdx.y * TM, n0 = blockIdx.x * TN;
   if (m0 >= M) return;
   __shared__ float As[TK][TM + 4];
@@ -34,10 +43,8 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(SimtGemm g, DevStatus* s
       const int m = m0 + mm, k = k0 + kk;
       float v = 0.f;
       if (m < M && k < K) {
-        long long row, col;
-        if (!g.a_trans) { row = g.a_gather ? g.idx[m] : m; col = k; }
-        else { row = g.a_gather ? g.idx[k] : k; col = m; }
-        v = g.A[row * g.lda + col];
+        const long long row = !g.a_trans ? token(g.a_gather, m, g.M) : token(g.a_gather, k, g.K);
+        if (row >= 0) v = g.A[row * g.lda + (!g.a_trans ? k : m)];
       }
       As[kk][mm] = v;
       // B tile: element (k, n)
@@ -47,7 +54,10 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(SimtGemm g, DevStatus* s
       float w = 0.f;
       if (n < g.N && k2 < K) {
         if (!g.b_trans) w = g.B[(long long)n * g.ldb + k2];
-        else w = g.B[(long long)(g.b_gather ? g.idx[k2] : k2) * g.ldb + n];
+        else {
+          const long long row = token(g.b_gather, k2, g.K);
+          if (row >= 0) w = g.B[row * g.ldb + n];
+        }
       }
       Bs[kk][nn] = w;
     }
@@ -70,14 +80,14 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(SimtGemm g, DevStatus* s
   for (int i = 0; i < 4; ++i) {
     const int m = m0 + ty * 4 + i;
     if (m >= M) continue;
-    const long long orow = g.c_scatter ? g.idx[m] : m;
+    const long long orow = token(g.c_scatter, m, g.M);
+    if (orow < 0) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = n0 + tx * 4 + j;
       if (n < g.N) g.C[orow * g.ldc + n] = acc[i][j];
     }
   }
-  (void)st;
 }
 
 }  // namespace

@@ -142,7 +142,7 @@ constexpr int kMaxGridY = 65535;
 __global__ void __launch_bounds__(256) colsum_part_kernel(const void* __restrict__ X, int is_bf16, long long ld,
                                                           int M, int N, const int32_t* __restrict__ gidx,
                                                           const int32_t* __restrict__ n_kept,
-                                                          float* __restrict__ part) {
+                                                          float* __restrict__ part, DevStatus* st) {
   const int nk = min(*n_kept, M);
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
   if (c >= N) return;
@@ -153,6 +153,10 @@ __global__ void __launch_bounds__(256) colsum_part_kernel(const void* __restrict
     for (int r = r0; r < r1; ++r) {
       float f[8];
       const long long row = gidx ? gidx[r] : r;
+      if ((unsigned long long)row >= (unsigned long long)M) {
+        if (c == 0) report_error(st, kErrBadIndex, 51);
+        continue;
+      }
       load8(X, is_bf16, row * ld + c, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] += f[i];
@@ -543,7 +547,7 @@ cudaError_t launch_colsum(const Ctx& c, const void* X, int x_is_bf16, long long 
                           const int32_t* gidx, const int32_t* n_kept, float* part, float* out) {
   const dim3 g1((N / 8 + 255) / 256, std::min((M + kColRows - 1) / kColRows, kMaxGridY));
   prof_begin(c, "colsum");
-  colsum_part_kernel<<<g1, 256, 0, c.stream>>>(X, x_is_bf16, ld, M, N, gidx, n_kept, part);
+  colsum_part_kernel<<<g1, 256, 0, c.stream>>>(X, x_is_bf16, ld, M, N, gidx, n_kept, part, c.st);
   colsum_reduce_kernel<<<(N + 31) / 32, 256, 0, c.stream>>>(part, N, N, kColRows, n_kept, out);
   prof_end(c);
   count_launch(2);
