@@ -466,15 +466,20 @@ __global__ void __launch_bounds__(256) embed_bwd_kernel(const __nv_bfloat16* __r
   if ((unsigned)t >= (unsigned)M) { if (threadIdx.x == 0) report_error(st, kErrBadIndex, 500); return; }
   const int id = ids[t];
   if ((unsigned)id >= (unsigned)V) { if (threadIdx.x == 0) report_error(st, kErrBadIndex, 501); return; }
+  // whether kept row q is of this id (an index outside the tokens, which its own block reports, is of none)
+  auto is_id = [&](int q) {
+    const int tq = idx[q];
+    return (unsigned)tq < (unsigned)M && ids[tq] == id;
+  };
   int dup = 0;
-  for (int q = threadIdx.x; q < r; q += blockDim.x) dup |= (ids[idx[q]] == id);
+  for (int q = threadIdx.x; q < r; q += blockDim.x) dup |= is_id(q);
   if (__syncthreads_or(dup)) return;
   // this block owns id; accumulate its rows in ascending order
   const int c0 = threadIdx.x * 8;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int base = r; base < nk; base += blockDim.x) {
     const int q = base + threadIdx.x;
-    const int hit = (q < nk) && (ids[idx[q]] == id);
+    const int hit = q < nk && is_id(q);
     // ordered compaction of this chunk's hits
     const unsigned bal = __ballot_sync(0xffffffffu, hit);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
