@@ -256,7 +256,7 @@ collider_status collider_ckpt_unpack(collider_dtype dtype, const collider_ckpt* 
 /* collider_linear_bwd (bf16) with X [M, K] saved as an 8-bit checkpoint of
  * FULL or COMPACT rows: dW = X_k^T . dY_k of the decoded values, dX and db as
  * there.  The products of up to 2560 kept rows accumulate on the tensor cores
- * and are added in f32.  K % 32 == 0 (K % 8 == 0 when dW is NULL, and X may
+ * and are added in f32 (dW on normal inputs: within 1e-6 of its norm).  K % 32 == 0 (K % 8 == 0 when dW is NULL, and X may
  * be NULL then), N % 8 == 0, 1 <= M <= 2^30.  dX may be dY, a FULL dX only a
  * FULL dY with K == N; it may not overlap X.  Workspace:
  * collider_linear_ckpt_workspace_size(). */

@@ -917,9 +917,10 @@ extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const c
   // The weight gradient's part runs on the side stream: X is decoded and dX's
   // filtered rows are zeroed beside the dX GEMM, and the dW GEMM's first tiles
   // take the SMs that the dX GEMM's last wave leaves.  Against one stream, with
-  // the three copies in one launch, 40% filtered: 172 and 179 us at 8192 rows x
-  // 5632 x 2048, 170 and 193 at 8192 x 2048 x 5632, 213 and 209 at 8192 x 1536 x
-  // 8960, 44 and 43 at 2048^3, 16 and 22 at 128 x 256 x 256.
+  // the three copies in one launch, 40% filtered: 171 and 178 us at 8192 rows x
+  // 5632 x 2048, 172 and 193 at 8192 x 2048 x 5632, 215 and 208 at 8192 x 1536 x
+  // 8960 (the one shape that loses by it), 35 and 35 at 2048^3, 12 and 18 at 128
+  // x 256 x 256; 358 and 378 at 65536 x 256 x 256, nothing filtered.
   Ctx cs = c;
   Side* side = nullptr;
   if (dX && dW) {
@@ -939,9 +940,11 @@ extern "C" collider_status collider_linear_bwd_ckpt(int M, int K, int N, const c
   }
   Ctx cp = c;
   cp.pdl = pdl_allowed();
-  // Whole tiles only: on the block shapes and down to 128 x 256 x 256 a
-  // stream-K tail never made these launches faster (2048 x 2048 x 2048, 1229
-  // rows kept: 57 us without, 82 us with; 128 x 256 x 256: 31 and 51 us).
+  // Whole tiles only: a stream-K tail is not cut into the pieces that bound dW's
+  // error (below), and gains little.  The call with one on dW's whole reduction:
+  // 167 us at 8192 x 5632 x 2048, 169 at 8192 x 2048 x 5632, 211 at 8192 x 1536 x
+  // 8960, but 39 at 2048^3, 27 at 128 x 256 x 256 and 408 at 65536 x 256 x 256 (a
+  // dW of one tile, whose 26 pieces one pair of CTAs takes one after the other).
   if (dX) {
     TcGemm g{};
     g.M = M; g.N = K; g.K = N;

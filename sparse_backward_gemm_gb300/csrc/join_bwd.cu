@@ -13,9 +13,9 @@
 //
 // Floor: da, dH, y, h are read and dx, dy written once (12 D bytes a kept row in
 // bf16, 10 D with 8-bit y and h) beside the zeros.  What bounds it is the
-// instructions of a row at 16 warps an SM (0.45 issued a cycle and scheduler): at
-// 4 x 2048 tokens of 2048 values, 40% filtered, the whole call takes 37.4 us,
-// 3.9 TB/s of the floor's bytes (22.0 us).  On the way there: both row sums taken one after
+// instructions of a row at 16 warps an SM (0.50 issued a cycle and scheduler): at
+// 4 x 2048 tokens of 2048 values, 40% filtered, the whole call takes 37.0 us,
+// 4.0 TB/s of the floor's bytes (22.0 us).  On the way there: both row sums taken one after
 // the other 65 us (a row waited twice for the group), all sums at once and two
 // rows in flight 52, tensors kept in registers from a row's sums to its gradients
 // and no question asked in the row loop 42, the pre norm's weight in registers 38.
@@ -596,7 +596,8 @@ BwdShape bwd_shape(int D, uint32_t bytes, bool eight, bool layer_norm, bool by_s
   const Shape t = make_shape(D, vpt, 16, 0, 0);
   const uint32_t stage = t.tpr * vpt * 8 * bytes + t.tpr / 32 * kHeadBytes + (eight ? exps_bytes(t.tpr, vpt) : 0);
   b.own = by_seq ? (size_t)t.groups * t.tpr * vpt * 8 * 4 * (layer_norm ? 2 : 1) : 0;
-  // (64 KB of ring a CTA: more stages only lengthen the start.  4 x 2048 tokens of 2048 values: 42.4 us, 45.3 at 112 KB)
+  // (64 KB of ring a CTA: more stages only lengthen the start.  4 x 2048 tokens of 2048 values: 37.0 us, 39.1 at
+  // 112 KB; 2 x 4096 of 1536, y and h in 8 bits: 39.2 and 39.1)
   b.s = make_shape(D, vpt, stage, b.own, 64 * 1024 + b.own);
   if (b.s.stages < 2) b.s = make_shape(D, vpt, stage, b.own, (b.ctas == 2 ? 112 : 224) * 1024);
   const size_t line = head_bytes(t.groups) + b.own + (t.groups > 1 ? (size_t)kSums * t.groups * D * 4 : 0);

@@ -10,7 +10,7 @@
 // f32; h and a are rounded once each.
 //
 // Floor: x and y are read and h and a written once, 8 D bytes a row in bf16:
-// 20.0 us for 8192 rows of 2048 values, which take 25.0 us (5.4 TB/s); the
+// 20.0 us for 8192 rows of 2048 values, which take 24.9 us (5.4 TB/s); the
 // instructions of a row at 16 warps an SM are next.  On the way there 61 us
 // (parameters read again for every row, scalar arithmetic), 29 (two vectors a
 // thread, packed arithmetic, cp.async), 25 (the pre norm's weight in registers).

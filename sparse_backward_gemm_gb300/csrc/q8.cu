@@ -4,8 +4,8 @@
 // 2502.00340, abstract), so a checkpoint needs the kept rows only, and at one
 // byte a value (plus 1/32 for the exponents) it is half as large as in bf16.
 // Both kernels are bound by HBM: a value moves 2 + 1.03 bytes once (4916 x 11264
-// values: 168 MB, 25.1 us at the measured copy rate; packing takes 27.0 us,
-// unpacking 28.9).  A warp takes 1024 consecutive values of one row at a time
+// values: 168 MB, 25.1 us at the measured copy rate; packing takes 26.1 us,
+// unpacking 28.5).  A warp takes 1024 consecutive values of one row at a time
 // (four 16-byte vectors a lane in flight), so that one long row spreads over
 // warps as many rows do; the maximum over a group's 32 values is two shuffles
 // among four lanes.
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) linear_prep_kernel(LinearPrep p, int
 
 // blocks of x: a warp a row, up to per_sm blocks an SM in all; of y: row
 // segments.  More blocks than an SM holds keep more loads in flight (packing
-// 4916 x 11264 values: 27.0 us at 32 an SM, 28.9 at 8; unpacking 28.9 and 31.1);
+// 4916 x 11264 values: 26.1 us at 32 an SM, 28.2 at 8; unpacking 28.5 and 30.6);
 // the copies beside a GEMM do best with fewer.
 constexpr int kManyPerSm = 32, kFewPerSm = 4;
 int segments(int N) { return (N / 8 + kSegVecs - 1) / kSegVecs; }
