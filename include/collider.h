@@ -66,6 +66,8 @@ typedef enum { COLLIDER_ARCH_LLAMA = 0, COLLIDER_ARCH_PHI = 1 } collider_arch;
 typedef enum { COLLIDER_NORM_RMS = 0, COLLIDER_NORM_LAYER = 1 } collider_norm;
 typedef enum { COLLIDER_ACT_SWIGLU = 0, COLLIDER_ACT_GELU_TANH = 1 } collider_act;
 typedef enum { COLLIDER_CKPT_E4M3 = 0, COLLIDER_CKPT_INT8 = 1 } collider_ckpt_format;
+typedef enum { COLLIDER_GLU_SILU = 0, COLLIDER_GLU_GELU_TANH = 1 } collider_glu;
+typedef enum { COLLIDER_GRAD_NORM_L2 = 0, COLLIDER_GRAD_NORM_MAX = 1 } collider_grad_norm_kind;
 
 /* ------------------------------------------------------------------------ */
 /* Status                                                                    */
@@ -621,6 +623,90 @@ size_t collider_layer_fwd_workspace_size(const collider_layer_desc* desc);
 collider_status collider_layer_fwd(const collider_layer_desc* desc, const collider_layer_params* w,
                                    const void* x, void* y, const collider_layer_acts* acts,
                                    void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gated feed-forward block (the pages have no counterpart: a decoder block's */
+/* MLP by itself, for blocks that are put together outside collider_layer_*)  */
+/* ------------------------------------------------------------------------ */
+
+/* For a row x of D values, W_up [D, 2F] = [gate | up] and W_down [F, D]:
+ *   [g | u] = x W_up;  s = act(g) . u;  y = s W_down     (. element-wise)
+ * act: SiLU, g / (1 + e^-g), or GELU in its tanh form.  All tensors bf16. */
+typedef struct {
+  int M;             /* tokens: 1 <= M <= 2^30 */
+  int D, F;          /* width and hidden width: multiples of 8, at most 2^20 */
+  int act;           /* collider_glu */
+  int grad_dtype;    /* collider_dtype of dw_up and dw_down */
+  int x_ld, up_ld, y_ld; /* row strides in elements of x and dx, of up, of y and
+                            dy: multiples of 8, at most 2^28; 0: D, 2F, D */
+} collider_ffn_desc;
+
+/* All M rows (the forward stays dense).  up [M, 2F] = [g | u] is what the
+ * backward reads; NULL: not kept.  g and u are f32 until s is formed; s is
+ * rounded to bf16 for the second product, which the tensor cores take in bf16,
+ * and each output is rounded once.  The outputs overlap each other and the
+ * inputs nowhere.  Workspace: collider_ffn_fwd_workspace_size(). */
+size_t collider_ffn_fwd_workspace_size(const collider_ffn_desc* desc);
+collider_status collider_ffn_fwd(const collider_ffn_desc* desc, const void* x, const void* w_up,
+                                 const void* w_down, void* up, void* y, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* Backward on the kept rows, from x, up as the forward stored it, and dy:
+ *   ds = dy W_down^T;  dg = ds . u . act'(g);  du = ds . act(g)
+ *   dx = [dg | du] W_up^T;  dW_up = x^T [dg | du];  dW_down = s^T dy
+ * Of these [dg | du] and s (formed again from up) are rounded to bf16 for the
+ * products; ds stays f32.  So f32 weight gradients carry the rounding of bf16
+ * factors too.  saved_rows: x and up hold M (FULL, read through idx) or n_kept
+ * (COMPACT) rows; dy_rows and dx_rows likewise; the filtered rows of a FULL dx
+ * are written 0.  idx (ascending) and n_kept both NULL: every token is kept.
+ * dx NULL, dw_up NULL, dw_down NULL: not wanted (x may then be NULL without
+ * dw_up, w_up without dx).  Outputs are overwritten, and overlap each other and
+ * the inputs nowhere.  Every sum has a fixed order: bit-identical from run to
+ * run.  A kept index outside the tokens is reported by collider_check; its row
+ * counts as zeros.  Workspace: collider_ffn_bwd_workspace_size(). */
+size_t collider_ffn_bwd_workspace_size(const collider_ffn_desc* desc);
+collider_status collider_ffn_bwd(const collider_ffn_desc* desc, const void* w_up, const void* w_down,
+                                 const void* x, const void* up, collider_rows saved_rows, const void* dy,
+                                 collider_rows dy_rows, const int32_t* idx, const int32_t* n_kept, void* dx,
+                                 collider_rows dx_rows, void* dw_up, void* dw_down, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norm of a list of gradients, and clipping (the pages have no counterpart: */
+/* what a training step does with the gradients before it applies them)       */
+/* ------------------------------------------------------------------------ */
+
+/* One gradient: n contiguous values of dtype (COLLIDER_F32 or COLLIDER_BF16,
+ * both may occur in a list), aligned to their size.  n = 0 is allowed. */
+typedef struct {
+  void* data;
+  long long n;
+  int dtype;
+} collider_grad;
+
+/* norm[0] = scale (sum of g^2 over all gradients)^(1/2), or scale max |g|
+ * (kind); norms[i] (may be NULL, as may norm): the same of gradient i alone; f32, device.
+ * scale (finite, > 0) stands for what the gradients are still to be multiplied
+ * by, such as one over the number of summed micro-batches.  Sums are held in
+ * f64, and squares too where f32's would overflow or vanish: the norm is finite
+ * wherever it fits f32.  A NaN gives NaN.  Bit-identical from run to run.
+ * grads is a host array of count (0 <= count <= 2^20) gradients, read during
+ * the call only; at most 2^40 values in all.  A gradient listed twice counts
+ * twice.  Workspace: collider_grad_norm_workspace_size(). */
+size_t collider_grad_norm_workspace_size(const collider_grad* grads, int count);
+collider_status collider_grad_norm(const collider_grad* grads, int count, int kind, float scale, float* norm,
+                                   float* norms, void* ws, size_t ws_bytes, void* stream);
+
+/* The norm as above, then every gradient in place
+ *   g <- coef g,  coef = scale min(1, max_norm / (norm + 1e-6)),
+ * in f32, rounded to the gradient's type once.  coef (f32 [1], device), norm
+ * and norms may be NULL.  If the norm is not finite, the gradients are left as
+ * they were and coef is 0: the step is to be skipped.  A coef of 1 writes
+ * nothing.  max_norm >= 0, infinity allowed (no clipping).  The gradients
+ * overlap each other and the outputs nowhere.  Workspace as for the norm. */
+collider_status collider_grad_clip(const collider_grad* grads, int count, int kind, float scale, float max_norm,
+                                   float* norm, float* norms, float* coef, void* ws, size_t ws_bytes,
+                                   void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Whole stack: embedding -> L blocks -> final RMSNorm -> LM head -> CE      */

@@ -24,6 +24,8 @@ Modules:
   ops         linear, RMSNorm, LayerNorm, SwiGLU, GELU-tanh, RoPE, CE, rounding
   attention   dense causal GQA forward (saved o, lse) and filtered backward
   block       decoder-block forward (saved set) and filtered backward
+  ffn         gated feed-forward block and its filtered backward
+  grads       norm of a list of gradients, clipping
   stack       L-block stack + final norm + LM head + embedding
 
 Pins: every function here is checked in ``tests/test_oracle_*.py`` against

@@ -31,6 +31,9 @@ __all__ = [
     "collider_attn_workspace_size", "collider_attn_bwd", "collider_layer_workspace_size",
     "collider_layer_bwd", "collider_layer_fwd_workspace_size", "collider_layer_fwd",
     "collider_stack_workspace_size", "collider_stack_bwd",
+    "GLU_SILU", "GLU_GELU_TANH", "GRAD_NORM_L2", "GRAD_NORM_MAX", "FfnDesc", "Grad", "grad_list",
+    "collider_ffn_fwd_workspace_size", "collider_ffn_fwd", "collider_ffn_bwd_workspace_size", "collider_ffn_bwd",
+    "collider_grad_norm_workspace_size", "collider_grad_norm", "collider_grad_clip",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcollider.so")
@@ -43,6 +46,8 @@ ARCH_LLAMA, ARCH_PHI = 0, 1
 NORM_RMS, NORM_LAYER = 0, 1
 ACT_SWIGLU, ACT_GELU_TANH = 0, 1
 CKPT_E4M3, CKPT_INT8 = 0, 1
+GLU_SILU, GLU_GELU_TANH = 0, 1
+GRAD_NORM_L2, GRAD_NORM_MAX = 0, 1
 
 
 class ColliderError(RuntimeError):
@@ -117,6 +122,15 @@ class ResidualNormGrads(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("dx", "dy", "dpost_w", "dpost_b", "dgate", "dres_w", "dpre_w", "dpre_b")]
 
 
+class FfnDesc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("M", "D", "F", "act", "grad_dtype", "x_ld", "up_ld", "y_ld")]
+
+
+class Grad(C.Structure):
+    """One gradient of a list (``collider_grad``); see :func:`grad_list`."""
+    _fields_ = [("data", C.c_void_p), ("n", C.c_longlong), ("dtype", C.c_int)]
+
+
 P = C.c_void_p
 I = C.c_int
 SZ = C.c_size_t
@@ -163,6 +177,13 @@ _SIGS = {
     "collider_stack_workspace_size": (SZ, [C.POINTER(LayerDesc), I, I]),
     "collider_stack_bwd": (I, [C.POINTER(LayerDesc), I, I, C.POINTER(LayerWeights), C.POINTER(LayerSaved),
                                P, P, P, P, P, P, P, P, P, P, P, C.POINTER(LayerGrads), P, P, P, P, SZ, P]),
+    "collider_ffn_fwd_workspace_size": (SZ, [C.POINTER(FfnDesc)]),
+    "collider_ffn_fwd": (I, [C.POINTER(FfnDesc), P, P, P, P, P, P, SZ, P]),
+    "collider_ffn_bwd_workspace_size": (SZ, [C.POINTER(FfnDesc)]),
+    "collider_ffn_bwd": (I, [C.POINTER(FfnDesc), P, P, P, P, I, P, I, P, P, P, I, P, P, P, SZ, P]),
+    "collider_grad_norm_workspace_size": (SZ, [C.POINTER(Grad), I]),
+    "collider_grad_norm": (I, [C.POINTER(Grad), I, I, C.c_float, P, P, P, SZ, P]),
+    "collider_grad_clip": (I, [C.POINTER(Grad), I, I, C.c_float, C.c_float, P, P, P, P, SZ, P]),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -450,3 +471,49 @@ def collider_stack_bwd(desc, L, V, weights, saved, logits, targets, ids, y, xL, 
                                     _ptr(y), _ptr(xL), _ptr(rstdf), _ptr(normf_w), _ptr(w_lm), _ptr(idx),
                                     _ptr(cu_kept), _ptr(n_kept), grads, _ptr(dnormf_w), _ptr(dw_lm), _ptr(dE),
                                     _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def collider_ffn_fwd_workspace_size(desc: FfnDesc) -> int:
+    return lib().collider_ffn_fwd_workspace_size(C.byref(desc))
+
+
+def collider_ffn_fwd(desc, x, w_up, w_down, up, y, ws, stream=None) -> None:
+    _check(lib().collider_ffn_fwd(C.byref(desc), _ptr(x), _ptr(w_up), _ptr(w_down), _ptr(up), _ptr(y), _ptr(ws),
+                                  _nbytes(ws), _stream(stream)))
+
+
+def collider_ffn_bwd_workspace_size(desc: FfnDesc) -> int:
+    return lib().collider_ffn_bwd_workspace_size(C.byref(desc))
+
+
+def collider_ffn_bwd(desc, w_up, w_down, x, up, saved_rows, dy, dy_rows, idx, n_kept, dx, dx_rows, dw_up, dw_down, ws,
+                     stream=None) -> None:
+    _check(lib().collider_ffn_bwd(C.byref(desc), _ptr(w_up), _ptr(w_down), _ptr(x), _ptr(up), saved_rows, _ptr(dy),
+                                  dy_rows, _ptr(idx), _ptr(n_kept), _ptr(dx), dx_rows, _ptr(dw_up), _ptr(dw_down),
+                                  _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def grad_list(tensors):
+    """The array of :class:`Grad` of these contiguous f32 or bf16 tensors; it keeps them alive."""
+    import torch
+    dtypes = {torch.float32: F32, torch.bfloat16: BF16}
+    for t in tensors:
+        if t.dtype not in dtypes or not t.is_contiguous():
+            raise TypeError("gradients are contiguous f32 or bf16 tensors")
+    a = (Grad * len(tensors))(*[Grad(t.data_ptr(), t.numel(), dtypes[t.dtype]) for t in tensors])
+    a.buffers = tuple(tensors)
+    return a
+
+
+def collider_grad_norm_workspace_size(grads, count) -> int:
+    return lib().collider_grad_norm_workspace_size(grads, count)
+
+
+def collider_grad_norm(grads, count, kind, scale, norm, norms, ws, stream=None) -> None:
+    _check(lib().collider_grad_norm(grads, count, kind, scale, _ptr(norm), _ptr(norms), _ptr(ws), _nbytes(ws),
+                                    _stream(stream)))
+
+
+def collider_grad_clip(grads, count, kind, scale, max_norm, norm, norms, coef, ws, stream=None) -> None:
+    _check(lib().collider_grad_clip(grads, count, kind, scale, max_norm, _ptr(norm), _ptr(norms), _ptr(coef), _ptr(ws),
+                                    _nbytes(ws), _stream(stream)))

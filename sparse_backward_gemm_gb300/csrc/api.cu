@@ -12,6 +12,7 @@
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -1916,4 +1917,314 @@ extern "C" collider_status collider_residual_norm_bwd(const collider_residual_no
   if (s != COLLIDER_OK) return s;
   CK(launch_join_bwd(c, j));
   return COLLIDER_OK;
+}
+
+// ===========================================================================
+// gated feed-forward block
+// ===========================================================================
+namespace {
+struct FfnLd {
+  long long x, up, y;
+};
+collider_status check_ffn_desc(const char* fn, const collider_ffn_desc* d, FfnLd* ld) {
+  if (!d) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null desc", fn);
+  if (d->act != COLLIDER_GLU_SILU && d->act != COLLIDER_GLU_GELU_TANH)
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: act %d", fn, d->act);
+  if (d->grad_dtype != COLLIDER_F32 && d->grad_dtype != COLLIDER_BF16)
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: grad_dtype %d", fn, d->grad_dtype);
+  if (d->M < 1 || d->M > (1 << 30)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need 1 <= M <= 2^30", fn);
+  if (d->D < 8 || d->D % 8 || d->D > (1 << 20) || d->F < 8 || d->F % 8 || d->F > (1 << 20))
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: D and F must be multiples of 8, at least 8 and at most 2^20", fn);
+  if (d->x_ld < 0 || d->up_ld < 0 || d->y_ld < 0) return fail(COLLIDER_ERR_INVALID_ARG, "%s: negative row stride", fn);
+  *ld = FfnLd{d->x_ld ? d->x_ld : d->D, d->up_ld ? d->up_ld : 2ll * d->F, d->y_ld ? d->y_ld : d->D};
+  if (ld->x < d->D || ld->x % 8 || ld->x > (1 << 28) || ld->up < 2ll * d->F || ld->up % 8 || ld->up > (1 << 28) ||
+      ld->y < d->D || ld->y % 8 || ld->y > (1 << 28))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: row strides must be at least the rows, multiples of 8 and at most 2^28", fn);
+  return COLLIDER_OK;
+}
+
+// memory that a call reads or writes
+struct Extent {
+  const void* p;
+  size_t bytes;
+};
+Extent rows_extent(const void* p, long long rows, long long ld, long long width, int esz = 2) {
+  return Extent{p, p ? (size_t)((rows - 1) * ld + width) * esz : 0};
+}
+// no output shares a byte with an input or another output
+bool any_overlap(std::initializer_list<Extent> out, std::initializer_list<Extent> in) {
+  for (const Extent* a = out.begin(); a != out.end(); ++a) {
+    if (!a->p) continue;
+    for (const Extent* b = a + 1; b != out.end(); ++b)
+      if (b->p && overlap(a->p, a->bytes, b->p, b->bytes)) return true;
+    for (const Extent& b : in)
+      if (b.p && overlap(a->p, a->bytes, b.p, b.bytes)) return true;
+  }
+  return false;
+}
+
+struct FfnFwdBufs {
+  float* acc;          // [M, 2F]
+  __nv_bfloat16* s;    // [M, F]
+};
+size_t ffn_fwd_carve(Carver& cv, const collider_ffn_desc* d, FfnFwdBufs* b) {
+  b->acc = cv.take<float>((size_t)d->M * 2 * d->F);
+  b->s = cv.take<__nv_bfloat16>((size_t)d->M * d->F);
+  return cv.used;
+}
+struct FfnBwdBufs {
+  __nv_bfloat16 *xk, *dyk;   // kept rows of x and dy, zero-padded to 128 rows
+  float* ds;                 // [Mp, F]
+  __nv_bfloat16 *dgu, *s;    // [Mp, 2F], [Mp, F]
+};
+size_t ffn_bwd_carve(Carver& cv, const collider_ffn_desc* d, FfnBwdBufs* b) {
+  const size_t Mp = (size_t)pad128(d->M);
+  b->xk = cv.take<__nv_bfloat16>(Mp * d->D);
+  b->dyk = cv.take<__nv_bfloat16>(Mp * d->D);
+  b->ds = cv.take<float>(Mp * d->F);
+  b->dgu = cv.take<__nv_bfloat16>(Mp * 2 * d->F);
+  b->s = cv.take<__nv_bfloat16>(Mp * d->F);
+  return cv.used;
+}
+}  // namespace
+
+extern "C" size_t collider_ffn_fwd_workspace_size(const collider_ffn_desc* d) {
+  FfnLd ld;
+  if (check_ffn_desc("collider_ffn_fwd_workspace_size", d, &ld) != COLLIDER_OK) return 0;
+  Carver cv{nullptr, 0, 0, true};
+  FfnFwdBufs b;
+  return ffn_fwd_carve(cv, d, &b);
+}
+
+extern "C" collider_status collider_ffn_fwd(const collider_ffn_desc* d, const void* x, const void* w_up,
+                                            const void* w_down, void* up, void* y, void* ws, size_t ws_bytes,
+                                            void* stream) {
+  static const char* fn = "collider_ffn_fwd";
+  FfnLd ld;
+  collider_status s = check_ffn_desc(fn, d, &ld);
+  if (s != COLLIDER_OK) return s;
+  if (!x || !w_up || !w_down || !y) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null x, w_up, w_down or y", fn);
+  for (const void* p : {x, w_up, w_down, static_cast<const void*>(up), static_cast<const void*>(y)})
+    if (!al16(p)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  const int M = d->M, D = d->D, F = d->F;
+  if (any_overlap({rows_extent(up, M, ld.up, 2 * F), rows_extent(y, M, ld.y, D)},
+                  {rows_extent(x, M, ld.x, D), rows_extent(w_up, D, 2 * F, 2 * F), rows_extent(w_down, F, D, D)}))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: up and y may not alias each other or an input", fn);
+  const size_t need = collider_ffn_fwd_workspace_size(d);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
+  Ctx c;
+  s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_memory(fn, {x, w_up, w_down, up, y, ws});
+  if (s != COLLIDER_OK) return s;
+  Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
+  FfnFwdBufs b;
+  ffn_fwd_carve(cv, d, &b);
+  TcGemm g{};
+  g.M = M; g.N = 2 * F; g.K = D;
+  g.A = x; g.lda = ld.x; g.a_rows = M;
+  g.B = w_up; g.ldb = 2 * F; g.b_mn_major = 1; g.b_rows = D;
+  g.C = b.acc; g.ldc = 2 * F; g.c_rows = M;
+  CK(launch_tc_gemm(c, g));
+  CK(launch_glu_fwd(c, d->act, M, F, b.acc, static_cast<__nv_bfloat16*>(up), ld.up, b.s));
+  g = TcGemm{};
+  g.M = M; g.N = D; g.K = F;
+  g.A = b.s; g.lda = F; g.a_rows = M;
+  g.B = w_down; g.ldb = D; g.b_mn_major = 1; g.b_rows = F;
+  g.C = y; g.ldc = ld.y; g.c_bf16 = 1; g.c_rows = M;
+  CK(launch_tc_gemm(c, g));
+  return COLLIDER_OK;
+}
+
+extern "C" size_t collider_ffn_bwd_workspace_size(const collider_ffn_desc* d) {
+  FfnLd ld;
+  if (check_ffn_desc("collider_ffn_bwd_workspace_size", d, &ld) != COLLIDER_OK) return 0;
+  Carver cv{nullptr, 0, 0, true};
+  FfnBwdBufs b;
+  return ffn_bwd_carve(cv, d, &b);
+}
+
+extern "C" collider_status collider_ffn_bwd(const collider_ffn_desc* d, const void* w_up, const void* w_down,
+                                            const void* x, const void* up, collider_rows saved_rows, const void* dy,
+                                            collider_rows dy_rows, const int32_t* idx, const int32_t* n_kept, void* dx,
+                                            collider_rows dx_rows, void* dw_up, void* dw_down, void* ws, size_t ws_bytes,
+                                            void* stream) {
+  static const char* fn = "collider_ffn_bwd";
+  FfnLd ld;
+  collider_status s = check_ffn_desc(fn, d, &ld);
+  if (s != COLLIDER_OK) return s;
+  if (!w_down || !up || !dy) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null w_down, up or dy", fn);
+  if (dx && !w_up) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dx needs w_up", fn);
+  if (dw_up && !x) return fail(COLLIDER_ERR_INVALID_ARG, "%s: dw_up needs x", fn);
+  if (!is_rows(saved_rows) || !is_rows(dy_rows) || !is_rows(dx_rows))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: rows are FULL or COMPACT", fn);
+  if (!idx != !n_kept) return fail(COLLIDER_ERR_INVALID_ARG, "%s: only one of idx and n_kept given", fn);
+  for (const void* p : {w_up, w_down, x, up, dy, static_cast<const void*>(dx), static_cast<const void*>(dw_up),
+                        static_cast<const void*>(dw_down)})
+    if (!al16(p)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  if (!al4({idx, n_kept})) return fail(COLLIDER_ERR_INVALID_ARG, "%s: a misaligned index", fn);
+  const int M = d->M, D = d->D, F = d->F, gsz = d->grad_dtype == COLLIDER_F32 ? 4 : 2;
+  const bool kept = idx != nullptr;
+  // (of COMPACT rows, whose number the host does not know, the first)
+  auto rows = [&](collider_rows r) { return kept && r == COLLIDER_ROWS_COMPACT ? 1 : M; };
+  if (any_overlap({rows_extent(dx, rows(dx_rows), ld.x, D), rows_extent(dw_up, D, 2 * F, 2 * F, gsz),
+                   rows_extent(dw_down, F, D, D, gsz)},
+                  {rows_extent(w_up, D, 2 * F, 2 * F), rows_extent(w_down, F, D, D),
+                   rows_extent(x, rows(saved_rows), ld.x, D), rows_extent(up, rows(saved_rows), ld.up, 2 * F),
+                   rows_extent(dy, rows(dy_rows), ld.y, D), Extent{idx, (size_t)(idx ? 4 : 0)},
+                   Extent{n_kept, (size_t)(n_kept ? 4 : 0)}}))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: dx, dw_up and dw_down may not alias each other or an input", fn);
+  const size_t need = collider_ffn_bwd_workspace_size(d);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
+  Ctx c;
+  s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_memory(fn, {w_up, w_down, x, up, dy, idx, n_kept, dx, dw_up, dw_down, ws});
+  if (s != COLLIDER_OK) return s;
+  if (!dx && !dw_up && !dw_down) return COLLIDER_OK;
+  Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
+  FfnBwdBufs b;
+  ffn_bwd_carve(cv, d, &b);
+  const long long cap = pad128(M);
+  const bool dx_full = dx_rows == COLLIDER_ROWS_FULL;
+  const void *xk = x, *dyk = dy;
+  long long xk_ld = ld.x, dyk_ld = ld.y, in_rows = M;   // a dense call reads x and dy where they are
+  if (kept) {
+    FfnPrep p{};
+    p.M = M; p.D = D; p.cap = cap; p.idx = idx; p.n_kept = n_kept;
+    p.x = static_cast<const __nv_bfloat16*>(x); p.x_ld = ld.x; p.x_full = saved_rows == COLLIDER_ROWS_FULL;
+    p.dy = static_cast<const __nv_bfloat16*>(dy); p.dy_ld = ld.y; p.dy_full = dy_rows == COLLIDER_ROWS_FULL;
+    p.xk = dw_up ? b.xk : nullptr;
+    p.dyk = b.dyk;
+    p.dx = dx_full ? static_cast<__nv_bfloat16*>(dx) : nullptr; p.dx_ld = ld.x;
+    CK(launch_ffn_prep(c, p));
+    xk = b.xk; dyk = b.dyk; xk_ld = dyk_ld = D; in_rows = cap;
+  }
+  TcGemm g{};
+  g.M = M; g.N = F; g.K = D;
+  g.A = dyk; g.lda = dyk_ld; g.a_rows = in_rows;
+  g.B = w_down; g.ldb = D; g.b_rows = F;
+  g.C = b.ds; g.ldc = F; g.c_rows = cap;
+  g.n_kept = n_kept; g.dyn = kept ? 1 : 0;
+  CK(launch_tc_gemm(c, g));
+  CK(launch_glu_bwd(c, d->act, M, F, b.ds, static_cast<const __nv_bfloat16*>(up), ld.up, saved_rows == COLLIDER_ROWS_FULL,
+                    b.dgu, b.s, cap, idx, n_kept));
+  if (dx) {
+    g = TcGemm{};
+    g.M = M; g.N = D; g.K = 2 * F;
+    g.A = b.dgu; g.lda = 2 * F; g.a_rows = cap;
+    g.B = w_up; g.ldb = 2 * F; g.b_rows = D;
+    g.C = dx; g.ldc = ld.x; g.c_bf16 = 1; g.c_rows = M;
+    g.zero_pad = kept && !dx_full;
+    g.c_idx = kept && dx_full ? idx : nullptr;
+    g.n_kept = n_kept; g.dyn = kept ? 1 : 0;
+    CK(launch_tc_gemm(c, g));
+  }
+  // A weight gradient, [in, out] = in_k^T out_k
+  auto dw = [&](const void* A, long long lda, long long a_rows, int Kin, const void* B, long long ldb, long long b_rows,
+                int Nout, void* C) {
+    TcGemm w{};
+    w.M = Kin; w.N = Nout; w.K = M;
+    w.A = A; w.lda = lda; w.a_mn_major = 1; w.a_rows = a_rows;
+    w.B = B; w.ldb = ldb; w.b_mn_major = 1; w.b_rows = b_rows;
+    w.C = C; w.ldc = Nout; w.c_bf16 = d->grad_dtype == COLLIDER_BF16;
+    w.n_kept = n_kept; w.dyn = kept ? 2 : 0;
+    return launch_tc_gemm(c, w);
+  };
+  if (dw_up) CK(dw(xk, xk_ld, in_rows, D, b.dgu, 2 * F, cap, 2 * F, dw_up));
+  if (dw_down) CK(dw(b.s, F, cap, F, dyk, dyk_ld, in_rows, D, dw_down));
+  return COLLIDER_OK;
+}
+
+// ===========================================================================
+// norm of gradients, and clipping
+// ===========================================================================
+namespace {
+collider_status check_grads(const char* fn, const collider_grad* g, int count, int kind, float scale) {
+  if (count < 0 || count > (1 << 20)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need 0 <= count <= 2^20", fn);
+  if (count && !g) return fail(COLLIDER_ERR_INVALID_ARG, "%s: null grads", fn);
+  if (kind != COLLIDER_GRAD_NORM_L2 && kind != COLLIDER_GRAD_NORM_MAX)
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: norm kind %d", fn, kind);
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: need a finite scale > 0", fn);
+  long long total = 0;
+  for (int i = 0; i < count; ++i) {
+    if (g[i].dtype != COLLIDER_F32 && g[i].dtype != COLLIDER_BF16)
+      return fail(COLLIDER_ERR_UNSUPPORTED, "%s: gradient %d: dtype %d", fn, i, g[i].dtype);
+    if (g[i].n < 0 || g[i].n > (1ll << 40)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: gradient %d: bad size", fn, i);
+    if (g[i].n && !g[i].data) return fail(COLLIDER_ERR_INVALID_ARG, "%s: gradient %d is null", fn, i);
+    if (reinterpret_cast<uintptr_t>(g[i].data) & (g[i].dtype == COLLIDER_F32 ? 3 : 1))
+      return fail(COLLIDER_ERR_INVALID_ARG, "%s: gradient %d is not aligned to its values", fn, i);
+    total += g[i].n;
+    if (total > (1ll << 40)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: more than 2^40 values", fn);
+  }
+  return COLLIDER_OK;
+}
+size_t grad_bytes(const collider_grad& g) { return (size_t)g.n * (g.dtype == COLLIDER_F32 ? 4 : 2); }
+
+collider_status grad_call(const char* fn, const collider_grad* grads, int count, int kind, float scale, bool clip,
+                          float max_norm, float* norm, float* norms, float* coef, void* ws, size_t ws_bytes, void* stream) {
+  collider_status s = check_grads(fn, grads, count, kind, scale);
+  if (s != COLLIDER_OK) return s;
+  if (!al4({norm, norms, coef})) return fail(COLLIDER_ERR_INVALID_ARG, "%s: outputs must be 4-byte aligned", fn);
+  const Extent out[3] = {{norm, 4}, {norms, (size_t)count * 4}, {coef, 4}};
+  for (int i = 0; i < 3; ++i)
+    for (int k = i + 1; k < 3; ++k)
+      if (out[i].p && out[k].p && overlap(out[i].p, out[i].bytes, out[k].p, out[k].bytes))
+        return fail(COLLIDER_ERR_INVALID_ARG, "%s: the outputs may not alias each other", fn);
+  std::vector<GradItem> items;
+  std::vector<std::pair<uintptr_t, uintptr_t>> at;   // the gradients' bytes
+  try {
+    items.reserve(count);
+    at.reserve(count);
+  } catch (const std::bad_alloc&) {
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: no host memory for a list of %d gradients", fn, count);
+  }
+  for (int i = 0; i < count; ++i) {
+    for (const Extent& o : out)
+      if (o.p && grads[i].n && overlap(o.p, o.bytes, grads[i].data, grad_bytes(grads[i])))
+        return fail(COLLIDER_ERR_INVALID_ARG, "%s: an output lies in gradient %d", fn, i);
+    items.push_back(GradItem{grads[i].data, grads[i].n, grads[i].dtype == COLLIDER_BF16});
+  }
+  if (clip) {
+    // (each value is read and written once only if no two gradients share it)
+    for (int i = 0; i < count; ++i)
+      if (grads[i].n)
+        at.emplace_back(reinterpret_cast<uintptr_t>(grads[i].data), reinterpret_cast<uintptr_t>(grads[i].data) + grad_bytes(grads[i]));
+    if (!std::is_sorted(at.begin(), at.end())) std::sort(at.begin(), at.end());
+    for (size_t i = 1; i < at.size(); ++i)
+      if (at[i].first < at[i - 1].second) return fail(COLLIDER_ERR_INVALID_ARG, "%s: two gradients overlap", fn);
+  }
+  const size_t need = collider_grad_norm_workspace_size(grads, count);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return fail(COLLIDER_ERR_INVALID_ARG, "%s: needs %zu bytes of 256-aligned workspace", fn, need);
+  Ctx c;
+  s = make_ctx(stream, &c);
+  if (s == COLLIDER_OK) s = check_memory(fn, {norm, norms, coef, ws});
+  for (int i = 0; i < count && s == COLLIDER_OK; ++i)
+    if (grads[i].n) s = check_memory(fn, {grads[i].data});
+  if (s != COLLIDER_OK) return s;
+  GradJob j{};
+  j.items = items.data(); j.count = count; j.max_kind = kind == COLLIDER_GRAD_NORM_MAX; j.scale = scale;
+  j.clip = clip; j.max_norm = max_norm; j.norm = norm; j.norms = norms; j.coef = coef;
+  j.part = static_cast<double*>(ws);
+  CK(launch_grad(c, j));
+  return COLLIDER_OK;
+}
+}  // namespace
+
+extern "C" size_t collider_grad_norm_workspace_size(const collider_grad*, int count) {
+  if (count < 0 || count > (1 << 20)) return 0;
+  return up256(grad_part_doubles(count) * sizeof(double));
+}
+
+extern "C" collider_status collider_grad_norm(const collider_grad* grads, int count, int kind, float scale, float* norm,
+                                              float* norms, void* ws, size_t ws_bytes, void* stream) {
+  return grad_call("collider_grad_norm", grads, count, kind, scale, false, 0.f, norm, norms, nullptr, ws, ws_bytes, stream);
+}
+
+extern "C" collider_status collider_grad_clip(const collider_grad* grads, int count, int kind, float scale, float max_norm,
+                                              float* norm, float* norms, float* coef, void* ws, size_t ws_bytes,
+                                              void* stream) {
+  if (!(max_norm >= 0.f)) return fail(COLLIDER_ERR_INVALID_ARG, "collider_grad_clip: need max_norm >= 0");
+  return grad_call("collider_grad_clip", grads, count, kind, scale, true, max_norm, norm, norms, coef, ws, ws_bytes, stream);
 }

@@ -1,0 +1,37 @@
+// The gated feed-forward block's activations, in f32 (sm_103a).
+#pragma once
+
+#include "common.cuh"
+
+namespace collider {
+
+constexpr int kGluSilu = 0, kGluGeluTanh = 1;
+
+// SiLU: a(g) = g p, p = sigmoid(g), a' = p (1 + g (1 - p)).
+// GELU (tanh form): with z = c (g + k g^3), (1 + tanh z) / 2 = sigmoid(2 z) = p,
+// so a(g) = g p and a' = p + 2 g p (1 - p) c (1 + 3 k g^2): one exponential and
+// one reciprocal either way, and no cancellation for g far below 0.
+template <int ACT>
+__device__ __forceinline__ float glu_gate(float g) {
+  constexpr float c2 = 2.f * 0.7978845608028654f, k = 0.044715f;
+  const float z = ACT == kGluSilu ? g : c2 * g * fmaf(k * g, g, 1.f);
+  return __frcp_rn(1.f + __expf(-z));
+}
+template <int ACT>
+__device__ __forceinline__ float glu_act(float g) {
+  return g * glu_gate<ACT>(g);
+}
+// a(g) and a'(g)
+template <int ACT>
+__device__ __forceinline__ void glu_both(float g, float* a, float* da) {
+  const float p = glu_gate<ACT>(g);
+  *a = g * p;
+  if (ACT == kGluSilu) {
+    *da = p * fmaf(g, 1.f - p, 1.f);
+  } else {
+    constexpr float c2 = 2.f * 0.7978845608028654f, k3 = 3.f * 0.044715f;
+    *da = fmaf(*a * (1.f - p), c2 * fmaf(k3 * g, g, 1.f), p);
+  }
+}
+
+}  // namespace collider

@@ -387,4 +387,51 @@ struct JoinBwd {
 size_t join_bwd_part_floats(int B, int T, int D, int gate_rows);
 cudaError_t launch_join_bwd(const Ctx& c, const JoinBwd& j);
 
+// ---- gradient norm and clipping (grad.cu) ------------------------------------
+struct GradItem {
+  void* p;        // n contiguous values, aligned to their size
+  long long n;
+  int bf16;
+};
+struct GradJob {
+  const GradItem* items;
+  int count;
+  int max_kind;   // 0: square root of the sum of squares, 1: largest magnitude
+  float scale;    // of the values, before the norm
+  int clip;
+  float max_norm;
+  float *norm, *norms, *coef;   // each may be null
+  double* part;   // grad_part_doubles(count)
+};
+constexpr int kGradMaxBlocks = 1024;   // blocks of a launch, at most
+size_t grad_part_doubles(int count);
+cudaError_t launch_grad(const Ctx& c, const GradJob& j);
+
+// ---- gated feed-forward block (ffn.cu) ----------------------------------------
+// What the backward's products read, in one launch: rows of x and dy (through
+// idx when *_full, else in order; idx null: in order) copied into xk and dyk,
+// zero-padded to 128 rows, and the rows of a FULL dx that are not kept zeroed.
+// A kept index outside the M rows is reported and its copies are rows of zeros.
+// Parts left out: xk, dyk, dx null.
+struct FfnPrep {
+  int M, D;
+  const __nv_bfloat16 *x, *dy;
+  long long x_ld, dy_ld, dx_ld;   // elements
+  int x_full, dy_full;
+  __nv_bfloat16 *xk, *dyk;        // [cap, D]
+  __nv_bfloat16* dx;
+  long long cap;
+  const int32_t* idx;
+  const int32_t* n_kept;
+};
+cudaError_t launch_ffn_prep(const Ctx& c, const FfnPrep& p);
+// up = bf16(acc) (may be null), s = bf16(act(g) u) of the f32 acc [M, 2F] = [g | u]
+cudaError_t launch_glu_fwd(const Ctx& c, int act, int M, int F, const float* acc, __nv_bfloat16* up, long long up_ld,
+                           __nv_bfloat16* s);
+// dgu = bf16([ds u act'(g) | ds act(g)]), s = bf16(act(g) u) for the kept rows, zero rows up to 128;
+// ds f32 [*, F] COMPACT; up FULL (read through idx) or COMPACT; idx and n_kept null: all M rows
+cudaError_t launch_glu_bwd(const Ctx& c, int act, int M, int F, const float* ds, const __nv_bfloat16* up, long long up_ld,
+                           int up_full, __nv_bfloat16* dgu, __nv_bfloat16* s, long long cap, const int32_t* idx,
+                           const int32_t* n_kept);
+
 }  // namespace collider
