@@ -6,8 +6,10 @@
 // HBM-bound: the norm reads every value once; clipping needs the whole norm
 // before it writes the first value, so it reads a second time.
 #include <algorithm>
+#include <mutex>
 
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace collider {
 
@@ -18,6 +20,7 @@ constexpr int kGradVecs = 8;             // 16-byte vectors a thread has in flig
 constexpr int kGradChunk = kGradThreads * kGradVecs;   // vectors of a chunk: 32 KB
 constexpr int kGradTable = 1024;         // tensors of a launch (24 KB of its 32 KB of parameters)
 constexpr int kGradBlocksPerSm = 4;
+constexpr size_t kGradKeep = 64 << 20;   // bytes that the norm leaves in L2 for the clipping pass
 
 // A launch's tensors, by value in its parameters: no copy to the device, so a
 // captured call replays with the addresses it was captured with.
@@ -113,17 +116,52 @@ __device__ __forceinline__ bool whole_vec(const Span& s, long long v) {
 // 1/64 of the f32 rate).  Where the largest magnitude leaves [2^-50, 2^60],
 // and squares of f32 could overflow or vanish, the same values are squared in
 // f64.
+// A block of kGradThreads threads (a quarter of a CTA in the small form below):
+// the thread's place in it, and its barrier
+__device__ __forceinline__ int block_thread() { return threadIdx.x & (kGradThreads - 1); }
+__device__ __forceinline__ void block_sync() { tc::named_bar(1 + threadIdx.x / kGradThreads, kGradThreads); }
+
+// The vectors of a chunk that this thread takes: v0 + thread + k * kGradThreads.
+// keep: what is loaded is read again soon (clipping).  Inside a tensor they are loaded without a question, all at once; only a
+// tensor's first and last chunk ask for each vector.
 template <bool BF>
-__device__ __forceinline__ void take_chunk(const Span& s, long long v0, int max_kind, double* sum, uint32_t* big) {
+__device__ __forceinline__ bool inner_chunk(const Span& s, long long v0) {
   constexpr int per = BF ? 8 : 4;
-  const long long vend = (s.end + per - 1) / per;
-  uint4 u[kGradVecs];
+  return v0 * per >= s.lead && (v0 + kGradChunk) * per <= s.end;
+}
+template <bool BF>
+__device__ __forceinline__ void load_chunk(const Span& s, long long v0, bool keep, uint4* u) {
+  constexpr int per = BF ? 8 : 4;
+  if (inner_chunk<BF>(s, v0)) {
+    const uint4* p = s.base + v0 + block_thread();
+    if (keep) {
 #pragma unroll
-  for (int k = 0; k < kGradVecs; ++k) {
-    const long long v = v0 + threadIdx.x + k * kGradThreads;
-    u[k] = make_uint4(0, 0, 0, 0);
-    if (v < vend) u[k] = whole_vec<BF>(s, v) ? __ldg(s.base + v) : load_edge<BF>(s, v);
+      for (int k = 0; k < kGradVecs; ++k) u[k] = p[k * kGradThreads];
+    } else {
+#pragma unroll
+      for (int k = 0; k < kGradVecs; ++k) u[k] = __ldcs(p + k * kGradThreads);
+    }
+  } else {
+    const long long vend = (s.end + per - 1) / per;
+#pragma unroll
+    for (int k = 0; k < kGradVecs; ++k) {
+      const long long v = v0 + block_thread() + k * kGradThreads;
+      u[k] = make_uint4(0, 0, 0, 0);
+      if (v < vend) u[k] = whole_vec<BF>(s, v) ? s.base[v] : load_edge<BF>(s, v);
+    }
   }
+}
+
+// Adds a thread's values of one chunk to its sum of squares (in f64), or takes
+// its largest magnitude (as the bits of |v|: a NaN is above infinity).
+// Squares are added in f32, at most 16 to a sum, and the sums in f64: one f64
+// operation a chunk and thread (an f64 multiply-add a value would bind, at
+// 1/64 of the f32 rate).  Where the largest magnitude leaves [2^-50, 2^60],
+// and squares of f32 could overflow or vanish, the same values are squared in
+// f64.
+template <bool BF, bool MAX>
+__device__ __forceinline__ void take_chunk(const uint4* u, double* sum, uint32_t* big) {
+  constexpr int per = BF ? 8 : 4;
   uint32_t m = 0;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -132,11 +170,11 @@ __device__ __forceinline__ void take_chunk(const Span& s, long long v0, int max_
     unpack_vec<BF>(u[k], f);
 #pragma unroll
     for (int i = 0; i < per; ++i) {
-      acc[i & 3] = fmaf(f[i], f[i], acc[i & 3]);
+      if (!MAX) acc[i & 3] = fmaf(f[i], f[i], acc[i & 3]);
       m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
     }
   }
-  if (max_kind) {
+  if (MAX) {
     *big = max(*big, m);
     return;
   }
@@ -152,32 +190,47 @@ __device__ __forceinline__ void take_chunk(const Span& s, long long v0, int max_
     *sum += (double)((acc[0] + acc[1]) + (acc[2] + acc[3]));
   }
 }
+template <bool BF, bool MAX>
+__device__ __forceinline__ void take_chunks(const Span& s, int c, int cend, int keep_from, double* sum, uint32_t* big) {
+  for (; c < cend; ++c) {
+    uint4 u[kGradVecs];
+    load_chunk<BF>(s, (long long)c * kGradChunk, c >= keep_from, u);
+    take_chunk<BF, MAX>(u, sum, big);
+  }
+}
 
 __device__ __forceinline__ double max_value(uint32_t bits) { return (double)__uint_as_float(bits); }
 // the larger of two magnitudes, a NaN above all
 __device__ __forceinline__ double max_nan(double a, double b) { return (a > b || a != a) ? a : b; }
 
-// sum (or maximum) over the block, in a fixed order; every thread gets it
+// Sum (or maximum) over the block, in a fixed order; every thread gets it.
+// One warp adds all of it: f64 runs at two operations a clock and SM, so eight
+// warps that each reduced their own and then each other's values would take
+// eight times as long (3 us an SM with four blocks).
 __device__ __forceinline__ double block_reduce(double v, int max_kind, double* red) {
+  block_sync();
+  red[block_thread()] = v;
+  block_sync();
+  if (block_thread() < 32) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = max_kind ? max_nan(v, w) : v + w;
+    for (int i = 1; i < kGradThreads / 32; ++i) {
+      const double w = red[block_thread() + 32 * i];
+      v = max_kind ? max_nan(v, w) : v + w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double w = __shfl_xor_sync(0xffffffffu, v, o);
+      v = max_kind ? max_nan(v, w) : v + w;
+    }
+    if (block_thread() == 0) red[0] = v;
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-  for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v = max_kind ? max_nan(v, red[i]) : v + red[i];
-  return v;
+  block_sync();
+  return red[0];
 }
 
-template <int N>
-__global__ void __launch_bounds__(kGradThreads) grad_part_kernel(const __grid_constant__ GradTable<N> t, int max_kind,
-                                                                 double* part) {
-  __shared__ double red[kGradThreads / 32];
-  grid_dep_wait();
-  const int b = blockIdx.x, blocks = gridDim.x;
+// block b's partials; the last `keep` of its chunks are left in L2
+template <typename Tab>
+__device__ __forceinline__ void part_block(const Tab& t, int b, int blocks, int keep, int max_kind, double* part, double* red) {
   int c = block_begin(t, b, blocks);
   const int cend = block_begin(t, b + 1, blocks);
   const int t_first = b == 0 ? 0 : tensor_of(t, c);
@@ -189,16 +242,31 @@ __global__ void __launch_bounds__(kGradThreads) grad_part_kernel(const __grid_co
       const Span s = span_of(t.p[k], t.n[k]);
       double sum = 0.0;
       uint32_t big = 0;
-      const int base = t.first[k];
-      if (s.per == 8)
-        for (; c < kend; ++c) take_chunk<true>(s, (long long)(c - base) * kGradChunk, max_kind, &sum, &big);
-      else
-        for (; c < kend; ++c) take_chunk<false>(s, (long long)(c - base) * kGradChunk, max_kind, &sum, &big);
+      const int at = t.first[k], kf = cend - keep - at;
+      if (s.per == 8) {
+        if (max_kind) take_chunks<true, true>(s, c - at, kend - at, kf, &sum, &big);
+        else take_chunks<true, false>(s, c - at, kend - at, kf, &sum, &big);
+      } else {
+        if (max_kind) take_chunks<false, true>(s, c - at, kend - at, kf, &sum, &big);
+        else take_chunks<false, false>(s, c - at, kend - at, kf, &sum, &big);
+      }
+      c = kend;
       v = block_reduce(max_kind ? max_value(big) : sum, max_kind, red);
     }
-    if (threadIdx.x == 0) part[b + k] = v;
+    if (block_thread() == 0) part[b + k] = v;
   }
 }
+
+template <int N>
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
+    grad_part_kernel(const __grid_constant__ GradTable<N> t, int keep, int max_kind, double* part) {
+  __shared__ double red[kGradThreads];
+  grid_dep_wait();
+  part_block(t, blockIdx.x, gridDim.x, keep, max_kind, part, red);
+}
+
+// a partial, in global memory or in the cluster's shared memory
+__device__ __forceinline__ double load_part(const double* p) { return *static_cast<const volatile double*>(p); }
 
 // tensor k's norm (before scale) from the partials of the blocks that met it; by one warp
 template <typename Tab>
@@ -209,7 +277,7 @@ __device__ __forceinline__ double tensor_norm(const Tab& t, int k, int blocks, i
     const int b0 = (int)((((long long)t.first[k] + 1) * blocks - 1) / t.chunks);
     const int b1 = (int)((((long long)t.first[k + 1]) * blocks - 1) / t.chunks);
     for (int b = b0 + (threadIdx.x & 31); b <= b1; b += 32) {
-      const double w = __ldcg(part + b + k);
+      const double w = load_part(part + b + k);
       v = max_kind ? max_nan(v, w) : v + w;
     }
 #pragma unroll
@@ -224,85 +292,95 @@ __device__ __forceinline__ double tensor_norm(const Tab& t, int k, int blocks, i
 // the norm of everything, from all slots; every thread of the block gets it
 __device__ __forceinline__ float total_norm(const double* part, int slots, int max_kind, float scale, double* red) {
   double v = 0.0;
-  for (int i = threadIdx.x; i < slots; i += blockDim.x) {
-    const double w = __ldcg(part + i);
+  for (int i = block_thread(); i < slots; i += kGradThreads) {
+    const double w = load_part(part + i);
     v = max_kind ? max_nan(v, w) : v + w;
   }
   v = block_reduce(v, max_kind, red);
-  return (float)((max_kind ? v : sqrt(v)) * (double)scale);
+  float* out = reinterpret_cast<float*>(red + 1);
+  if (block_thread() == 0) *out = (float)((max_kind ? v : sqrt(v)) * (double)scale);   // (by one thread: an f64 root is long)
+  block_sync();
+  return *out;
+}
+
+// the tensors' norms, by the warps of all blocks in turn
+template <typename Tab>
+__device__ __forceinline__ void write_norms(const Tab& t, int b, int blocks, int max_kind, float scale, int part_blocks,
+                                            const double* part, float* norms) {
+  constexpr int warps = kGradThreads / 32;
+  for (int k = b * warps + (block_thread() >> 5); k < t.count; k += blocks * warps) {
+    const double v = tensor_norm(t, k, part_blocks, max_kind, part);
+    if ((threadIdx.x & 31) == 0) norms[k] = (float)(v * (double)scale);
+  }
 }
 
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) grad_finish_kernel(const __grid_constant__ GradTable<N> t, int max_kind,
                                                                    float scale, int blocks, const double* part, const double* all,
                                                                    int slots, float* norm, float* norms) {
-  __shared__ double red[kGradThreads / 32];
+  __shared__ double red[kGradThreads];
   grid_dep_wait();
-  if (norms)
-    for (int k = blockIdx.x * (kGradThreads / 32) + (threadIdx.x >> 5); k < t.count; k += gridDim.x * (kGradThreads / 32)) {
-      const double v = tensor_norm(t, k, blocks, max_kind, part);
-      if ((threadIdx.x & 31) == 0) norms[k] = (float)(v * (double)scale);
-    }
+  if (norms) write_norms(t, blockIdx.x, gridDim.x, max_kind, scale, blocks, part, norms);
   if (blockIdx.x == 0 && norm) {
     const float v = total_norm(all, slots, max_kind, scale, red);
-    if (threadIdx.x == 0) *norm = v;
+    if (block_thread() == 0) *norm = v;
   }
 }
 
 template <bool BF>
+__device__ __forceinline__ uint4 scaled(const uint4& u, float coef) {
+  constexpr int per = BF ? 8 : 4;
+  float f[8];
+  unpack_vec<BF>(u, f);
+#pragma unroll
+  for (int i = 0; i < per; ++i) f[i] *= coef;
+  return BF ? pack8(f)
+            : make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <bool BF>
 __device__ __forceinline__ void scale_chunk(const Span& s, long long v0, float coef) {
   constexpr int per = BF ? 8 : 4;
-  const long long vend = (s.end + per - 1) / per;
   uint4* out = const_cast<uint4*>(s.base);
   uint4 u[kGradVecs];
+  load_chunk<BF>(s, v0, false, u);
+  if (inner_chunk<BF>(s, v0)) {
+    out += v0 + block_thread();
 #pragma unroll
-  for (int k = 0; k < kGradVecs; ++k) {
-    const long long v = v0 + threadIdx.x + k * kGradThreads;
-    if (v < vend) u[k] = whole_vec<BF>(s, v) ? out[v] : load_edge<BF>(s, v);
+    for (int k = 0; k < kGradVecs; ++k) __stcs(out + k * kGradThreads, scaled<BF>(u[k], coef));
+    return;
   }
+  const long long vend = (s.end + per - 1) / per;
 #pragma unroll
   for (int k = 0; k < kGradVecs; ++k) {
-    const long long v = v0 + threadIdx.x + k * kGradThreads;
+    const long long v = v0 + block_thread() + k * kGradThreads;
     if (v >= vend) continue;
-    float f[8];
-    unpack_vec<BF>(u[k], f);
-#pragma unroll
-    for (int i = 0; i < per; ++i) f[i] *= coef;
+    const uint4 w = scaled<BF>(u[k], coef);
     if (whole_vec<BF>(s, v)) {
-      out[v] = BF ? pack8(f)
-                  : make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    } else {
+      out[v] = w;
+      continue;
+    }
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int i = 0; i < per; ++i) {
-        const long long at = v * per + i;
-        if (at < s.lead || at >= s.end) continue;
-        if (BF) reinterpret_cast<__nv_bfloat16*>(out + v)[i] = __float2bfloat16_rn(f[i]);
-        else reinterpret_cast<float*>(out + v)[i] = f[i];
-      }
+    for (int i = 0; i < per; ++i) {
+      const long long at = v * per + i;
+      if (at < s.lead || at >= s.end) continue;
+      if (BF) reinterpret_cast<uint16_t*>(out + v)[i] = (uint16_t)(x[i >> 1] >> (16 * (i & 1)));
+      else reinterpret_cast<uint32_t*>(out + v)[i] = x[i];
     }
   }
 }
 
-// Every block sums all partials for itself (6 KB from L2 at one launch's 608
-// blocks), so the coefficient needs no kernel of its own.
-template <int N>
-__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_constant__ GradTable<N> t, int max_kind,
-                                                                  float scale, float max_norm, const double* part,
-                                                                  const double* all, int slots, float* norm, float* norms,
-                                                                  float* coef_out) {
-  __shared__ double red[kGradThreads / 32];
-  grid_dep_wait();
-  const int b = blockIdx.x, blocks = gridDim.x;
+// Block b's gradients scaled.  Every block sums all partials for itself (6 KB
+// from L2 at one launch's 608 blocks), so the coefficient needs no kernel of
+// its own.
+template <typename Tab>
+__device__ __forceinline__ void scale_block(const Tab& t, int b, int blocks, int max_kind, float scale, float max_norm,
+                                            const double* all, int slots, float* norm, float* coef_out, double* red) {
   const float nv = total_norm(all, slots, max_kind, scale, red);
   const bool fine = isfinite(nv);
   const float clip = fminf(1.f, __fdiv_rn(max_norm, __fadd_rn(nv, 1e-6f)));
   const float coef = fine ? __fmul_rn(scale, clip) : 0.f;
-  if (norms)
-    for (int k = b * (kGradThreads / 32) + (threadIdx.x >> 5); k < t.count; k += blocks * (kGradThreads / 32)) {
-      const double v = tensor_norm(t, k, blocks, max_kind, part);
-      if ((threadIdx.x & 31) == 0) norms[k] = (float)(v * (double)scale);
-    }
-  if (b == 0 && threadIdx.x == 0) {
+  if (b == 0 && block_thread() == 0) {
     if (norm) *norm = nv;
     if (coef_out) *coef_out = coef;
   }
@@ -319,6 +397,45 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_c
     else
       for (; c > stop; --c) scale_chunk<false>(s, (long long)(c - 1 - base) * kGradChunk, coef);
   }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
+    grad_scale_kernel(const __grid_constant__ GradTable<N> t, int max_kind, float scale, float max_norm, const double* part,
+                      const double* all, int slots, float* norm, float* norms, float* coef_out) {
+  __shared__ double red[kGradThreads];
+  grid_dep_wait();
+  if (norms) write_norms(t, blockIdx.x, gridDim.x, max_kind, scale, gridDim.x, part, norms);
+  scale_block(t, blockIdx.x, gridDim.x, max_kind, scale, max_norm, all, slots, norm, coef_out, red);
+}
+
+// A small set in one launch: one cluster of 16 CTAs of four blocks each, whose
+// barrier stands between the partials, which lie in the first CTA's shared
+// memory, and what is made of them.
+constexpr int kSmallCtas = 16, kSmallPerCta = 4, kSmallBlocks = kSmallCtas * kSmallPerCta;
+constexpr int kSmallChunks = 128, kSmallTensors = 32;
+__global__ void __launch_bounds__(kGradThreads* kSmallPerCta)
+    grad_small_kernel(const __grid_constant__ GradTable<kSmallTensors> t, int blocks, int max_kind, int clip, float scale,
+                      float max_norm, float* norm, float* norms, float* coef_out) {
+  __shared__ double red_all[kSmallPerCta][kGradThreads];
+  __shared__ double part_all[kSmallBlocks + kSmallTensors];
+  grid_dep_wait();
+  tc::cluster_sync();   // the first CTA's shared memory is there
+  double* part = tc::peer_generic(part_all, 0);
+  const int b = blockIdx.x * kSmallPerCta + threadIdx.x / kGradThreads;
+  double* red = red_all[threadIdx.x / kGradThreads];
+  if (b < blocks) part_block(t, b, blocks, 1 << 28, max_kind, part, red);
+  tc::cluster_sync();
+  const int slots = blocks + t.count;
+  if (clip) {
+    if (b < blocks) scale_block(t, b, blocks, max_kind, scale, max_norm, part, slots, norm, coef_out, red);
+  } else if (b == 0 && norm) {
+    const float v = total_norm(part, slots, max_kind, scale, red);
+    if (block_thread() == 0) *norm = v;
+  }
+  // (the other CTAs' warps first: block 0 has the total to do)
+  if (norms) write_norms(t, kSmallBlocks - 1 - b, kSmallBlocks, max_kind, scale, blocks, part, norms);
+  tc::cluster_sync();   // the first CTA stays until its partials are read
 }
 
 int chunks_of(const GradItem& g) {
@@ -359,7 +476,8 @@ cudaError_t run_piece(const Ctx& c, const GradJob& j, int stage, const GradItem*
   cudaError_t e;
   if (stage == 0) {
     prof_begin(c, "grad_part");
-    e = launch_k(c, false, grad_part_kernel<N>, dim3(blocks), dim3(kGradThreads), 0, 1, t, j.max_kind, part);
+    const int keep = j.clip ? (int)(kGradKeep / (kGradChunk * 16) / blocks) : 0;
+    e = launch_k(c, false, grad_part_kernel<N>, dim3(blocks), dim3(kGradThreads), 0, 1, t, keep, j.max_kind, part);
   } else if (j.clip) {
     prof_begin(c, "grad_scale");
     e = launch_k(cc, pdl_allowed(), grad_scale_kernel<N>, dim3(blocks), dim3(kGradThreads), 0, 1, t, j.max_kind, j.scale,
@@ -383,7 +501,49 @@ size_t grad_part_doubles(int count) {
   return pieces * kGradMaxBlocks + (size_t)(count < 0 ? 0 : count);
 }
 
+// whether the device takes a cluster of kSmallCtas CTAs of the small form
+static bool small_fits() {
+  static std::mutex mu;
+  static signed char known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!known[dev]) {
+    auto k = grad_small_kernel;
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSmallCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(kSmallCtas);
+    cfg.blockDim = dim3(kGradThreads * kSmallPerCta);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const bool ok = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();
+    known[dev] = ok ? 1 : -1;
+  }
+  return known[dev] > 0;
+}
+
 cudaError_t launch_grad(const Ctx& c, const GradJob& j) {
+  if (j.count <= kSmallTensors && small_fits()) {
+    long long chunks = 0;
+    for (int i = 0; i < j.count; ++i) chunks += chunks_of(j.items[i]);
+    if (chunks <= kSmallChunks) {
+      GradTable<kSmallTensors> t;
+      fill(&t, j.items, j.count);
+      const int blocks = t.chunks < 1 ? 1 : t.chunks < kSmallBlocks ? t.chunks : kSmallBlocks;
+      prof_begin(c, "grad_small");
+      const cudaError_t e = launch_k(c, false, grad_small_kernel, dim3(kSmallCtas), dim3(kGradThreads * kSmallPerCta), 0,
+                                     kSmallCtas, t, blocks, j.max_kind, j.clip, j.scale, j.max_norm, j.norm, j.norms, j.coef);
+      prof_end(c);
+      count_launch();
+      return launched(e);
+    }
+  }
   const int pieces = j.count <= 0 ? 1 : (j.count + kGradTable - 1) / kGradTable;
   if (c.num_sms * kGradBlocksPerSm > kGradMaxBlocks) return cudaErrorNotSupported;
   int slots = 0;
@@ -394,7 +554,7 @@ cudaError_t launch_grad(const Ctx& c, const GradJob& j) {
       int used = 0;
       float* norms = j.norms ? j.norms + i0 : nullptr;
       // (a short list's table is a few hundred bytes of parameters instead of 20 KB)
-      const cudaError_t e = n <= 32 ? run_piece<32>(c, j, stage, j.items + i0, n, j.part + at, &used, slots, norms, p == 0)
+      const cudaError_t e = n <= kSmallTensors ? run_piece<kSmallTensors>(c, j, stage, j.items + i0, n, j.part + at, &used, slots, norms, p == 0)
                                     : run_piece<kGradTable>(c, j, stage, j.items + i0, n, j.part + at, &used, slots, norms, p == 0);
       if (e != cudaSuccess) return e;
       at += used;
