@@ -1964,26 +1964,30 @@ bool any_overlap(std::initializer_list<Extent> out, std::initializer_list<Extent
 }
 
 struct FfnFwdBufs {
-  float* acc;          // [M, 2F]
   __nv_bfloat16* s;    // [M, F]
+  float* partial;
+  int* counters;
 };
 size_t ffn_fwd_carve(Carver& cv, const collider_ffn_desc* d, FfnFwdBufs* b) {
-  b->acc = cv.take<float>((size_t)d->M * 2 * d->F);
   b->s = cv.take<__nv_bfloat16>((size_t)d->M * d->F);
+  b->partial = cv.take<float>(ffn_partial_floats());
+  b->counters = cv.take<int>(ffn_counters());
   return cv.used;
 }
 struct FfnBwdBufs {
   __nv_bfloat16 *xk, *dyk;   // kept rows of x and dy, zero-padded to 128 rows
-  float* ds;                 // [Mp, F]
   __nv_bfloat16 *dgu, *s;    // [Mp, 2F], [Mp, F]
+  float* partial;
+  int* counters;
 };
 size_t ffn_bwd_carve(Carver& cv, const collider_ffn_desc* d, FfnBwdBufs* b) {
   const size_t Mp = (size_t)pad128(d->M);
   b->xk = cv.take<__nv_bfloat16>(Mp * d->D);
   b->dyk = cv.take<__nv_bfloat16>(Mp * d->D);
-  b->ds = cv.take<float>(Mp * d->F);
   b->dgu = cv.take<__nv_bfloat16>(Mp * 2 * d->F);
   b->s = cv.take<__nv_bfloat16>(Mp * d->F);
+  b->partial = cv.take<float>(ffn_partial_floats());
+  b->counters = cv.take<int>(ffn_counters());
   return cv.used;
 }
 }  // namespace
@@ -2020,19 +2024,20 @@ extern "C" collider_status collider_ffn_fwd(const collider_ffn_desc* d, const vo
   Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
   FfnFwdBufs b;
   ffn_fwd_carve(cv, d, &b);
-  TcGemm g{};
-  g.M = M; g.N = 2 * F; g.K = D;
-  g.A = x; g.lda = ld.x; g.a_rows = M;
-  g.B = w_up; g.ldb = 2 * F; g.b_mn_major = 1; g.b_rows = D;
-  g.C = b.acc; g.ldc = 2 * F; g.c_rows = M;
-  CK(launch_tc_gemm(c, g));
-  CK(launch_glu_fwd(c, d->act, M, F, b.acc, static_cast<__nv_bfloat16*>(up), ld.up, b.s));
-  g = TcGemm{};
+  FfnUp u{};
+  u.act = d->act; u.M = M; u.D = D; u.F = F;
+  u.x = x; u.x_ld = ld.x; u.w_up = w_up;
+  u.up = static_cast<__nv_bfloat16*>(up); u.up_ld = ld.up; u.s = b.s;
+  u.counters = b.counters;
+  CK(launch_ffn_up(c, u));
+  FfnProduct g{};
   g.M = M; g.N = D; g.K = F;
   g.A = b.s; g.lda = F; g.a_rows = M;
-  g.B = w_down; g.ldb = D; g.b_mn_major = 1; g.b_rows = F;
-  g.C = y; g.ldc = ld.y; g.c_bf16 = 1; g.c_rows = M;
-  CK(launch_tc_gemm(c, g));
+  g.B = w_down; g.ldb = D; g.b_mn = 1; g.b_rows = F;
+  g.C = y; g.ldc = ld.y; g.c_rows = M;
+  Ctx cp = c;
+  cp.pdl = pdl_allowed();
+  CK(launch_ffn_group(cp, &g, 1, M, nullptr, nullptr, b.partial, b.counters));
   return COLLIDER_OK;
 }
 
@@ -2100,39 +2105,41 @@ extern "C" collider_status collider_ffn_bwd(const collider_ffn_desc* d, const vo
     CK(launch_ffn_prep(c, p));
     xk = b.xk; dyk = b.dyk; xk_ld = dyk_ld = D; in_rows = cap;
   }
-  TcGemm g{};
-  g.M = M; g.N = F; g.K = D;
-  g.A = dyk; g.lda = dyk_ld; g.a_rows = in_rows;
-  g.B = w_down; g.ldb = D; g.b_rows = F;
-  g.C = b.ds; g.ldc = F; g.c_rows = cap;
-  g.n_kept = n_kept; g.dyn = kept ? 1 : 0;
-  CK(launch_tc_gemm(c, g));
-  CK(launch_glu_bwd(c, d->act, M, F, b.ds, static_cast<const __nv_bfloat16*>(up), ld.up, saved_rows == COLLIDER_ROWS_FULL,
-                    b.dgu, b.s, cap, idx, n_kept));
-  if (dx) {
-    g = TcGemm{};
-    g.M = M; g.N = D; g.K = 2 * F;
-    g.A = b.dgu; g.lda = 2 * F; g.a_rows = cap;
-    g.B = w_up; g.ldb = 2 * F; g.b_rows = D;
-    g.C = dx; g.ldc = ld.x; g.c_bf16 = 1; g.c_rows = M;
-    g.zero_pad = kept && !dx_full;
-    g.c_idx = kept && dx_full ? idx : nullptr;
-    g.n_kept = n_kept; g.dyn = kept ? 1 : 0;
-    CK(launch_tc_gemm(c, g));
-  }
-  // A weight gradient, [in, out] = in_k^T out_k
-  auto dw = [&](const void* A, long long lda, long long a_rows, int Kin, const void* B, long long ldb, long long b_rows,
-                int Nout, void* C) {
-    TcGemm w{};
-    w.M = Kin; w.N = Nout; w.K = M;
-    w.A = A; w.lda = lda; w.a_mn_major = 1; w.a_rows = a_rows;
-    w.B = B; w.ldb = ldb; w.b_mn_major = 1; w.b_rows = b_rows;
-    w.C = C; w.ldc = Nout; w.c_bf16 = d->grad_dtype == COLLIDER_BF16;
-    w.n_kept = n_kept; w.dyn = kept ? 2 : 0;
-    return launch_tc_gemm(c, w);
+  Ctx cp = c;
+  cp.pdl = pdl_allowed();
+  FfnDs e{};
+  e.act = d->act; e.M = M; e.D = D; e.F = F;
+  e.dy = dyk; e.dy_ld = dyk_ld; e.dy_rows = in_rows; e.w_down = w_down;
+  e.up = static_cast<const __nv_bfloat16*>(up); e.up_ld = ld.up; e.up_full = saved_rows == COLLIDER_ROWS_FULL;
+  e.dgu = b.dgu; e.s = b.s; e.cap = cap; e.idx = idx; e.n_kept = n_kept; e.counters = b.counters;
+  CK(launch_ffn_ds(kept ? cp : c, e));
+  FfnProduct g[3] = {};
+  int np = 0;
+  auto add_dx = [&] {
+    if (!dx) return;
+    FfnProduct& q = g[np++];
+    q.M = M; q.N = D; q.K = 2 * F; q.dyn = kept ? 1 : 0;
+    q.A = b.dgu; q.lda = 2 * F; q.a_rows = cap;
+    q.B = w_up; q.ldb = 2 * F; q.b_rows = D;
+    q.C = dx; q.ldc = ld.x; q.c_rows = M;
+    q.scatter = kept && dx_full; q.zero_pad = kept && !dx_full;
   };
-  if (dw_up) CK(dw(xk, xk_ld, in_rows, D, b.dgu, 2 * F, cap, 2 * F, dw_up));
-  if (dw_down) CK(dw(b.s, F, cap, F, dyk, dyk_ld, in_rows, D, dw_down));
+  // a weight gradient, [in, out] = in_k^T out_k
+  auto add_dw = [&](const void* A, long long lda, long long a_rows, int Kin, const void* B, long long ldb, long long b_rows,
+                    int Nout, void* C) {
+    if (!C) return;
+    FfnProduct& q = g[np++];
+    q.M = Kin; q.N = Nout; q.K = M; q.dyn = kept ? 2 : 0;
+    q.A = A; q.lda = lda; q.a_rows = a_rows; q.a_mn = 1;
+    q.B = B; q.ldb = ldb; q.b_rows = b_rows; q.b_mn = 1;
+    q.C = C; q.ldc = Nout; q.c_rows = Kin; q.c_f32 = d->grad_dtype == COLLIDER_F32;
+  };
+  // one list of tiles, the longer reductions first
+  if (2 * F >= M) add_dx();
+  add_dw(xk, xk_ld, in_rows, D, b.dgu, 2 * F, cap, 2 * F, dw_up);
+  add_dw(b.s, F, cap, F, dyk, dyk_ld, in_rows, D, dw_down);
+  if (2 * F < M) add_dx();
+  CK(launch_ffn_group(cp, g, np, M, idx, n_kept, b.partial, b.counters));
   return COLLIDER_OK;
 }
 

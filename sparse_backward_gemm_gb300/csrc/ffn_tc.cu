@@ -1,0 +1,815 @@
+// The gated feed-forward block's matrix products on the 5th-generation tensor
+// cores (sm_103a), each with what stands beside it in the formulas:
+//   kUp     [g | u] = x W_up and s = act(g) u in one kernel: a tile's 256
+//           accumulator columns are 128 of g and the same 128 of u, so a thread
+//           of the epilogue holds both factors of the product in f32;
+//   kDs     ds = dy W_down^T and [dg | du] = [ds u act'(g) | ds act(g)],
+//           s = act(g) u: ds stays in tensor memory, g and u come through
+//           shared memory beside the products;
+//   kGroup  up to three plain products in one launch (dx, dW_up and dW_down; or
+//           y alone): their tiles form one list, whose tail is cut evenly.
+// All three are 2-SM kernels: a pair of CTAs works on a 256 x 256 tile, TMA
+// feeds a ring of 64-deep k-slices, one thread issues the MMAs into one of two
+// accumulators while eight warps empty the other.  Every wait is bounded.
+#include <algorithm>
+#include <mutex>
+
+#include "glu.cuh"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace collider {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kUp = 0, kDs = 1, kGroup = 2;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;   // warp 0 TMA, warp 1 MMA and TMEM, warps 2-9 epilogue
+constexpr int kBM = 128, kBN = 256, kBK = 64;   // a CTA's rows, the pair's columns, a k-slice
+constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + 128 * kBK * 2;
+constexpr int kGroupRows = 16;    // 256-row units that follow each other down a column of tiles
+constexpr int kMaxWorkers = 80;   // CTA pairs of a launch, at most
+constexpr int kMaxTail = 1024;    // tiles of the part that is cut
+// kDs: an epilogue warp's 32 x 32 values of g, u and s, twice
+constexpr uint32_t kChunkBytes = 32 * 64, kSlotBytes = 3 * kChunkBytes;
+template <int EPI>
+struct Cfg {
+  static constexpr int kStages = EPI == kDs ? 4 : 7;
+  static constexpr uint32_t kEpiBytes = EPI == kDs ? kEpiWarps * 2 * kSlotBytes : 0;
+  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 256 + (EPI == kGroup ? 4 * (kMaxWorkers + 1) + 64 : 0);
+};
+
+struct Maps {
+  CUtensorMap m[6];   // kUp: x, W_up; kDs: dy, W_down, dg, du, s (stores); kGroup: A and B of each product
+};
+struct Params {
+  int M, F, kb;       // kUp, kDs: tokens, hidden width, k-slices
+  const int32_t* n_kept;   // null: every row
+  const int32_t* idx;      // kDs: rows of up (null: in order); kGroup: rows of a product's output that wants them
+  // kUp / kDs
+  __nv_bfloat16 *up, *s;
+  long long up_ld;
+  int* zero;          // counters that the launch behind this one starts from
+  int n_zero;
+  // kGroup
+  FfnProduct p[3];
+  int np;
+  float* partial;     // [2 * pairs][2][kBN / 4][kBM][4] f32
+  int* counters;      // [kMaxTail][2], zero on entry and left zero
+  DevStatus* st;
+};
+
+// A tile list's work: whole tiles for each pair in turn, then the tail.
+//   The tiles of all products stand in one list, the longest reductions first;
+// pair w takes tiles w, w + W, ...  Where that would leave the last wave poorly
+// filled, only the whole waves that fit the even share (all k-slices / W) are
+// given out so, and the k-slices of the tiles behind them are cut into
+// contiguous ranges, one a pair, that fill each pair up to its share.  A tile
+// cut between pairs is finished by whichever comes last, from all parts parked
+// in memory, in the order of the pairs: the same sum whoever that is.
+//   Cutting costs a chain of memory round trips at the end (park, count, read
+// back), about 4 us or 16 k-slices; less gain than that is left alone.
+constexpr int kCutGain = 16;
+constexpr int kMinRange = 6;    // k-slices of a pair's range, at least
+struct Sched {
+  int np, W, wid;
+  int units[3], tiles[3], kb[3];   // 256-row units, tiles, k-slices of each product
+  int first[4];                    // first tile of each product
+  int dp;                          // tiles given out whole
+  int tail_first[3], tail_off[4];  // first tile of each product's tail, and its k-slices before
+  const int* begin;                // [W + 1]: the ranges
+};
+__device__ __forceinline__ int count_mod(int a, int b, int w, int W) {   // t in [a, b) with t % W == w
+  if (b <= a) return 0;
+  const int lo = a + ((w - a) % W + W) % W;
+  return lo < b ? (b - 1 - lo) / W + 1 : 0;
+}
+
+struct Tile {
+  int p, k0, k1;
+  int m0, n0;     // this CTA's first row, the tile's first column
+  int t;
+  bool whole;
+};
+__device__ __forceinline__ void place(int units, int n_tiles, int t, int rank, int* m0, int* n0) {
+  const int per = kGroupRows * n_tiles, g = t / per, r = t % per;
+  const int gm = min(kGroupRows, units - g * kGroupRows);
+  *m0 = (2 * (g * kGroupRows + r % gm) + rank) * kBM;
+  *n0 = r / gm;
+}
+
+// the pair's pieces of work in order
+struct Iter {
+  const Sched& s;
+  int tile, it, end;
+  __device__ Iter(const Sched& sc) : s(sc), tile(sc.wid), it(0), end(0) {
+    if (s.dp < s.first[s.np]) {
+      it = s.begin[s.wid];
+      end = s.begin[s.wid + 1];
+    }
+  }
+  __device__ bool next(int rank, Tile* o) {
+    if (tile < s.dp) {
+      o->t = tile;
+      tile += s.W;
+      o->p = 0;
+      while (o->p + 1 < s.np && o->t >= s.first[o->p + 1]) ++o->p;
+      o->k0 = 0;
+      o->k1 = s.kb[o->p];
+    } else {
+      if (it >= end) return false;
+      o->p = 0;
+      while (o->p + 1 < s.np && it >= s.tail_off[o->p + 1]) ++o->p;
+      const int kb = s.kb[o->p], rel = it - s.tail_off[o->p];
+      o->t = s.tail_first[o->p] + rel / kb;
+      o->k0 = rel % kb;
+      o->k1 = min(kb, o->k0 + end - it);
+      it += o->k1 - o->k0;
+    }
+    o->whole = o->k0 == 0 && o->k1 == s.kb[o->p];
+    place(s.units[o->p], s.tiles[o->p] / s.units[o->p], o->t - s.first[o->p], rank, &o->m0, &o->n0);
+    return true;
+  }
+};
+
+// 32 columns of one row of a product's output
+__device__ __forceinline__ void store32(const FfnProduct& p, long long row, int col, const float* v) {
+  if (p.c_f32) {
+    float* out = static_cast<float*>(p.C) + row * p.ldc + col;
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      if (col + 4 * g + 4 <= p.N)
+        *reinterpret_cast<float4*>(out + 4 * g) = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+  } else {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + row * p.ldc + col;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (col + 8 * g + 8 <= p.N) *reinterpret_cast<uint4*>(out + 8 * g) = pack8(v + 8 * g);
+  }
+}
+__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* out, int col, int cols, const float* v) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    if (col + 8 * g + 8 <= cols) *reinterpret_cast<uint4*>(out + 8 * g) = pack8(v + 8 * g);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <int EPI, int ACT>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  constexpr int S = Cfg<EPI>::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* epi = smem + S * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + Cfg<EPI>::kEpiBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  int* begin = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S), tfull0 = smem_u32(bars + 2 * S),
+                 tempty0 = smem_u32(bars + 2 * S + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, 2 * 32 * kEpiWarps);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 2 * kBN);
+  fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer's barriers exist before any copy or commit reaches them
+  fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dep_wait();   // the kept count, the operands and the outputs are the kernels' ahead until here
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int W = gridDim.x >> 1, wid = blockIdx.x >> 1;
+  int n = p.M;
+  if (p.n_kept) n = min(p.M, max(0, *p.n_kept));
+
+  // ---------------- the tile list ----------------
+  Sched sc;
+  sc.W = W;
+  sc.wid = wid;
+  sc.begin = begin;
+  if (EPI == kGroup) {
+    sc.np = p.np;
+    int total = 0;
+    long long slices = 0;
+    for (int i = 0; i < 3; ++i) {
+      sc.first[i] = total;
+      if (i >= p.np) { sc.units[i] = 1; sc.tiles[i] = sc.kb[i] = 0; continue; }
+      const FfnProduct& q = p.p[i];
+      const int m = q.dyn == 1 ? min(q.M, n) : q.M, k = q.dyn == 2 ? min(q.K, n) : q.K;
+      sc.units[i] = (m + 2 * kBM - 1) / (2 * kBM);
+      sc.tiles[i] = sc.units[i] * ((q.N + kBN - 1) / kBN);
+      sc.kb[i] = (k + kBK - 1) / kBK;
+      total += sc.tiles[i];
+      slices += (long long)sc.tiles[i] * sc.kb[i];
+      if (sc.units[i] == 0) sc.units[i] = 1;
+    }
+    sc.first[3] = total;
+    for (int i = p.np; i < 3; ++i) sc.first[i] = total;
+    sc.dp = total;
+    // pair 0 has the most of every wave: its load if all tiles are whole, and
+    // the whole waves that fit the even share
+    const int share = (int)(slices / W);
+    int load0 = 0, waves = 0, fit = 0;
+    for (int i = 0; i < p.np; ++i) {
+      const int c = count_mod(sc.first[i], sc.first[i] + sc.tiles[i], 0, W);
+      if (waves >= 0) {
+        const int room = sc.kb[i] > 0 ? (share - fit) / sc.kb[i] : c;
+        const int take = min(c, max(0, room));
+        fit += take * sc.kb[i];
+        waves += take;
+        if (take < c) waves = -waves - 1;   // (no more)
+      }
+      load0 += c * sc.kb[i];
+    }
+    if (waves < 0) waves = -waves - 1;
+    const int dp = min(total, waves * W);
+    if (p.partial && load0 >= share + kCutGain && total - dp <= kMaxTail) {
+      sc.dp = dp;
+      int off = 0;
+      for (int i = 0; i < 3; ++i) {
+        sc.tail_first[i] = max(sc.first[i], dp);
+        sc.tail_off[i] = off;
+        if (i < p.np) off += max(0, sc.first[i] + sc.tiles[i] - sc.tail_first[i]) * sc.kb[i];
+      }
+      sc.tail_off[3] = off;
+      if (warp == 2) {
+        // a pair's range fills it up to its share; short tails go to fewer pairs
+        const int G = max(1, min(W, off / kMinRange));
+        long long before = 0, room[kMaxWorkers / 32 + 1], at[kMaxWorkers / 32 + 1];
+#pragma unroll
+        for (int j = 0; j <= kMaxWorkers / 32; ++j) {
+          const int w = lane + 32 * j;
+          int load = 0;
+          if (w < G)
+            for (int i = 0; i < p.np; ++i) load += sc.kb[i] * count_mod(sc.first[i], min(dp, sc.first[i] + sc.tiles[i]), w, W);
+          room[j] = w < G ? max(0, share + 1 - load) : 0;
+          long long x = room[j];
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          at[j] = before + x - room[j];
+          before += __shfl_sync(0xffffffffu, x, 31);
+        }
+#pragma unroll
+        for (int j = 0; j <= kMaxWorkers / 32; ++j) {
+          const int w = lane + 32 * j;
+          if (w <= W) begin[w] = w >= G ? off : (int)(before > 0 ? at[j] * off / before : (long long)off * w / G);
+        }
+      }
+    }
+    __syncthreads();
+  } else {
+    sc.np = 1;
+    sc.units[0] = (n + 2 * kBM - 1) / (2 * kBM);
+    sc.tiles[0] = sc.units[0] * ((p.F + (EPI == kUp ? 127 : 255)) / (EPI == kUp ? 128 : 256));
+    sc.kb[0] = p.kb;
+    sc.first[0] = 0;
+    for (int i = 1; i < 4; ++i) sc.first[i] = sc.tiles[0];
+    sc.dp = sc.tiles[0];
+    if (sc.units[0] == 0) sc.units[0] = 1;
+    if (p.zero && blockIdx.x == 0)
+      for (int i = threadIdx.x; i < p.n_zero; i += kThreads) p.zero[i] = 0;
+  }
+
+  if (EPI == kGroup && p.n_kept && n == 0) {
+    // nothing kept: sums over the kept rows are 0
+    if (warp >= 2)
+      for (int i = 0; i < p.np; ++i) {
+        const FfnProduct& q = p.p[i];
+        if (q.dyn != 2) continue;
+        float z[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) z[e] = 0.f;
+        const int cols = (q.N + 31) / 32;
+        for (long long e = blockIdx.x * (long long)(32 * kEpiWarps) + threadIdx.x - 64; e < (long long)q.M * cols;
+             e += (long long)gridDim.x * 32 * kEpiWarps)
+          store32(q, e / cols, (int)(e % cols) * 32, z);
+      }
+  } else if (warp == 0) {
+    // ---------------- TMA producer: the converged warp waits, one elected lane issues ----------------
+    const bool leader = elect_one();
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned site) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.st, site)) != 0;
+    };
+    auto aborted = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;   // stages with copies issued, and the phase parity armed
+    Iter iter(sc);
+    Tile t;
+    while (iter.next(rank, &t) && !aborted()) {
+      const CUtensorMap* ma = &maps.m[EPI == kGroup ? 2 * t.p : 0];
+      const CUtensorMap* mb = ma + 1;
+      const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
+      // this CTA's half of the tile's columns: of kUp, all 128 of g or of u
+      const int nb = EPI == kUp ? t.n0 * 128 + rank * p.F : t.n0 * kBN + rank * 128;
+      bool ok = true;
+      for (int kb = t.k0; kb < t.k1; ++kb) {
+        if (!wait(empty0 + 8 * stage, phase ^ 1u, 1)) { ok = false; break; }
+        const uint32_t fb = full0 + 8 * stage;
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (leader) {
+          const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+          const int kx = kb * kBK;
+          if (rank == 0) mbar_expect_tx(fb, 2 * kStageBytes);   // both CTAs' copies are counted on the even CTA's barrier
+          const uint32_t lb = map_to_rank(fb, 0);
+          if (!a_mn) {
+            tma_load_2d_pair(sa, ma, lb, kx, t.m0);
+          } else {
+            tma_load_2d_pair(sa, ma, lb, t.m0, kx);
+            tma_load_2d_pair(sa + 8192, ma, lb, t.m0 + 64, kx);
+          }
+          if (!b_mn) {
+            tma_load_2d_pair(sb, mb, lb, kx, nb);
+          } else {
+            tma_load_2d_pair(sb, mb, lb, nb, kx);
+            tma_load_2d_pair(sb + 8192, mb, lb, nb + 64, kx);
+          }
+        }
+        __syncwarp();
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+    }
+    if (!aborted()) {
+      // both MMAs release every stage (their commits land in this CTA's empty
+      // barriers) before this CTA may leave the cluster
+      for (int i = 0; i < S; ++i) {
+        if (!wait(empty0 + 8 * stage, phase ^ 1u, 5)) break;
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (aborted() && leader) {
+      // another role gave up: let this thread's copies still in flight land
+      // (bounded, 10 ms per stage) before the CTA releases its shared memory
+      for (int s = 0; s < S; ++s) {
+        if (!((armed >> s) & 1u)) continue;
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try(full0 + 8 * s, (armed_parity >> s) & 1u) && globaltimer_ns() - t0 < 10000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ---------------- MMA issuer (the even CTA) ----------------
+      const bool leader = elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity, unsigned site) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.st, site)) != 0;
+      };
+      int stage = 0;
+      uint32_t phase = 0;
+      int seg = 0;
+      Iter iter(sc);
+      Tile t;
+      while (iter.next(rank, &t) && !__any_sync(0xffffffffu, *abort_flag != 0)) {
+        const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
+        const uint32_t idesc = idesc_bf16(2 * kBM, kBN, a_mn, b_mn);
+        const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32, a_lbo = a_mn ? 8192 : 16, b_lbo = b_mn ? 8192 : 16;
+        const int acc = seg & 1;
+        if (!wait(tempty0 + 8 * acc, ((seg >> 1) & 1) ^ 1u, 2)) break;
+        fence_after();
+        const uint32_t d = tmem_base + acc * kBN;
+        bool ok = true;
+        for (int kb = t.k0; kb < t.k1; ++kb) {
+          if (!wait(full0 + 8 * stage, phase, 3)) { ok = false; break; }
+          fence_after();
+          if (leader) {
+            const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_bf16_pair(d, sdesc(sa + kk * a_step, a_lbo, 1024), sdesc(sb + kk * b_step, b_lbo, 1024), idesc,
+                            (kb > t.k0) || (kk > 0));
+            mma_commit_pair_mc(empty0 + 8 * stage, 3);
+          }
+          __syncwarp();
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if (leader) mma_commit_pair_mc(tfull0 + 8 * acc, 3);
+        __syncwarp();
+        ++seg;
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 2..9) ----------------
+    auto release_acc = [&](int acc) { mbar_arrive_cluster(map_to_rank(tempty0 + 8 * acc, 0)); };
+    volatile int no_abort = 0;   // (timeout-only waits: the threads leave together)
+    const int q = warp & 3;      // TMEM lane quadrant this warp may access
+    const int half = (warp - 2) >> 2;
+    const int rl = q * 32 + lane;
+    int seg = 0;
+    Iter iter(sc);
+    Tile t;
+    if constexpr (EPI == kUp) {
+      while (iter.next(rank, &t)) {
+        const int acc = seg & 1;
+        const int row = t.m0 + rl;
+        if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
+        fence_after();
+        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 64;
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          float g[32], u[32];
+          tmem_ld32(tc0 + c, g);
+          tmem_ld32(tc0 + 128 + c, u);
+          if (c == 32) {
+            fence_before();
+            release_acc(acc);
+          }
+          const int col = t.n0 * 128 + half * 64 + c;
+          if (row >= n) continue;
+          if (p.up) {
+            __nv_bfloat16* o = p.up + (long long)row * p.up_ld + col;
+            store_bf16x32(o, col, p.F, g);
+            store_bf16x32(o + p.F, col, p.F, u);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g[i] = glu_act<ACT>(g[i]) * u[i];
+          store_bf16x32(p.s + (long long)row * p.F + col, col, p.F, g);
+        }
+        ++seg;
+      }
+    } else if constexpr (EPI == kDs) {
+      // A chunk is 32 rows x 32 columns of this warp.  Its g and u are copied to
+      // shared memory (16-byte pieces, their order within 64-byte rows XORed
+      // with bits of the row, the layout the stores expect), one chunk ahead of
+      // the one in work, the next tile's first two before its products are
+      // done; [dg | du] and s take their places and leave by TMA.
+      const uint32_t slots = smem_u32(epi) + (warp - 2) * 2 * kSlotBytes;
+      const uint32_t sw = ((lane >> 1) & 3) * 16;             // of this thread's row
+      const int prow = lane >> 2, piece = lane & 3;           // the copies' rows: prow + 8 i
+      int ahead = 0;         // copies begun in all (slot = ahead & 1)
+      // rows of `up` that a tile's copies read (row prow + 8 i of the warp's 32), -1: none
+      int src[4];
+      auto rows_of_tile = [&](const Tile& x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = x.m0 + q * 32 + prow + 8 * i;
+          int s = r < n ? r : -1;
+          if (s >= 0 && p.idx) {
+            s = p.idx[r];
+            if ((unsigned)s >= (unsigned)p.M) {
+              report_error(p.st, kErrBadIndex, 702);
+              s = -1;
+            }
+          }
+          src[i] = s;
+        }
+      };
+      auto copy = [&](const Tile& x, int c) {
+        const uint32_t dst = slots + (ahead & 1) * kSlotBytes;
+        const int col = x.n0 * kBN + half * 128 + c * 32 + piece * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = prow + 8 * i;
+          const bool there = src[i] >= 0 && col < p.F;
+          const __nv_bfloat16* g = p.up + (there ? src[i] * p.up_ld + col : 0);
+          const uint32_t at = dst + r * 64 + ((piece ^ ((r >> 1) & 3)) * 16);
+          cp_async16(at, g, there);
+          cp_async16(at + kChunkBytes, g + (there ? p.F : 0), there);
+        }
+        cp_async_commit();
+        ++ahead;
+      };
+      bool more = iter.next(rank, &t);
+      if (more) {
+        rows_of_tile(t);
+        copy(t, 0);
+        copy(t, 1);
+      }
+      int done = 0;          // chunks worked on
+      while (more) {
+        Tile nx;
+        const bool next = iter.next(rank, &nx);
+        const int acc = seg & 1;
+        const int row = t.m0 + rl;
+        if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
+        fence_after();
+        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 128;
+        for (int c = 0; c < 4; ++c) {
+          float d[32];
+          tmem_ld32(tc0 + c * 32, d);
+          if (c == 3) {
+            fence_before();
+            release_acc(acc);
+          }
+          if (row >= n) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) d[i] = 0.f;
+          }
+          cp_async_wait<1>();
+          __syncwarp();
+          const uint32_t buf = slots + (done & 1) * kSlotBytes + lane * 64;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t at = buf + ((j * 16) ^ sw);
+            float g[8], u[8], s[8];
+            unpack8(lds128(at), g);
+            unpack8(lds128(at + kChunkBytes), u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float a, da;
+              glu_both<ACT>(g[i], &a, &da);
+              s[i] = a * u[i];
+              g[i] = d[8 * j + i] * u[i] * da;
+              u[i] = d[8 * j + i] * a;
+            }
+            sts128(at, pack8(g));
+            sts128(at + kChunkBytes, pack8(u));
+            sts128(at + 2 * kChunkBytes, pack8(s));
+          }
+          fence_async_smem();
+          __syncwarp();
+          const int col = t.n0 * kBN + half * 128 + c * 32, r0 = t.m0 + q * 32;
+          if (lane == 0) {
+            if (col < p.F && r0 < (int)p.p[0].M) {   // (p[0].M: rows of the outputs' buffers)
+              const uint32_t b = slots + (done & 1) * kSlotBytes;
+              tma_store_2d(&maps.m[2], b, col, r0);
+              tma_store_2d(&maps.m[3], b + kChunkBytes, col, r0);
+              tma_store_2d(&maps.m[4], b + 2 * kChunkBytes, col, r0);
+            }
+            bulk_commit();
+            bulk_wait_read_all();   // the slot is read out before the copies below fill it again
+          }
+          __syncwarp();
+          ++done;
+          if (c < 2) {
+            copy(t, c + 2);
+          } else if (next) {
+            if (c == 2) rows_of_tile(nx);
+            copy(nx, c - 2);
+          } else {
+            cp_async_commit();      // (an empty group keeps the count)
+            ++ahead;
+          }
+        }
+        t = nx;
+        more = next;
+        ++seg;
+      }
+      cp_async_wait<0>();
+      if (lane == 0) bulk_wait_all();
+    } else {
+      while (iter.next(rank, &t)) {
+        const FfnProduct& pr = p.p[t.p];
+        const int acc = seg & 1;
+        const int M = pr.dyn == 1 ? min(pr.M, n) : pr.M;
+        const int row = t.m0 + rl;
+        bool row_ok = row < M;
+        long long out_row = row;
+        if (pr.scatter && row_ok) {
+          const int o = p.idx[row];
+          row_ok = o >= 0 && o < pr.c_rows;
+          out_row = o;
+          if (!row_ok) report_error(p.st, kErrBadIndex, 703);
+        }
+        // rows behind the kept ones that a COMPACT output holds zeros in
+        const bool row_zero = !row_ok && pr.zero_pad && row < padded_rows(M, pr.c_rows);
+        if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
+        fence_after();
+        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 128;
+        const int col0 = t.n0 * kBN + half * 128;
+        if (t.whole) {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            float v[32];
+            tmem_ld32(tc0 + c, v);
+            if (c == 96) {
+              fence_before();
+              release_acc(acc);
+            }
+            if (row_zero) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            }
+            if (row_ok || row_zero) store32(pr, out_row, col0 + c, v);
+          }
+        } else {
+          // part of a tile: park it, and finish the tile if this pair is the last
+          auto owner = [&](int x) {
+            int lo = 0, hi = W - 1;   // the last pair whose range begins at or before x (and is not empty)
+            while (lo < hi) {
+              const int mid = (lo + hi + 1) >> 1;
+              if (begin[mid] <= x) lo = mid; else hi = mid - 1;
+            }
+            return lo;
+          };
+          const int x0 = sc.tail_off[t.p] + (t.t - sc.tail_first[t.p]) * sc.kb[t.p], x1 = x0 + sc.kb[t.p];
+          const int c_first = owner(x0), c_last = owner(x1 - 1);
+          // A pair parks at most two parts: in place 0 of the tile its range
+          // begins in, in place 1 of the tile it ends in.
+          auto slot_of = [&](int w) {
+            const int at = 2 * w + (begin[w] >= x0 && begin[w] < x1 ? 0 : 1);
+            return p.partial + ((long long)at * 2 + rank) * (kBM * kBN);
+          };
+          float* own = slot_of(wid);
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            float v[32];
+            tmem_ld32(tc0 + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              __stcg(reinterpret_cast<float4*>(own + ((long long)((half * 128 + c + i) >> 2) * kBM + rl) * 4),
+                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+          }
+          fence_before();
+          release_acc(acc);
+          __threadfence();
+          named_bar(1, 32 * kEpiWarps);
+          if (threadIdx.x == 64) {
+            int parts = 0;
+            for (int w = c_first; w <= c_last; ++w) parts += begin[w] < begin[w + 1];
+            int* ctr = p.counters + (long long)(t.t - sc.dp) * 2 + rank;
+            const int last = atomicAdd(ctr, 1) == parts - 1;
+            if (last) *ctr = 0;
+            *last_flag = last;
+          }
+          named_bar(1, 32 * kEpiWarps);
+          if (*last_flag && (row_ok || row_zero)) {
+            __threadfence();
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+              for (int w = c_first; w <= c_last; ++w) {
+                if (begin[w] == begin[w + 1]) continue;
+                const float* from = slot_of(w);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 x =
+                      __ldcg(reinterpret_cast<const float4*>(from + ((long long)((half * 128 + c + i) >> 2) * kBM + rl) * 4));
+                  v[i] += x.x; v[i + 1] += x.y; v[i + 2] += x.z; v[i + 3] += x.w;
+                }
+              }
+              if (row_zero) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+              }
+              store32(pr, out_row, col0 + c, v);
+            }
+          }
+          named_bar(1, 32 * kEpiWarps);   // last_flag is reused by the next piece
+        }
+        ++seg;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kBN);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+template <int EPI, int ACT>
+cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, const Params& p, long long tiles, long long m, long long n,
+                   long long k, int dyn) {
+  auto kern = ffn_kernel<EPI, ACT>;
+  constexpr size_t smem = Cfg<EPI>::kSmem;
+  // per device, once: the shared-memory opt-in, and how many pairs run at once
+  static std::mutex mu;
+  static int known[64] = {0};
+  int dev = 0, pairs = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev >= 0 && dev < 64) pairs = known[dev];
+    if (pairs == 0) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(2 * (c.num_sms / 2));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      pairs = std::min({pairs, c.num_sms / 2, kMaxWorkers});
+      if (pairs < 1) return cudaErrorNotSupported;
+      if (dev >= 0 && dev < 64) known[dev] = pairs;
+    }
+  }
+  // (a group's tail may go to every pair)
+  const int grid = 2 * (EPI == kGroup ? pairs : (int)std::max(1ll, std::min<long long>(tiles, pairs)));
+  prof_begin(c, name, m, n, k, dyn);
+  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(grid), dim3(kThreads), smem, 2, maps, p);
+  prof_end(c);
+  count_launch();
+  return launched(e);
+}
+
+bool k_major(CUtensorMap* m, const void* p, long long inner, long long rows, long long ld) {
+  return make_tensor_map(m, p, false, inner, rows, ld, 64, 128);
+}
+bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, long long ld) {
+  return make_tensor_map(m, p, false, inner, rows, ld, 64, 64);
+}
+
+}  // namespace
+
+size_t ffn_partial_floats() { return (size_t)2 * kMaxWorkers * 2 * kBM * kBN; }
+int ffn_counters() { return 2 * kMaxTail; }
+
+cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
+  Maps maps{};
+  if (!k_major(&maps.m[0], a.x, a.D, a.M, a.x_ld) || !mn_major(&maps.m[1], a.w_up, 2ll * a.F, a.D, 2ll * a.F))
+    return cudaErrorInvalidValue;
+  Params p{};
+  p.M = a.M; p.F = a.F; p.kb = (a.D + kBK - 1) / kBK;
+  p.up = a.up; p.up_ld = a.up_ld; p.s = a.s;
+  p.zero = a.counters; p.n_zero = ffn_counters();
+  p.st = c.st;
+  const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 127) / 128);
+  return a.act == kGluSilu ? launch<kUp, kGluSilu>(c, "ffn_up", maps, p, tiles, a.M, 2ll * a.F, a.D, 0)
+                           : launch<kUp, kGluGeluTanh>(c, "ffn_up", maps, p, tiles, a.M, 2ll * a.F, a.D, 0);
+}
+
+cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a) {
+  Maps maps{};
+  bool ok = k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld) && k_major(&maps.m[1], a.w_down, a.D, a.F, a.D);
+  // each half of [dg | du] has a map of its own: a store stops at its last column
+  ok = ok && make_store_map(&maps.m[2], a.dgu, a.F, a.cap, 2ll * a.F) && make_store_map(&maps.m[3], a.dgu + a.F, a.F, a.cap, 2ll * a.F) &&
+       make_store_map(&maps.m[4], a.s, a.F, a.cap, a.F);
+  if (!ok) return cudaErrorInvalidValue;
+  Params p{};
+  p.M = a.M; p.F = a.F; p.kb = (a.D + kBK - 1) / kBK;
+  p.n_kept = a.n_kept; p.idx = a.up_full ? a.idx : nullptr;
+  p.up = const_cast<__nv_bfloat16*>(a.up); p.up_ld = a.up_ld;
+  p.p[0].M = (int)a.cap;
+  p.zero = a.counters; p.n_zero = ffn_counters();
+  p.st = c.st;
+  const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 255) / 256);
+  const int dyn = a.n_kept ? 1 : 0;
+  return a.act == kGluSilu ? launch<kDs, kGluSilu>(c, "ffn_ds", maps, p, tiles, a.M, a.F, a.D, dyn)
+                           : launch<kDs, kGluGeluTanh>(c, "ffn_ds", maps, p, tiles, a.M, a.F, a.D, dyn);
+}
+
+cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, const int32_t* idx, const int32_t* n_kept,
+                             float* partial, int* counters) {
+  Maps maps{};
+  Params p{};
+  for (int i = 0; i < np; ++i) {
+    const bool a_ok = q[i].a_mn ? mn_major(&maps.m[2 * i], q[i].A, q[i].M, q[i].a_rows, q[i].lda)
+                                : k_major(&maps.m[2 * i], q[i].A, q[i].K, q[i].a_rows, q[i].lda);
+    const bool b_ok = q[i].b_mn ? mn_major(&maps.m[2 * i + 1], q[i].B, q[i].N, q[i].b_rows, q[i].ldb)
+                                : k_major(&maps.m[2 * i + 1], q[i].B, q[i].K, q[i].b_rows, q[i].ldb);
+    if (!a_ok || !b_ok) return cudaErrorInvalidValue;
+    p.p[i] = q[i];
+  }
+  p.np = np;
+  p.M = M; p.idx = idx; p.n_kept = n_kept;
+  p.partial = partial; p.counters = counters;
+  p.st = c.st;
+  return launch<kGroup, 0>(c, "ffn_group", maps, p, 0, q[0].M, q[0].N, q[0].K, q[0].dyn);
+}
+
+}  // namespace collider

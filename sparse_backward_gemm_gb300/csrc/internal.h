@@ -425,13 +425,46 @@ struct FfnPrep {
   const int32_t* n_kept;
 };
 cudaError_t launch_ffn_prep(const Ctx& c, const FfnPrep& p);
-// up = bf16(acc) (may be null), s = bf16(act(g) u) of the f32 acc [M, 2F] = [g | u]
-cudaError_t launch_glu_fwd(const Ctx& c, int act, int M, int F, const float* acc, __nv_bfloat16* up, long long up_ld,
-                           __nv_bfloat16* s);
-// dgu = bf16([ds u act'(g) | ds act(g)]), s = bf16(act(g) u) for the kept rows, zero rows up to 128;
-// ds f32 [*, F] COMPACT; up FULL (read through idx) or COMPACT; idx and n_kept null: all M rows
-cudaError_t launch_glu_bwd(const Ctx& c, int act, int M, int F, const float* ds, const __nv_bfloat16* up, long long up_ld,
-                           int up_full, __nv_bfloat16* dgu, __nv_bfloat16* s, long long cap, const int32_t* idx,
-                           const int32_t* n_kept);
+// The products (ffn_tc.cu).  counters: ffn_counters() ints that launch_ffn_up
+// and launch_ffn_ds set to 0 for a launch_ffn_group behind them in the stream;
+// partial: ffn_partial_floats() floats of scratch.
+size_t ffn_partial_floats();
+int ffn_counters();
+// up = bf16(x W_up) (may be null), s = bf16(act(g) u) of the f32 [g | u]
+struct FfnUp {
+  int act, M, D, F;
+  const void* x; long long x_ld;
+  const void* w_up;
+  __nv_bfloat16* up; long long up_ld;
+  __nv_bfloat16* s;   // [M, F]
+  int* counters;
+};
+cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a);
+// dgu = bf16([ds u act'(g) | ds act(g)]) of the f32 ds = dy W_down^T, and s =
+// bf16(act(g) u), of the kept rows (n_kept null: all M), in order; [g | u] =
+// up's rows through idx (up_full) or in order.  Rows up to the next multiple of
+// 128 are 0.
+struct FfnDs {
+  int act, M, D, F;
+  const void* dy; long long dy_ld, dy_rows;
+  const void* w_down;
+  const __nv_bfloat16* up; long long up_ld; int up_full;
+  __nv_bfloat16 *dgu, *s;   // [cap, 2F], [cap, F]
+  long long cap;            // a multiple of 128
+  const int32_t *idx, *n_kept;
+  int* counters;
+};
+cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a);
+// C[m, n] = sum_k A(m, k) B(n, k), operands stored as TcGemm's.  dyn 1: M, 2: K
+// is limited by *n_kept.  C bf16 or f32; scatter: row m goes to row idx[m] (kept
+// below c_rows); zero_pad: rows up to the next multiple of 128 (below c_rows) are 0.
+struct FfnProduct {
+  int M, N, K, dyn;
+  const void* A; long long lda, a_rows; int a_mn;
+  const void* B; long long ldb, b_rows; int b_mn;
+  void* C; long long ldc, c_rows; int c_f32, scatter, zero_pad;
+};
+cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, const int32_t* idx, const int32_t* n_kept,
+                             float* partial, int* counters);
 
 }  // namespace collider
