@@ -32,32 +32,33 @@ constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + 128 * kBK * 
 constexpr int kGroupRows = 16;    // 256-row units that follow each other down a column of tiles
 constexpr int kMaxWorkers = 80;   // CTA pairs of a launch, at most
 constexpr int kMaxTail = 1024;    // tiles of the part that is cut
-// kDs: an epilogue warp's 32 x 32 values of g, u and s, twice
-constexpr uint32_t kChunkBytes = 32 * 64, kSlotBytes = 3 * kChunkBytes;
+// kDs: an epilogue warp's 32 x 32 values of g and u, twice
+constexpr uint32_t kChunkBytes = 32 * 64, kSlotBytes = 2 * kChunkBytes;
 template <int EPI>
 struct Cfg {
-  static constexpr int kStages = EPI == kDs ? 4 : 7;
+  static constexpr int kStages = EPI == kDs ? 5 : 7;
   static constexpr uint32_t kEpiBytes = EPI == kDs ? kEpiWarps * 2 * kSlotBytes : 0;
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 256 + (EPI == kGroup ? 4 * (kMaxWorkers + 1) + 64 : 0);
 };
 
 struct Maps {
-  CUtensorMap m[6];   // kUp: x, W_up; kDs: dy, W_down, dg, du, s (stores); kGroup: A and B of each product
+  CUtensorMap m[6];   // A and B of each product
 };
 struct Params {
   int M, F, kb;       // kUp, kDs: tokens, hidden width, k-slices
   const int32_t* n_kept;   // null: every row
   const int32_t* idx;      // kDs: rows of up (null: in order); kGroup: rows of a product's output that wants them
-  // kUp / kDs
-  __nv_bfloat16 *up, *s;
-  long long up_ld;
+  // kUp (up null: not kept) / kDs
+  __nv_bfloat16 *up, *s, *dgu;
+  long long up_ld, cap;    // cap: rows of dgu and s
   int* zero;          // counters that the launch behind this one starts from
   int n_zero;
   // kGroup
   FfnProduct p[3];
   int np;
+  uint32_t by_pairs;  // 2^32 / pairs, rounded up
   float* partial;     // [2 * pairs][2][kBN / 4][kBM][4] f32
-  int* counters;      // [kMaxTail][2], zero on entry and left zero
+  int* counters;      // [kMaxTail][2][2], zero on entry and left zero
   DevStatus* st;
 };
 
@@ -67,8 +68,9 @@ struct Params {
 // filled, only the whole waves that fit the even share (all k-slices / W) are
 // given out so, and the k-slices of the tiles behind them are cut into
 // contiguous ranges, one a pair, that fill each pair up to its share.  A tile
-// cut between pairs is finished by whichever comes last, from all parts parked
-// in memory, in the order of the pairs: the same sum whoever that is.
+// cut between pairs is finished by whichever comes last, which adds the
+// parts that the others parked in memory and its own accumulator, in the order
+// of the pairs: the same sum whoever that is.
 //   Cutting costs a chain of memory round trips at the end (park, count, read
 // back), about 4 us or 16 k-slices; less gain than that is left alone.
 constexpr int kCutGain = 16;
@@ -81,10 +83,10 @@ struct Sched {
   int tail_first[3], tail_off[4];  // first tile of each product's tail, and its k-slices before
   const int* begin;                // [W + 1]: the ranges
 };
-__device__ __forceinline__ int count_mod(int a, int b, int w, int W) {   // t in [a, b) with t % W == w
-  if (b <= a) return 0;
-  const int lo = a + ((w - a) % W + W) % W;
-  return lo < b ? (b - 1 - lo) / W + 1 : 0;
+// t in [a, b) with t % W == w; magic: 2^32 / W rounded up (exact below 2^32 / W)
+__device__ __forceinline__ int count_mod(int a, int b, int w, uint32_t magic) {
+  const int fa = a > w ? (int)__umulhi(a - w - 1, magic) + 1 : 0, fb = b > w ? (int)__umulhi(b - w - 1, magic) + 1 : 0;
+  return max(0, fb - fa);
 }
 
 struct Tile {
@@ -134,50 +136,87 @@ struct Iter {
   }
 };
 
-// 32 columns of one row of a product's output
-__device__ __forceinline__ void store32(const FfnProduct& p, long long row, int col, const float* v) {
-  if (p.c_f32) {
-    float* out = static_cast<float*>(p.C) + row * p.ldc + col;
+// Four 16-byte pieces of each lane's row become one piece of each of four rows:
+// piece (lane & 3) of rows (lane & ~3) + i, so that four lanes store 64 bytes of
+// one row together (a lane that stores pieces of its own row alone touches 32
+// lines with every instruction, four times the L1 cycles).
+__device__ __forceinline__ void transpose4(uint4* v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int g = 0; g < 8; ++g)
-      if (col + 4 * g + 4 <= p.N)
-        *reinterpret_cast<float4*>(out + 4 * g) = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-  } else {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + row * p.ldc + col;
+  for (int st = 1; st <= 2; st <<= 1) {
+    const bool hi = (lane & st) != 0;
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      if (col + 8 * g + 8 <= p.N) *reinterpret_cast<uint4*>(out + 8 * g) = pack8(v + 8 * g);
+    for (int j = 0; j < 4; ++j) {
+      if (j & st) continue;
+      uint4& a = v[j];
+      uint4& b = v[j + st];
+      uint4 s = hi ? a : b;
+      s.x = __shfl_xor_sync(0xffffffffu, s.x, st);
+      s.y = __shfl_xor_sync(0xffffffffu, s.y, st);
+      s.z = __shfl_xor_sync(0xffffffffu, s.z, st);
+      s.w = __shfl_xor_sync(0xffffffffu, s.w, st);
+      if (hi) a = s; else b = s;
+    }
   }
 }
-__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* out, int col, int cols, const float* v) {
+// The rows that this lane stores to, as offsets (elements), -1: none; of the
+// lane's own row `off`, by the whole warp.
+struct Rows4 {
+  long long off[4];
+  __device__ __forceinline__ explicit Rows4(long long own) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
-    if (col + 8 * g + 8 <= cols) *reinterpret_cast<uint4*>(out + 8 * g) = pack8(v + 8 * g);
+    for (int i = 0; i < 4; ++i) off[i] = __shfl_sync(0xffffffffu, own, (threadIdx.x & 28) + i);
+  }
+};
+// 32 bf16 columns from `col` on (below cols) of the warp's 32 rows; v: this
+// lane's row.  By the whole warp.
+__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* base, const Rows4& rows, int col, int cols, const uint4* packed) {
+  uint4 v[4] = {packed[0], packed[1], packed[2], packed[3]};
+  transpose4(v);
+  col += 8 * (threadIdx.x & 3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (rows.off[i] >= 0 && col < cols) *reinterpret_cast<uint4*>(base + rows.off[i] + col) = v[i];
+}
+__device__ __forceinline__ void pack32(const float* v, uint4* o) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) o[g] = pack8(v + 8 * g);
+}
+// the same of a product's output, bf16 or f32
+__device__ __forceinline__ void store32(const FfnProduct& p, const Rows4& rows, int col, const float* v) {
+  uint4 w[4];
+  if (!p.c_f32) {
+    pack32(v, w);
+    store_bf16x32(static_cast<__nv_bfloat16*>(p.C), rows, col, p.N, w);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = make_uint4(__float_as_uint(v[16 * h + 4 * i]), __float_as_uint(v[16 * h + 4 * i + 1]),
+                        __float_as_uint(v[16 * h + 4 * i + 2]), __float_as_uint(v[16 * h + 4 * i + 3]));
+    transpose4(w);
+    const int c = col + 16 * h + 4 * (threadIdx.x & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (rows.off[i] >= 0 && c < p.N) *reinterpret_cast<uint4*>(static_cast<float*>(p.C) + rows.off[i] + c) = w[i];
+  }
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(x), "r"(y)
-               : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 template <int EPI, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
@@ -206,6 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 0 && lane < (EPI == kGroup ? 2 * p.np : 2))
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.m[lane])) : "memory");
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 2 * kBN);
   fence_before();
   __syncthreads();
@@ -244,22 +285,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     sc.dp = total;
     // pair 0 has the most of every wave: its load if all tiles are whole, and
     // the whole waves that fit the even share
-    const int share = (int)(slices / W);
-    int load0 = 0, waves = 0, fit = 0;
+    const uint32_t magic = p.by_pairs;
+    const int share = slices < (1ll << 30) ? (int)__umulhi((uint32_t)slices, magic) : 0;   // (within one of slices / W)
+    int load0 = 0, waves = 0, fit = 0, left = 0;
+    bool full = false;
     for (int i = 0; i < p.np; ++i) {
-      const int c = count_mod(sc.first[i], sc.first[i] + sc.tiles[i], 0, W);
-      if (waves >= 0) {
-        const int room = sc.kb[i] > 0 ? (share - fit) / sc.kb[i] : c;
-        const int take = min(c, max(0, room));
-        fit += take * sc.kb[i];
-        waves += take;
-        if (take < c) waves = -waves - 1;   // (no more)
-      }
+      const int c = count_mod(sc.first[i], sc.first[i] + sc.tiles[i], 0, magic);
       load0 += c * sc.kb[i];
+      if (full || sc.kb[i] == 0) continue;
+      const int take = min(c, max(0, (share - fit) / sc.kb[i]));
+      fit += take * sc.kb[i];
+      waves += take;
+      left = sc.kb[i];
+      full = take < c;
     }
-    if (waves < 0) waves = -waves - 1;
+    // (ranges shorter than a tile would cut tiles into more than two: a wave more for them)
+    if (waves > 0 && share - fit < left) --waves;
     const int dp = min(total, waves * W);
-    if (p.partial && load0 >= share + kCutGain && total - dp <= kMaxTail) {
+    if (p.partial && share > 0 && load0 >= share + kCutGain && total - dp <= kMaxTail) {
       sc.dp = dp;
       int off = 0;
       for (int i = 0; i < 3; ++i) {
@@ -271,27 +314,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == 2) {
         // a pair's range fills it up to its share; short tails go to fewer pairs
         const int G = max(1, min(W, off / kMinRange));
-        long long before = 0, room[kMaxWorkers / 32 + 1], at[kMaxWorkers / 32 + 1];
+        int before = 0, at[kMaxWorkers / 32 + 1];
 #pragma unroll
         for (int j = 0; j <= kMaxWorkers / 32; ++j) {
           const int w = lane + 32 * j;
           int load = 0;
           if (w < G)
-            for (int i = 0; i < p.np; ++i) load += sc.kb[i] * count_mod(sc.first[i], min(dp, sc.first[i] + sc.tiles[i]), w, W);
-          room[j] = w < G ? max(0, share + 1 - load) : 0;
-          long long x = room[j];
+            for (int i = 0; i < p.np; ++i) load += sc.kb[i] * count_mod(sc.first[i], min(dp, sc.first[i] + sc.tiles[i]), w, magic);
+          const int room = w < G ? max(1, share + 1 - load) : 0;
+          int x = room;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
           }
-          at[j] = before + x - room[j];
+          at[j] = before + x - room;
           before += __shfl_sync(0xffffffffu, x, 31);
         }
+        const float ratio = __fdividef((float)off, (float)before);   // (rounding moves a cut by a few k-slices at most)
 #pragma unroll
         for (int j = 0; j <= kMaxWorkers / 32; ++j) {
           const int w = lane + 32 * j;
-          if (w <= W) begin[w] = w >= G ? off : (int)(before > 0 ? at[j] * off / before : (long long)off * w / G);
+          if (w <= W) begin[w] = w >= G ? off : min(off, (int)((float)at[j] * ratio));
         }
       }
     }
@@ -315,13 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < p.np; ++i) {
         const FfnProduct& q = p.p[i];
         if (q.dyn != 2) continue;
-        float z[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) z[e] = 0.f;
-        const int cols = (q.N + 31) / 32;
-        for (long long e = blockIdx.x * (long long)(32 * kEpiWarps) + threadIdx.x - 64; e < (long long)q.M * cols;
-             e += (long long)gridDim.x * 32 * kEpiWarps)
-          store32(q, e / cols, (int)(e % cols) * 32, z);
+        const long long bytes = (long long)q.M * q.ldc * (q.c_f32 ? 4 : 2);   // (a weight gradient's rows are contiguous)
+        for (long long e = (blockIdx.x * (long long)(32 * kEpiWarps) + threadIdx.x - 64) * 16; e < bytes;
+             e += (long long)gridDim.x * 32 * kEpiWarps * 16)
+          *reinterpret_cast<uint4*>(static_cast<char*>(q.C) + e) = make_uint4(0, 0, 0, 0);
       }
   } else if (warp == 0) {
     // ---------------- TMA producer: the converged warp waits, one elected lane issues ----------------
@@ -442,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (iter.next(rank, &t)) {
         const int acc = seg & 1;
         const int row = t.m0 + rl;
+        const Rows4 up_rows(row < n ? row * p.up_ld : -1), s_rows(row < n ? (long long)row * p.F : -1);
         if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
         fence_after();
         const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 64;
@@ -455,31 +497,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             release_acc(acc);
           }
           const int col = t.n0 * 128 + half * 64 + c;
-          if (row >= n) continue;
+          uint4 w[4];
           if (p.up) {
-            __nv_bfloat16* o = p.up + (long long)row * p.up_ld + col;
-            store_bf16x32(o, col, p.F, g);
-            store_bf16x32(o + p.F, col, p.F, u);
+            pack32(g, w);
+            store_bf16x32(p.up, up_rows, col, p.F, w);
+            pack32(u, w);
+            store_bf16x32(p.up + p.F, up_rows, col, p.F, w);
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] = glu_act<ACT>(g[i]) * u[i];
-          store_bf16x32(p.s + (long long)row * p.F + col, col, p.F, g);
+          pack32(g, w);
+          store_bf16x32(p.s, s_rows, col, p.F, w);
         }
         ++seg;
       }
     } else if constexpr (EPI == kDs) {
       // A chunk is 32 rows x 32 columns of this warp.  Its g and u are copied to
       // shared memory (16-byte pieces, their order within 64-byte rows XORed
-      // with bits of the row, the layout the stores expect), one chunk ahead of
-      // the one in work, the next tile's first two before its products are
-      // done; [dg | du] and s take their places and leave by TMA.
+      // with bits of the row, so that the lanes' reads of their own rows meet
+      // no bank twice), two chunks ahead of the one in work; a tile's first two
+      // before its products are done.
       const uint32_t slots = smem_u32(epi) + (warp - 2) * 2 * kSlotBytes;
       const uint32_t sw = ((lane >> 1) & 3) * 16;             // of this thread's row
       const int prow = lane >> 2, piece = lane & 3;           // the copies' rows: prow + 8 i
       int ahead = 0;         // copies begun in all (slot = ahead & 1)
       // rows of `up` that a tile's copies read (row prow + 8 i of the warp's 32), -1: none
-      int src[4];
-      auto rows_of_tile = [&](const Tile& x) {
+      int src[4], src_next[4];
+      auto rows_of_tile = [&](const Tile& x, int* to) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = x.m0 + q * 32 + prow + 8 * i;
@@ -491,17 +535,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               s = -1;
             }
           }
-          src[i] = s;
+          to[i] = s;
         }
       };
-      auto copy = [&](const Tile& x, int c) {
+      auto copy = [&](const Tile& x, const int* from, int c) {
         const uint32_t dst = slots + (ahead & 1) * kSlotBytes;
         const int col = x.n0 * kBN + half * 128 + c * 32 + piece * 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = prow + 8 * i;
-          const bool there = src[i] >= 0 && col < p.F;
-          const __nv_bfloat16* g = p.up + (there ? src[i] * p.up_ld + col : 0);
+          const bool there = from[i] >= 0 && col < p.F;
+          const __nv_bfloat16* g = p.up + (there ? from[i] * p.up_ld + col : 0);
           const uint32_t at = dst + r * 64 + ((piece ^ ((r >> 1) & 3)) * 16);
           cp_async16(at, g, there);
           cp_async16(at + kChunkBytes, g + (there ? p.F : 0), there);
@@ -511,19 +555,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool more = iter.next(rank, &t);
       if (more) {
-        rows_of_tile(t);
-        copy(t, 0);
-        copy(t, 1);
+        rows_of_tile(t, src);
+        copy(t, src, 0);
+        copy(t, src, 1);
       }
       int done = 0;          // chunks worked on
       while (more) {
         Tile nx;
         const bool next = iter.next(rank, &nx);
+        if (next) rows_of_tile(nx, src_next);
         const int acc = seg & 1;
         const int row = t.m0 + rl;
+        const Rows4 up_rows(row < p.cap ? row * 2ll * p.F : -1), s_rows(row < p.cap ? (long long)row * p.F : -1);
         if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
         fence_after();
         const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 128;
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           float d[32];
           tmem_ld32(tc0 + c * 32, d);
@@ -531,19 +578,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_before();
             release_acc(acc);
           }
-          if (row >= n) {
+          if (row >= n) {   // (the rows behind the kept ones that are written are 0)
 #pragma unroll
             for (int i = 0; i < 32; ++i) d[i] = 0.f;
           }
           cp_async_wait<1>();
           __syncwarp();
           const uint32_t buf = slots + (done & 1) * kSlotBytes + lane * 64;
+          uint4 g4[4], u4[4], s4[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t at = buf + ((j * 16) ^ sw);
+            g4[j] = lds128(buf + ((j * 16) ^ sw));
+            u4[j] = lds128(buf + kChunkBytes + ((j * 16) ^ sw));
+          }
+          __syncwarp();     // the slot is read: the chunk after the next may come
+          ++done;
+          if (c < 2) {
+            copy(t, src, c + 2);
+          } else if (next) {
+            copy(nx, src_next, c - 2);
+          } else {
+            cp_async_commit();      // (an empty group keeps the count)
+            ++ahead;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
             float g[8], u[8], s[8];
-            unpack8(lds128(at), g);
-            unpack8(lds128(at + kChunkBytes), u);
+            unpack8(g4[j], g);
+            unpack8(u4[j], u);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float a, da;
@@ -552,41 +614,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               g[i] = d[8 * j + i] * u[i] * da;
               u[i] = d[8 * j + i] * a;
             }
-            sts128(at, pack8(g));
-            sts128(at + kChunkBytes, pack8(u));
-            sts128(at + 2 * kChunkBytes, pack8(s));
+            g4[j] = pack8(g);
+            u4[j] = pack8(u);
+            s4[j] = pack8(s);
           }
-          fence_async_smem();
-          __syncwarp();
-          const int col = t.n0 * kBN + half * 128 + c * 32, r0 = t.m0 + q * 32;
-          if (lane == 0) {
-            if (col < p.F && r0 < (int)p.p[0].M) {   // (p[0].M: rows of the outputs' buffers)
-              const uint32_t b = slots + (done & 1) * kSlotBytes;
-              tma_store_2d(&maps.m[2], b, col, r0);
-              tma_store_2d(&maps.m[3], b + kChunkBytes, col, r0);
-              tma_store_2d(&maps.m[4], b + 2 * kChunkBytes, col, r0);
-            }
-            bulk_commit();
-            bulk_wait_read_all();   // the slot is read out before the copies below fill it again
-          }
-          __syncwarp();
-          ++done;
-          if (c < 2) {
-            copy(t, c + 2);
-          } else if (next) {
-            if (c == 2) rows_of_tile(nx);
-            copy(nx, c - 2);
-          } else {
-            cp_async_commit();      // (an empty group keeps the count)
-            ++ahead;
-          }
+          const int col = t.n0 * kBN + half * 128 + c * 32;
+          store_bf16x32(p.dgu, up_rows, col, p.F, g4);
+          store_bf16x32(p.dgu + p.F, up_rows, col, p.F, u4);
+          store_bf16x32(p.s, s_rows, col, p.F, s4);
         }
         t = nx;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) src[i] = src_next[i];
         more = next;
         ++seg;
       }
       cp_async_wait<0>();
-      if (lane == 0) bulk_wait_all();
     } else {
       while (iter.next(rank, &t)) {
         const FfnProduct& pr = p.p[t.p];
@@ -605,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_zero = !row_ok && pr.zero_pad && row < padded_rows(M, pr.c_rows);
         if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
         fence_after();
+        const Rows4 rows(row_ok || row_zero ? out_row * pr.ldc : -1);
         const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 128;
         const int col0 = t.n0 * kBN + half * 128;
         if (t.whole) {
@@ -620,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0.f;
             }
-            if (row_ok || row_zero) store32(pr, out_row, col0 + c, v);
+            store32(pr, rows, col0 + c, v);
           }
         } else {
           // part of a tile: park it, and finish the tile if this pair is the last
@@ -640,52 +684,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int at = 2 * w + (begin[w] >= x0 && begin[w] < x1 ? 0 : 1);
             return p.partial + ((long long)at * 2 + rank) * (kBM * kBN);
           };
-          float* own = slot_of(wid);
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            float v[32];
-            tmem_ld32(tc0 + c, v);
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              __stcg(reinterpret_cast<float4*>(own + ((long long)((half * 128 + c + i) >> 2) * kBM + rl) * 4),
-                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
-          }
-          fence_before();
-          release_acc(acc);
-          __threadfence();
-          named_bar(1, 32 * kEpiWarps);
+          int* ctr = p.counters + ((long long)(t.t - sc.dp) * 2 + rank) * 2;   // pairs that came, parts parked
           if (threadIdx.x == 64) {
             int parts = 0;
             for (int w = c_first; w <= c_last; ++w) parts += begin[w] < begin[w + 1];
-            int* ctr = p.counters + (long long)(t.t - sc.dp) * 2 + rank;
-            const int last = atomicAdd(ctr, 1) == parts - 1;
-            if (last) *ctr = 0;
-            *last_flag = last;
+            *last_flag = atomicAdd(ctr, 1) == parts - 1 ? parts : 0;
           }
           named_bar(1, 32 * kEpiWarps);
-          if (*last_flag && (row_ok || row_zero)) {
+          const int parts = *last_flag;
+          const bool live = row_ok || row_zero;   // (rows behind the last are not parked)
+          if (!parts) {
+            float* own = slot_of(wid);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              float v[32];
+              tmem_ld32(tc0 + c, v);
+              if (!live) continue;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                __stcg(reinterpret_cast<float4*>(own + ((long long)((half * 128 + c + i) >> 2) * kBM + rl) * 4),
+                       make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+            }
+            fence_before();
+            release_acc(acc);
+            __threadfence();
+            named_bar(1, 32 * kEpiWarps);
+            if (threadIdx.x == 64) atomicAdd(ctr + 1, 1);
+          } else {
+            // the others have come, so they are at work on their parking: they
+            // wait for nobody, whichever kernels hold the other SMs
+            if (threadIdx.x == 64) {
+              wait_turn(ctr + 1, parts - 1, p.st, 6);
+              ctr[0] = 0;
+              ctr[1] = 0;
+            }
+            named_bar(1, 32 * kEpiWarps);
             __threadfence();
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
               float v[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0.f;
-              for (int w = c_first; w <= c_last; ++w) {
+#pragma unroll 1
+              for (int w = c_first; w <= c_last; ++w) {   // in the order of the pairs, this one's part from its accumulator
                 if (begin[w] == begin[w + 1]) continue;
-                const float* from = slot_of(w);
+                float x[32];
+                if (w == wid) {
+                  tmem_ld32(tc0 + c, x);
+                } else if (live) {
+                  const float* from = slot_of(w) + ((long long)((half * 128 + c) >> 2) * kBM + rl) * 4;
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 x =
-                      __ldcg(reinterpret_cast<const float4*>(from + ((long long)((half * 128 + c + i) >> 2) * kBM + rl) * 4));
-                  v[i] += x.x; v[i + 1] += x.y; v[i + 2] += x.z; v[i + 3] += x.w;
+                  for (int i = 0; i < 8; ++i) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(from + i * kBM * 4));
+                    x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) x[i] = 0.f;
                 }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += x[i];
               }
               if (row_zero) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
               }
-              store32(pr, out_row, col0 + c, v);
+              store32(pr, rows, col0 + c, v);
             }
+            fence_before();
+            release_acc(acc);
           }
           named_bar(1, 32 * kEpiWarps);   // last_flag is reused by the next piece
         }
@@ -705,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // host side
 template <int EPI, int ACT>
-cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, const Params& p, long long tiles, long long m, long long n,
+cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, long long tiles, long long m, long long n,
                    long long k, int dyn) {
   auto kern = ffn_kernel<EPI, ACT>;
   constexpr size_t smem = Cfg<EPI>::kSmem;
@@ -740,6 +807,8 @@ cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, const Param
   }
   // (a group's tail may go to every pair)
   const int grid = 2 * (EPI == kGroup ? pairs : (int)std::max(1ll, std::min<long long>(tiles, pairs)));
+  p.by_pairs = (uint32_t)(((1ull << 32) + grid / 2 - 1) / (grid / 2));
+  if (grid < 4) p.partial = nullptr;   // (nobody to share with; 2^32 / 1 does not fit)
   prof_begin(c, name, m, n, k, dyn);
   e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(grid), dim3(kThreads), smem, 2, maps, p);
   prof_end(c);
@@ -757,7 +826,7 @@ bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, lo
 }  // namespace
 
 size_t ffn_partial_floats() { return (size_t)2 * kMaxWorkers * 2 * kBM * kBN; }
-int ffn_counters() { return 2 * kMaxTail; }
+int ffn_counters() { return 4 * kMaxTail; }
 
 cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
   Maps maps{};
@@ -775,16 +844,13 @@ cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
 
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a) {
   Maps maps{};
-  bool ok = k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld) && k_major(&maps.m[1], a.w_down, a.D, a.F, a.D);
-  // each half of [dg | du] has a map of its own: a store stops at its last column
-  ok = ok && make_store_map(&maps.m[2], a.dgu, a.F, a.cap, 2ll * a.F) && make_store_map(&maps.m[3], a.dgu + a.F, a.F, a.cap, 2ll * a.F) &&
-       make_store_map(&maps.m[4], a.s, a.F, a.cap, a.F);
+  const bool ok = k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld) && k_major(&maps.m[1], a.w_down, a.D, a.F, a.D);
   if (!ok) return cudaErrorInvalidValue;
   Params p{};
   p.M = a.M; p.F = a.F; p.kb = (a.D + kBK - 1) / kBK;
   p.n_kept = a.n_kept; p.idx = a.up_full ? a.idx : nullptr;
   p.up = const_cast<__nv_bfloat16*>(a.up); p.up_ld = a.up_ld;
-  p.p[0].M = (int)a.cap;
+  p.dgu = a.dgu; p.s = a.s; p.cap = a.cap;
   p.zero = a.counters; p.n_zero = ffn_counters();
   p.st = c.st;
   const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 255) / 256);

@@ -640,9 +640,8 @@ cudaError_t launch_variant(const Ctx& c, const TcGemm& g, const CUtensorMap& ma,
 
 }  // namespace
 
-namespace {
-bool encode_map(CUtensorMap* m, const void* base, bool f32, long long inner, long long rows, long long ld, int box_inner,
-                int box_rows, CUtensorMapSwizzle swizzle) {
+bool make_tensor_map(CUtensorMap* m, const void* base, bool f32, long long inner, long long rows, long long ld,
+                     int box_inner, int box_rows) {
   auto enc = get_encode();
   if (!enc) return false;
   const int esz = f32 ? 4 : 2;
@@ -652,8 +651,8 @@ bool encode_map(CUtensorMap* m, const void* base, bool f32, long long inner, lon
   cuuint32_t estr[2] = {1u, 1u};
   auto encode = [&] {
     return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult r = encode();
   if (r != CUDA_SUCCESS) {
@@ -663,16 +662,6 @@ bool encode_map(CUtensorMap* m, const void* base, bool f32, long long inner, lon
     if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
   }
   return r == CUDA_SUCCESS;
-}
-}  // namespace
-
-bool make_tensor_map(CUtensorMap* m, const void* base, bool f32, long long inner, long long rows, long long ld,
-                     int box_inner, int box_rows) {
-  return encode_map(m, base, f32, inner, rows, ld, box_inner, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-bool make_store_map(CUtensorMap* m, const void* base, long long inner, long long rows, long long ld) {
-  return encode_map(m, base, false, inner, rows, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool tc_gemm_supported(const TcGemm& g) {

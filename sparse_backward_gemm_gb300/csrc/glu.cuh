@@ -11,11 +11,23 @@ constexpr int kGluSilu = 0, kGluGeluTanh = 1;
 // GELU (tanh form): with z = c (g + k g^3), (1 + tanh z) / 2 = sigmoid(2 z) = p,
 // so a(g) = g p and a' = p + 2 g p (1 - p) c (1 + 3 k g^2): one exponential and
 // one reciprocal either way, and no cancellation for g far below 0.
+// The exponential and the reciprocal are the hardware's (about 2^-22 of the
+// value each): every result is rounded to bf16.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 template <int ACT>
 __device__ __forceinline__ float glu_gate(float g) {
-  constexpr float c2 = 2.f * 0.7978845608028654f, k = 0.044715f;
-  const float z = ACT == kGluSilu ? g : c2 * g * fmaf(k * g, g, 1.f);
-  return __frcp_rn(1.f + __expf(-z));
+  constexpr float log2e = 1.4426950408889634f, c2 = 2.f * 0.7978845608028654f, k = 0.044715f;
+  const float z = ACT == kGluSilu ? -log2e * g : (-log2e * c2) * g * fmaf(k * g, g, 1.f);
+  return rcp_approx(1.f + ex2_approx(z));
 }
 template <int ACT>
 __device__ __forceinline__ float glu_act(float g) {

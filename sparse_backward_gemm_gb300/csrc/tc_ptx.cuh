@@ -323,7 +323,5 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols) {
 // size = 128 bytes (64 bf16 or 32 f32), 128-byte swizzle, zero fill.
 bool make_tensor_map(CUtensorMap* m, const void* base, bool f32, long long inner, long long rows, long long ld,
                      int box_inner, int box_rows);
-// The same for stores of 32 x 32 bf16 tiles: rows of 64 bytes, 64-byte swizzle.
-bool make_store_map(CUtensorMap* m, const void* base, long long inner, long long rows, long long ld);
 
 }  // namespace collider
