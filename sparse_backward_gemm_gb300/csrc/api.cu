@@ -2024,6 +2024,15 @@ extern "C" collider_status collider_ffn_fwd(const collider_ffn_desc* d, const vo
   Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
   FfnFwdBufs b;
   ffn_fwd_carve(cv, d, &b);
+  if (M <= kFfnFew) {
+    FfnFew f{};
+    f.act = d->act; f.M = M; f.D = D; f.F = F;
+    f.x = x; f.x_ld = ld.x; f.w_up = w_up; f.w_down = w_down;
+    f.up = static_cast<__nv_bfloat16*>(up); f.up_ld = ld.up; f.s = b.s;
+    f.y = static_cast<__nv_bfloat16*>(y); f.y_ld = ld.y;
+    CK(launch_ffn_few(c, f));
+    return COLLIDER_OK;
+  }
   FfnUp u{};
   u.act = d->act; u.M = M; u.D = D; u.F = F;
   u.x = x; u.x_ld = ld.x; u.w_up = w_up;

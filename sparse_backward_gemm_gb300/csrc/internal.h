@@ -455,6 +455,17 @@ struct FfnDs {
   int* counters;
 };
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a);
+// up (may be null), s and y of M <= kFfnFew tokens (ffn_few.cu)
+constexpr int kFfnFew = 64;
+struct FfnFew {
+  int act, M, D, F;
+  const void* x; long long x_ld;
+  const void *w_up, *w_down;
+  __nv_bfloat16* up; long long up_ld;
+  __nv_bfloat16* s;   // [M, F]
+  __nv_bfloat16* y; long long y_ld;
+};
+cudaError_t launch_ffn_few(const Ctx& c, const FfnFew& a);
 // C[m, n] = sum_k A(m, k) B(n, k), operands stored as TcGemm's.  dyn 1: M, 2: K
 // is limited by *n_kept.  C bf16 or f32; scatter: row m goes to row idx[m] (kept
 // below c_rows); zero_pad: rows up to the next multiple of 128 (below c_rows) are 0.
