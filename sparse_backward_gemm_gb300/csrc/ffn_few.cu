@@ -23,13 +23,18 @@ constexpr uint32_t kWBytes = 128 * 64 * 2;   // a 64-deep slice of the weights' 
 constexpr int kFewRows = 128;
 
 struct FewParams {
-  int M, N, kb;        // tokens; columns of the output (up: F); k-slices in all
-  int phase;           // 0: [g | u] and s, 1: y
+  int M, N, kb;        // tokens; columns of the output (kUp: F); k-slices in all
   __nv_bfloat16 *up, *out;   // up: null, or [M, 2F]; out: s or y
   long long up_ld, out_ld;
   DevStatus* st;
 };
 
+constexpr int kUp = 0, kDown = 1;   // the first product with the activation, the second
+
+// The second product's ring fits beside one of the first's in an SM: while the
+// first runs, it fills with weights.  (A deeper one, 8 slices beside 4: one of
+// its clusters finds no 8 SMs with room until the others are gone, 28 us
+// instead of 23 at 1 token x 2048 x 5632.)
 template <int NT>
 struct FewCfg {
   static constexpr uint32_t kXBytes = NT * 128, kStage = kWBytes + kXBytes;
@@ -37,7 +42,7 @@ struct FewCfg {
   static constexpr size_t kSmem = 1024 + kStages * kStage + 128;
 };
 
-template <int NT, int ACT>
+template <int NT, int PHASE, int ACT>
 __global__ void __launch_bounds__(kFewThreads)
     ffn_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, FewParams p) {
   using C = FewCfg<NT>;
@@ -67,9 +72,9 @@ __global__ void __launch_bounds__(kFewThreads)
   fence_after();
   // The second product's CTAs may come while the first's are still at work (all
   // of those have started) and fill their rings with weights.
-  if (p.phase == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (PHASE == kUp) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
-  const int parts = gridDim.x, part = blockIdx.x, col0 = blockIdx.y * (p.phase == 0 ? 64 : 128);
+  const int parts = gridDim.x, part = blockIdx.x, col0 = blockIdx.y * (PHASE == kUp ? 64 : 128);
   const int k0 = (int)((long long)part * p.kb / parts), k1 = (int)((long long)(part + 1) * p.kb / parts);
   if (warp == 0) {
     const bool leader = elect_one();
@@ -77,7 +82,7 @@ __global__ void __launch_bounds__(kFewThreads)
       const uint32_t sa = smem_u32(smem + stage * C::kStage), fb = full0 + 8 * stage;
       mbar_expect_tx(fb, C::kStage);
       tma_load_2d(sa, &mw, fb, col0, kb * 64);
-      tma_load_2d(sa + 8192, &mw, fb, p.phase == 0 ? p.N + col0 : col0 + 64, kb * 64);
+      tma_load_2d(sa + 8192, &mw, fb, PHASE == kUp ? p.N + col0 : col0 + 64, kb * 64);
     };
     auto tokens = [&](int kb, int stage) {
       tma_load_2d(smem_u32(smem + stage * C::kStage) + kWBytes, &mx, full0 + 8 * stage, kb * 64, 0);
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kFewThreads)
         a.x += x.x; a.y += x.y; b.x += y.x; b.y += y.y;
       }
       const int col = col0 + 2 * lane;
-      if (p.phase == 0) {
+      if (PHASE == kUp) {
         if (col >= p.N) continue;
         if (p.up) {
           __nv_bfloat16* o = p.up + t * p.up_ld + col;
@@ -193,10 +198,10 @@ int few_parts(int blocks, int kb, int num_sms) {
   return parts;
 }
 
-template <int NT, int ACT>
-cudaError_t launch_few(const Ctx& c, const char* name, bool pdl, const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p,
-                       int blocks) {
-  auto k = ffn_few_kernel<NT, ACT>;
+template <int NT, int PHASE, int ACT>
+cudaError_t launch_few(const Ctx& c, const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p) {
+  auto k = ffn_few_kernel<NT, PHASE, ACT>;
+  constexpr size_t smem = FewCfg<NT>::kSmem;
   static std::mutex mu;
   static bool known[64] = {false};
   int dev = 0;
@@ -205,25 +210,25 @@ cudaError_t launch_few(const Ctx& c, const char* name, bool pdl, const CUtensorM
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 64 || !known[dev]) {
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(FewCfg<NT>::kSmem));
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) known[dev] = true;
     }
   }
+  const int blocks = PHASE == kUp ? (p.N + 63) / 64 : (p.N + 127) / 128;
   const int parts = few_parts(blocks, p.kb, c.num_sms);
-  prof_begin(c, name, p.M, p.phase == 0 ? 2ll * p.N : p.N, p.kb * 64, 0);
-  e = launch_k(c, pdl && pdl_allowed(), k, dim3(parts, blocks), dim3(kFewThreads), FewCfg<NT>::kSmem, parts, mx, mw, p);
+  prof_begin(c, PHASE == kUp ? "ffn_few_up" : "ffn_few_down", p.M, PHASE == kUp ? 2ll * p.N : p.N, p.kb * 64, 0);
+  e = launch_k(c, PHASE == kDown && pdl_allowed(), k, dim3(parts, blocks), dim3(kFewThreads), smem, parts, mx, mw, p);
   prof_end(c);
   count_launch();
   return launched(e);
 }
 
-template <int ACT>
-cudaError_t launch_few_any(const Ctx& c, const char* name, bool pdl, const CUtensorMap& mx, const CUtensorMap& mw,
-                           const FewParams& p, int blocks) {
-  if (p.M <= 16) return launch_few<16, ACT>(c, name, pdl, mx, mw, p, blocks);
-  if (p.M <= 32) return launch_few<32, ACT>(c, name, pdl, mx, mw, p, blocks);
-  return launch_few<64, ACT>(c, name, pdl, mx, mw, p, blocks);
+template <int PHASE, int ACT>
+cudaError_t launch_few_any(const Ctx& c, const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p) {
+  if (p.M <= 16) return launch_few<16, PHASE, ACT>(c, mx, mw, p);
+  if (p.M <= 32) return launch_few<32, PHASE, ACT>(c, mx, mw, p);
+  return launch_few<64, PHASE, ACT>(c, mx, mw, p);
 }
 
 }  // namespace
@@ -235,12 +240,11 @@ cudaError_t launch_ffn_few(const Ctx& c, const FfnFew& a) {
       !make_tensor_map(&mw, a.w_up, false, 2ll * a.F, a.D, 2ll * a.F, 64, 64) ||
       !make_tensor_map(&ms, a.s, false, a.F, a.M, a.F, 64, nt) || !make_tensor_map(&md, a.w_down, false, a.D, a.F, a.D, 64, 64))
     return cudaErrorInvalidValue;
-  FewParams p{a.M, a.F, (a.D + 63) / 64, 0, a.up, a.s, a.up_ld, a.F, c.st};
-  cudaError_t e = a.act == kGluSilu ? launch_few_any<kGluSilu>(c, "ffn_few_up", false, mx, mw, p, (a.F + 63) / 64)
-                                    : launch_few_any<kGluGeluTanh>(c, "ffn_few_up", false, mx, mw, p, (a.F + 63) / 64);
+  FewParams p{a.M, a.F, (a.D + 63) / 64, a.up, a.s, a.up_ld, a.F, c.st};
+  cudaError_t e = a.act == kGluSilu ? launch_few_any<kUp, kGluSilu>(c, mx, mw, p) : launch_few_any<kUp, kGluGeluTanh>(c, mx, mw, p);
   if (e != cudaSuccess) return e;
-  p = FewParams{a.M, a.D, (a.F + 63) / 64, 1, nullptr, a.y, 0, a.y_ld, c.st};
-  return launch_few_any<kGluSilu>(c, "ffn_few_down", true, ms, md, p, (a.D + 127) / 128);
+  p = FewParams{a.M, a.D, (a.F + 63) / 64, nullptr, a.y, 0, a.y_ld, c.st};
+  return launch_few_any<kDown, kGluSilu>(c, ms, md, p);
 }
 
 }  // namespace collider

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- epilogue (warps 2..9) ----------------
-    auto release_acc = [&](int acc) { mbar_arrive_cluster(map_to_rank(tempty0 + 8 * acc, 0)); };
+    auto release_acc = [&](int acc) { mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8 * acc, 0)); };
     volatile int no_abort = 0;   // (timeout-only waits: the threads leave together)
     const int q = warp & 3;      // TMEM lane quadrant this warp may access
     const int half = (warp - 2) >> 2;
@@ -520,50 +520,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t slots = smem_u32(epi) + (warp - 2) * 2 * kSlotBytes;
       const uint32_t sw = ((lane >> 1) & 3) * 16;             // of this thread's row
       const int prow = lane >> 2, piece = lane & 3;           // the copies' rows: prow + 8 i
-      int ahead = 0;         // copies begun in all (slot = ahead & 1)
-      // rows of `up` that a tile's copies read (row prow + 8 i of the warp's 32), -1: none
-      int src[4], src_next[4];
-      auto rows_of_tile = [&](const Tile& x, int* to) {
+      // The copies run ahead by an iterator of their own: tile, chunk in it, and
+      // the rows of `up` of the tile (row prow + 8 i of the warp's 32).
+      constexpr int kNoRow = INT32_MIN;
+      Iter ahead(sc);
+      Tile ct;
+      bool copying;
+      int chunk = 0, slot = 0;
+      int src[4];
+      auto next_rows = [&] {
+        copying = ahead.next(rank, &ct);
+        chunk = 0;
+        if (!copying) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = x.m0 + q * 32 + prow + 8 * i;
-          int s = r < n ? r : -1;
-          if (s >= 0 && p.idx) {
-            s = p.idx[r];
-            if ((unsigned)s >= (unsigned)p.M) {
-              report_error(p.st, kErrBadIndex, 702);
-              s = -1;
-            }
+          const int r = ct.m0 + q * 32 + prow + 8 * i;
+          src[i] = r < n ? p.idx ? p.idx[r] : r : kNoRow;
+        }
+      };
+      auto copy = [&] {
+        if (copying) {
+          const uint32_t dst = slots + slot * kSlotBytes;
+          const int col = ct.n0 * kBN + half * 128 + chunk * 32 + piece * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = prow + 8 * i;
+            const bool there = (unsigned)src[i] < (unsigned)p.M && col < p.F;
+            if (chunk == 0 && !there && src[i] != kNoRow && col < p.F) report_error(p.st, kErrBadIndex, 702);
+            const __nv_bfloat16* g = p.up + (there ? src[i] * p.up_ld + col : 0);
+            const uint32_t at = dst + r * 64 + ((piece ^ ((r >> 1) & 3)) * 16);
+            cp_async16(at, g, there);
+            cp_async16(at + kChunkBytes, g + (there ? p.F : 0), there);
           }
-          to[i] = s;
+          if (++chunk == 4) next_rows();
         }
+        cp_async_commit();      // (an empty group keeps the count)
+        slot ^= 1;
       };
-      auto copy = [&](const Tile& x, const int* from, int c) {
-        const uint32_t dst = slots + (ahead & 1) * kSlotBytes;
-        const int col = x.n0 * kBN + half * 128 + c * 32 + piece * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = prow + 8 * i;
-          const bool there = from[i] >= 0 && col < p.F;
-          const __nv_bfloat16* g = p.up + (there ? from[i] * p.up_ld + col : 0);
-          const uint32_t at = dst + r * 64 + ((piece ^ ((r >> 1) & 3)) * 16);
-          cp_async16(at, g, there);
-          cp_async16(at + kChunkBytes, g + (there ? p.F : 0), there);
-        }
-        cp_async_commit();
-        ++ahead;
-      };
-      bool more = iter.next(rank, &t);
-      if (more) {
-        rows_of_tile(t, src);
-        copy(t, src, 0);
-        copy(t, src, 1);
-      }
+      next_rows();
+      copy();
+      copy();
       int done = 0;          // chunks worked on
-      while (more) {
-        Tile nx;
-        const bool next = iter.next(rank, &nx);
-        if (next) rows_of_tile(nx, src_next);
+      while (iter.next(rank, &t)) {
         const int acc = seg & 1;
         const int row = t.m0 + rl;
         const Rows4 up_rows(row < p.cap ? row * 2ll * p.F : -1), s_rows(row < p.cap ? (long long)row * p.F : -1);
@@ -593,14 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();     // the slot is read: the chunk after the next may come
           ++done;
-          if (c < 2) {
-            copy(t, src, c + 2);
-          } else if (next) {
-            copy(nx, src_next, c - 2);
-          } else {
-            cp_async_commit();      // (an empty group keeps the count)
-            ++ahead;
-          }
+          copy();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float g[8], u[8], s[8];
@@ -623,10 +614,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_bf16x32(p.dgu + p.F, up_rows, col, p.F, u4);
           store_bf16x32(p.s, s_rows, col, p.F, s4);
         }
-        t = nx;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) src[i] = src_next[i];
-        more = next;
         ++seg;
       }
       cp_async_wait<0>();
