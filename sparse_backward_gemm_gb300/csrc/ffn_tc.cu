@@ -25,19 +25,23 @@ namespace {
 using namespace tc;
 
 constexpr int kUp = 0, kDs = 1, kGroup = 2;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;   // warp 0 TMA, warp 1 MMA and TMEM, warps 2-9 epilogue
+// warp 0: TMA; warp 1: MMA and TMEM; the others: epilogue.  kDs's has long
+// chains (copy, accumulator, activation, three stores), which twice the warps
+// hide better.
+constexpr int epi_warps(int epi) { return epi == kDs ? 16 : 8; }
 constexpr int kBM = 128, kBN = 256, kBK = 64;   // a CTA's rows, the pair's columns, a k-slice
 constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + 128 * kBK * 2;
 constexpr int kGroupRows = 16;    // 256-row units that follow each other down a column of tiles
 constexpr int kMaxWorkers = 80;   // CTA pairs of a launch, at most
 constexpr int kMaxTail = 1024;    // tiles of the part that is cut
-// kDs: an epilogue warp's 32 x 32 values of g and u, twice
-constexpr uint32_t kChunkBytes = 32 * 64, kSlotBytes = 2 * kChunkBytes;
+// kDs: an epilogue warp's 32 x 16 values of g and u, twice
+constexpr int kDsCols = 16;
+constexpr uint32_t kChunkBytes = 32 * kDsCols * 2, kSlotBytes = 2 * kChunkBytes;
 template <int EPI>
 struct Cfg {
+  static constexpr int kWarps = epi_warps(EPI), kThreads = 64 + 32 * kWarps;
   static constexpr int kStages = EPI == kDs ? 5 : 7;
-  static constexpr uint32_t kEpiBytes = EPI == kDs ? kEpiWarps * 2 * kSlotBytes : 0;
+  static constexpr uint32_t kEpiBytes = EPI == kDs ? kWarps * 2 * kSlotBytes : 0;
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 256 + (EPI == kGroup ? 4 * (kMaxWorkers + 1) + 64 : 0);
 };
 
@@ -136,29 +140,29 @@ struct Iter {
   }
 };
 
+// Exchanges between lanes `st` apart: of each pair (a in the lower lane, b in
+// the upper) the lower lane's b and the upper lane's a change places.
+__device__ __forceinline__ void swap_lanes(uint4& a, uint4& b, int st) {
+  const bool hi = (threadIdx.x & st) != 0;
+  uint4 s = hi ? a : b;
+  s.x = __shfl_xor_sync(0xffffffffu, s.x, st);
+  s.y = __shfl_xor_sync(0xffffffffu, s.y, st);
+  s.z = __shfl_xor_sync(0xffffffffu, s.z, st);
+  s.w = __shfl_xor_sync(0xffffffffu, s.w, st);
+  if (hi) a = s; else b = s;
+}
 // Four 16-byte pieces of each lane's row become one piece of each of four rows:
 // piece (lane & 3) of rows (lane & ~3) + i, so that four lanes store 64 bytes of
 // one row together (a lane that stores pieces of its own row alone touches 32
 // lines with every instruction, four times the L1 cycles).
 __device__ __forceinline__ void transpose4(uint4* v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int st = 1; st <= 2; st <<= 1) {
-    const bool hi = (lane & st) != 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j & st) continue;
-      uint4& a = v[j];
-      uint4& b = v[j + st];
-      uint4 s = hi ? a : b;
-      s.x = __shfl_xor_sync(0xffffffffu, s.x, st);
-      s.y = __shfl_xor_sync(0xffffffffu, s.y, st);
-      s.z = __shfl_xor_sync(0xffffffffu, s.z, st);
-      s.w = __shfl_xor_sync(0xffffffffu, s.w, st);
-      if (hi) a = s; else b = s;
-    }
-  }
+  swap_lanes(v[0], v[1], 1);
+  swap_lanes(v[2], v[3], 1);
+  swap_lanes(v[0], v[2], 2);
+  swap_lanes(v[1], v[3], 2);
 }
+// two pieces likewise: piece (lane & 1) of rows (lane & ~1) + i
+__device__ __forceinline__ void transpose2(uint4* v) { swap_lanes(v[0], v[1], 1); }
 // The rows that this lane stores to, as offsets (elements), -1: none; of the
 // lane's own row `off`, by the whole warp.
 struct Rows4 {
@@ -218,9 +222,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 template <int EPI, int ACT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-  constexpr int S = Cfg<EPI>::kStages;
+  constexpr int S = Cfg<EPI>::kStages, kEpiWarps = Cfg<EPI>::kWarps, kThreads = Cfg<EPI>::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* epi = smem + S * kStageBytes;
@@ -470,11 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---------------- epilogue (warps 2..9) ----------------
+    // ---------------- epilogue (warps 2...) ----------------
     auto release_acc = [&](int acc) { mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8 * acc, 0)); };
     volatile int no_abort = 0;   // (timeout-only waits: the threads leave together)
     const int q = warp & 3;      // TMEM lane quadrant this warp may access
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - 2) >> 2;   // its share of the columns: of kUp 64 of g and of u, of kDs 64, else 128
     const int rl = q * 32 + lane;
     int seg = 0;
     Iter iter(sc);
@@ -512,43 +516,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++seg;
       }
     } else if constexpr (EPI == kDs) {
-      // A chunk is 32 rows x 32 columns of this warp.  Its g and u are copied to
-      // shared memory (16-byte pieces, their order within 64-byte rows XORed
-      // with bits of the row, so that the lanes' reads of their own rows meet
-      // no bank twice), two chunks ahead of the one in work; a tile's first two
-      // before its products are done.
+      // A chunk is 32 rows x 16 columns of this warp.  Its g and u are copied to
+      // shared memory (16-byte pieces, the two of a 32-byte row swapped in every
+      // other four rows, so that the lanes' reads of their own rows meet no bank
+      // twice), two chunks ahead of the one in work; a tile's first two before
+      // its products are done.
       const uint32_t slots = smem_u32(epi) + (warp - 2) * 2 * kSlotBytes;
-      const uint32_t sw = ((lane >> 1) & 3) * 16;             // of this thread's row
-      const int prow = lane >> 2, piece = lane & 3;           // the copies' rows: prow + 8 i
+      const uint32_t sw = ((lane >> 2) & 1) * 16;             // of this thread's row
+      const int prow = lane >> 1, piece = lane & 1;           // the copies' rows: prow + 16 i
       // The copies run ahead by an iterator of their own: tile, chunk in it, and
-      // the rows of `up` of the tile (row prow + 8 i of the warp's 32).
+      // the rows of `up` of the tile (row prow + 16 i of the warp's 32).
       constexpr int kNoRow = INT32_MIN;
       Iter ahead(sc);
       Tile ct;
       bool copying;
       int chunk = 0, slot = 0;
-      int src[4];
+      int src[2];
       auto next_rows = [&] {
         copying = ahead.next(rank, &ct);
         chunk = 0;
         if (!copying) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = ct.m0 + q * 32 + prow + 8 * i;
+        for (int i = 0; i < 2; ++i) {
+          const int r = ct.m0 + q * 32 + prow + 16 * i;
           src[i] = r < n ? p.idx ? p.idx[r] : r : kNoRow;
         }
       };
       auto copy = [&] {
         if (copying) {
           const uint32_t dst = slots + slot * kSlotBytes;
-          const int col = ct.n0 * kBN + half * 128 + chunk * 32 + piece * 8;
+          const int col = ct.n0 * kBN + half * 64 + chunk * kDsCols + piece * 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = prow + 8 * i;
+          for (int i = 0; i < 2; ++i) {
+            const int r = prow + 16 * i;
             const bool there = (unsigned)src[i] < (unsigned)p.M && col < p.F;
             if (chunk == 0 && !there && src[i] != kNoRow && col < p.F) report_error(p.st, kErrBadIndex, 702);
             const __nv_bfloat16* g = p.up + (there ? src[i] * p.up_ld + col : 0);
-            const uint32_t at = dst + r * 64 + ((piece ^ ((r >> 1) & 3)) * 16);
+            const uint32_t at = dst + r * 32 + ((piece ^ ((r >> 2) & 1)) * 16);
             cp_async16(at, g, there);
             cp_async16(at + kChunkBytes, g + (there ? p.F : 0), there);
           }
@@ -564,55 +568,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (iter.next(rank, &t)) {
         const int acc = seg & 1;
         const int row = t.m0 + rl;
-        const Rows4 up_rows(row < p.cap ? row * 2ll * p.F : -1), s_rows(row < p.cap ? (long long)row * p.F : -1);
+        // where this lane's stores go: piece (lane & 1) of rows (lane & ~1) + i
+        long long out[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = t.m0 + q * 32 + (lane & 30) + i;
+          out[i] = r < p.cap ? (long long)r * p.F : -1;
+        }
         if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
         fence_after();
-        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 128;
+        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 64;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          float d[32];
-          tmem_ld32(tc0 + c * 32, d);
-          if (c == 3) {
-            fence_before();
-            release_acc(acc);
-          }
-          if (row >= n) {   // (the rows behind the kept ones that are written are 0)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) d[i] = 0.f;
-          }
+          uint32_t d[kDsCols];
+          tmem_ld16_async(tc0 + c * kDsCols, d);
           cp_async_wait<1>();
           __syncwarp();
-          const uint32_t buf = slots + (done & 1) * kSlotBytes + lane * 64;
-          uint4 g4[4], u4[4], s4[4];
+          const uint32_t buf = slots + (done & 1) * kSlotBytes + lane * 32;
+          uint4 g4[2], u4[2], s4[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             g4[j] = lds128(buf + ((j * 16) ^ sw));
             u4[j] = lds128(buf + kChunkBytes + ((j * 16) ^ sw));
           }
           __syncwarp();     // the slot is read: the chunk after the next may come
           ++done;
           copy();
+          tmem_wait_ld();
+          if (c == 3) {
+            fence_before();
+            release_acc(acc);
+          }
+          if (row >= n) {   // (the rows behind the kept ones that are written are 0)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+            for (int i = 0; i < kDsCols; ++i) d[i] = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
             float g[8], u[8], s[8];
             unpack8(g4[j], g);
             unpack8(u4[j], u);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+              const float ds = __uint_as_float(d[8 * j + i]);
               float a, da;
               glu_both<ACT>(g[i], &a, &da);
               s[i] = a * u[i];
-              g[i] = d[8 * j + i] * u[i] * da;
-              u[i] = d[8 * j + i] * a;
+              g[i] = ds * u[i] * da;
+              u[i] = ds * a;
             }
             g4[j] = pack8(g);
             u4[j] = pack8(u);
             s4[j] = pack8(s);
           }
-          const int col = t.n0 * kBN + half * 128 + c * 32;
-          store_bf16x32(p.dgu, up_rows, col, p.F, g4);
-          store_bf16x32(p.dgu + p.F, up_rows, col, p.F, u4);
-          store_bf16x32(p.s, s_rows, col, p.F, s4);
+          transpose2(g4);
+          transpose2(u4);
+          transpose2(s4);
+          const int col = t.n0 * kBN + half * 64 + c * kDsCols + 8 * (lane & 1);
+          if (col < p.F) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (out[i] < 0) continue;
+              *reinterpret_cast<uint4*>(p.dgu + 2 * out[i] + col) = g4[i];
+              *reinterpret_cast<uint4*>(p.dgu + 2 * out[i] + p.F + col) = u4[i];
+              *reinterpret_cast<uint4*>(p.s + out[i] + col) = s4[i];
+            }
+          }
         }
         ++seg;
       }
@@ -781,7 +802,7 @@ cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, l
       attr[0].val.clusterDim.x = 2;
       attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3(2 * (c.num_sms / 2));
-      cfg.blockDim = dim3(kThreads);
+      cfg.blockDim = dim3(Cfg<EPI>::kThreads);
       cfg.dynamicSmemBytes = smem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
@@ -797,7 +818,7 @@ cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, l
   p.by_pairs = (uint32_t)(((1ull << 32) + grid / 2 - 1) / (grid / 2));
   if (grid < 4) p.partial = nullptr;   // (nobody to share with; 2^32 / 1 does not fit)
   prof_begin(c, name, m, n, k, dyn);
-  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(grid), dim3(kThreads), smem, 2, maps, p);
+  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(grid), dim3(Cfg<EPI>::kThreads), smem, 2, maps, p);
   prof_end(c);
   count_launch();
   return launched(e);
