@@ -31,6 +31,8 @@ __device__ __forceinline__ bool warp_contains(const int32_t* __restrict__ idx, i
 }
 
 __global__ void __launch_bounds__(256) ffn_prep_kernel(FfnPrep p, DevStatus* st) {
+  // (the product behind this kernel sets itself up beside its last blocks)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n = rows_of(p.n_kept, p.M);
   const int lane = threadIdx.x & 31, wpb = blockDim.x >> 5, vecs = p.D >> 3;
   const int w0 = blockIdx.x * wpb + (threadIdx.x >> 5), ws = gridDim.x * wpb;

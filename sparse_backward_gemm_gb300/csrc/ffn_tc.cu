@@ -62,7 +62,7 @@ struct Params {
   int np;
   uint32_t by_pairs;  // 2^32 / pairs, rounded up
   float* partial;     // [2 * pairs][2][kBN / 4][kBM][4] f32
-  int* counters;      // [kMaxTail][2][2], zero on entry and left zero
+  int* counters;      // [kMaxTail][2], zero on entry and left zero
   DevStatus* st;
 };
 
@@ -657,6 +657,34 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
         if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
         fence_after();
         const Rows4 rows(row_ok || row_zero ? out_row * pr.ldc : -1);
+        // a tile that is cut: its k-slices' places in the tail, the pairs that share it
+        int x0 = 0, x1 = 0, c_first = 0, c_last = 0;
+        int* ctr = nullptr;
+        if (!t.whole) {
+          auto owner = [&](int x) {
+            int lo = 0, hi = W - 1;   // the last pair whose range begins at or before x (and is not empty)
+            while (lo < hi) {
+              const int mid = (lo + hi + 1) >> 1;
+              if (begin[mid] <= x) lo = mid; else hi = mid - 1;
+            }
+            return lo;
+          };
+          x0 = sc.tail_off[t.p] + (t.t - sc.tail_first[t.p]) * sc.kb[t.p];
+          x1 = x0 + sc.kb[t.p];
+          c_first = owner(x0);
+          c_last = owner(x1 - 1);
+          // Low half: pairs that came, high half: parts parked.  The pair that
+          // comes last finishes the tile.  Whoever came has no other tile to
+          // wait for, so the last may wait for the others' parts, whichever
+          // kernels hold the other SMs.
+          ctr = p.counters + (t.t - sc.dp) * 2 + rank;
+          if (threadIdx.x == 64) {
+            int parts = 0;
+            for (int w = c_first; w <= c_last; ++w) parts += begin[w] < begin[w + 1];
+            const int old = atomicAdd(ctr, 1);
+            last_flag[0] = (old & 0xffff) == parts - 1 ? parts : 0;
+          }
+        }
         const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 128;
         const int col0 = t.n0 * kBN + half * 128;
         if (t.whole) {
@@ -675,29 +703,12 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             store32(pr, rows, col0 + c, v);
           }
         } else {
-          // part of a tile: park it, and finish the tile if this pair is the last
-          auto owner = [&](int x) {
-            int lo = 0, hi = W - 1;   // the last pair whose range begins at or before x (and is not empty)
-            while (lo < hi) {
-              const int mid = (lo + hi + 1) >> 1;
-              if (begin[mid] <= x) lo = mid; else hi = mid - 1;
-            }
-            return lo;
-          };
-          const int x0 = sc.tail_off[t.p] + (t.t - sc.tail_first[t.p]) * sc.kb[t.p], x1 = x0 + sc.kb[t.p];
-          const int c_first = owner(x0), c_last = owner(x1 - 1);
           // A pair parks at most two parts: in place 0 of the tile its range
           // begins in, in place 1 of the tile it ends in.
           auto slot_of = [&](int w) {
             const int at = 2 * w + (begin[w] >= x0 && begin[w] < x1 ? 0 : 1);
             return p.partial + ((long long)at * 2 + rank) * (kBM * kBN);
           };
-          int* ctr = p.counters + ((long long)(t.t - sc.dp) * 2 + rank) * 2;   // pairs that came, parts parked
-          if (threadIdx.x == 64) {
-            int parts = 0;
-            for (int w = c_first; w <= c_last; ++w) parts += begin[w] < begin[w + 1];
-            *last_flag = atomicAdd(ctr, 1) == parts - 1 ? parts : 0;
-          }
           named_bar(1, 32 * kEpiWarps);
           const int parts = *last_flag;
           const bool live = row_ok || row_zero;   // (rows behind the last are not parked)
@@ -717,41 +728,55 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             release_acc(acc);
             __threadfence();
             named_bar(1, 32 * kEpiWarps);
-            if (threadIdx.x == 64) atomicAdd(ctr + 1, 1);
+            if (threadIdx.x == 64) atomicAdd(ctr, 0x10000);
           } else {
-            // the others have come, so they are at work on their parking: they
-            // wait for nobody, whichever kernels hold the other SMs
             if (threadIdx.x == 64) {
-              wait_turn(ctr + 1, parts - 1, p.st, 6);
-              ctr[0] = 0;
-              ctr[1] = 0;
+              wait_turn(ctr, ((parts - 1) << 16) + parts, p.st, 6);   // (all have come: the low half stands)
+              *ctr = 0;
             }
             named_bar(1, 32 * kEpiWarps);
             __threadfence();
+            // One other part (the most usual): its next 32 columns are on their
+            // way while these are added.
+            const int other = parts == 2 ? (c_first == wid ? c_last : c_first) : -1;
+            auto load_part = [&](int w, int c, float* x) {
+              if (live) {
+                const float* from = slot_of(w) + ((long long)((half * 128 + c) >> 2) * kBM + rl) * 4;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 y = __ldcg(reinterpret_cast<const float4*>(from + i * kBM * 4));
+                  x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = 0.f;
+              }
+            };
+            float next[32];
+            if (other >= 0) load_part(other, 0, next);
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
               float v[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0.f;
-#pragma unroll 1
-              for (int w = c_first; w <= c_last; ++w) {   // in the order of the pairs, this one's part from its accumulator
-                if (begin[w] == begin[w + 1]) continue;
+              if (other >= 0) {
                 float x[32];
-                if (w == wid) {
-                  tmem_ld32(tc0 + c, x);
-                } else if (live) {
-                  const float* from = slot_of(w) + ((long long)((half * 128 + c) >> 2) * kBM + rl) * 4;
+                tmem_ld32(tc0 + c, v);
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4*>(from + i * kBM * 4));
-                    x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
-                  }
-                } else {
+                for (int i = 0; i < 32; ++i) x[i] = next[i];
+                if (c < 96) load_part(other, c + 32, next);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                for (int i = 0; i < 32; ++i) v[i] += x[i];   // (of two, either order is the same)
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+                for (int w = c_first; w <= c_last; ++w) {   // in the order of the pairs, this one's part from its accumulator
+                  if (begin[w] == begin[w + 1]) continue;
+                  float x[32];
+                  if (w == wid) tmem_ld32(tc0 + c, x);
+                  else load_part(w, c, x);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) v[i] += x[i];
                 }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += x[i];
               }
               if (row_zero) {
 #pragma unroll
@@ -834,7 +859,7 @@ bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, lo
 }  // namespace
 
 size_t ffn_partial_floats() { return (size_t)2 * kMaxWorkers * 2 * kBM * kBN; }
-int ffn_counters() { return 4 * kMaxTail; }
+int ffn_counters() { return 2 * kMaxTail; }
 
 cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
   Maps maps{};

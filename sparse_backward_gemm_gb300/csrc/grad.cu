@@ -268,6 +268,11 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
 // a partial, in global memory or in the cluster's shared memory
 __device__ __forceinline__ double load_part(const double* p) { return *static_cast<const volatile double*>(p); }
 
+// the root of a sum, in f32 (a root of an f64 is about 1 us here) where the sum is well inside f32
+__device__ __forceinline__ double root(double v) {
+  return v > 1e-30 && v < 1e30 ? (double)__fsqrt_rn((float)v) : sqrt(v);
+}
+
 // tensor k's norm (before scale) from the partials of the blocks that met it; by one warp
 template <typename Tab>
 __device__ __forceinline__ double tensor_norm(const Tab& t, int k, int blocks, int max_kind, const double* part) {
@@ -286,7 +291,7 @@ __device__ __forceinline__ double tensor_norm(const Tab& t, int k, int blocks, i
       v = max_kind ? max_nan(v, w) : v + w;
     }
   }
-  return max_kind ? v : sqrt(v);
+  return max_kind ? v : root(v);
 }
 
 // the norm of everything, from all slots; every thread of the block gets it
@@ -298,7 +303,7 @@ __device__ __forceinline__ float total_norm(const double* part, int slots, int m
   }
   v = block_reduce(v, max_kind, red);
   float* out = reinterpret_cast<float*>(red + 1);
-  if (block_thread() == 0) *out = (float)((max_kind ? v : sqrt(v)) * (double)scale);   // (by one thread: an f64 root is long)
+  if (block_thread() == 0) *out = (float)((max_kind ? v : root(v)) * (double)scale);
   block_sync();
   return *out;
 }
