@@ -257,7 +257,10 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
   cluster_sync();   // the peer's barriers exist before any copy or commit reaches them
   fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  grid_dep_wait();   // the kept count, the operands and the outputs are the kernels' ahead until here
+  // The kernel behind this one in the call may come as SMs fall free (all CTAs
+  // of this one have started) and set itself up: the kept count is none of its
+  // predecessors' in the call, the first of which was launched behind all before.
+  if (EPI != kGroup) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int rank = static_cast<int>(cluster_ctarank());
   const int W = gridDim.x >> 1, wid = blockIdx.x >> 1;
   int n = p.M;
@@ -353,9 +356,10 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
     for (int i = 1; i < 4; ++i) sc.first[i] = sc.tiles[0];
     sc.dp = sc.tiles[0];
     if (sc.units[0] == 0) sc.units[0] = 1;
-    if (p.zero && blockIdx.x == 0)
-      for (int i = threadIdx.x; i < p.n_zero; i += kThreads) p.zero[i] = 0;
   }
+  grid_dep_wait();   // the operands, the counters and the outputs are the kernels' ahead until here
+  if (EPI != kGroup && p.zero && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.n_zero; i += kThreads) p.zero[i] = 0;
 
   if (EPI == kGroup && p.n_kept && n == 0) {
     // nothing kept: sums over the kept rows are 0
