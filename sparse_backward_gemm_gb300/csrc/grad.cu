@@ -20,7 +20,7 @@ constexpr int kGradVecs = 8;             // 16-byte vectors a thread has in flig
 constexpr int kGradChunk = kGradThreads * kGradVecs;   // vectors of a chunk: 32 KB
 constexpr int kGradTable = 1024;         // tensors of a launch (24 KB of its 32 KB of parameters)
 constexpr int kGradBlocksPerSm = 4;
-constexpr size_t kGradKeep = 64 << 20;   // bytes that the norm leaves in L2 for the clipping pass
+constexpr size_t kGradKeep = 96 << 20;   // bytes that the norm leaves in L2 for the clipping pass (176 MB: 88 us, with none left 93)
 
 // A launch's tensors, by value in its parameters: no copy to the device, so a
 // captured call replays with the addresses it was captured with.
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
     grad_part_kernel(const __grid_constant__ GradTable<N> t, int keep, int max_kind, double* part) {
   __shared__ double red[kGradThreads];
   grid_dep_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (this call's second kernel sets itself up beside the last blocks)
   part_block(t, blockIdx.x, gridDim.x, keep, max_kind, part, red);
 }
 
@@ -281,9 +282,12 @@ __device__ __forceinline__ double tensor_norm(const Tab& t, int k, int blocks, i
     // the block of a chunk c: the largest b with begin(b) <= c
     const int b0 = (int)((((long long)t.first[k] + 1) * blocks - 1) / t.chunks);
     const int b1 = (int)((((long long)t.first[k + 1]) * blocks - 1) / t.chunks);
-    for (int b = b0 + (threadIdx.x & 31); b <= b1; b += 32) {
-      const double w = load_part(part + b + k);
-      v = max_kind ? max_nan(v, w) : v + w;
+    for (int b = b0 + (threadIdx.x & 31); b <= b1; b += 128) {   // (four loads in flight)
+      double w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = b + 32 * i <= b1 ? load_part(part + b + 32 * i + k) : 0.0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v = max_kind ? max_nan(v, w[i]) : v + w[i];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -297,9 +301,12 @@ __device__ __forceinline__ double tensor_norm(const Tab& t, int k, int blocks, i
 // the norm of everything, from all slots; every thread of the block gets it
 __device__ __forceinline__ float total_norm(const double* part, int slots, int max_kind, float scale, double* red) {
   double v = 0.0;
-  for (int i = block_thread(); i < slots; i += kGradThreads) {
-    const double w = load_part(part + i);
-    v = max_kind ? max_nan(v, w) : v + w;
+  for (int i = block_thread(); i < slots; i += 4 * kGradThreads) {
+    double w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = i + j * kGradThreads < slots ? load_part(part + i + j * kGradThreads) : 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v = max_kind ? max_nan(v, w[j]) : v + w[j];
   }
   v = block_reduce(v, max_kind, red);
   float* out = reinterpret_cast<float*>(red + 1);
@@ -325,8 +332,9 @@ __global__ void __launch_bounds__(kGradThreads) grad_finish_kernel(const __grid_
                                                                    int slots, float* norm, float* norms) {
   __shared__ double red[kGradThreads];
   grid_dep_wait();
+  // (the total by the last block, which has the fewest tensors' norms to do)
   if (norms) write_norms(t, blockIdx.x, gridDim.x, max_kind, scale, blocks, part, norms);
-  if (blockIdx.x == 0 && norm) {
+  if (blockIdx.x == gridDim.x - 1 && norm) {
     const float v = total_norm(all, slots, max_kind, scale, red);
     if (block_thread() == 0) *norm = v;
   }
@@ -410,8 +418,8 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
                       const double* all, int slots, float* norm, float* norms, float* coef_out) {
   __shared__ double red[kGradThreads];
   grid_dep_wait();
-  if (norms) write_norms(t, blockIdx.x, gridDim.x, max_kind, scale, gridDim.x, part, norms);
   scale_block(t, blockIdx.x, gridDim.x, max_kind, scale, max_norm, all, slots, norm, coef_out, red);
+  if (norms) write_norms(t, blockIdx.x, gridDim.x, max_kind, scale, gridDim.x, part, norms);
 }
 
 // A small set in one launch: one cluster of 16 CTAs of four blocks each, whose
