@@ -79,6 +79,7 @@ struct Params {
 // back), about 4 us or 16 k-slices; less gain than that is left alone.
 constexpr int kCutGain = 16;
 constexpr int kMinRange = 6;    // k-slices of a pair's range, at least
+constexpr int kMaxParts = 4;    // pairs to a tile of the tail, about: each part is 3 us more for whoever finishes it
 struct Sched {
   int np, W, wid;
   int units[3], tiles[3], kb[3];   // 256-row units, tiles, k-slices of each product
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       sc.tail_off[3] = off;
       if (warp == 2) {
         // a pair's range fills it up to its share; short tails go to fewer pairs
-        const int G = max(1, min(W, off / kMinRange));
+        const int G = max(1, min(min(W, off / kMinRange), kMaxParts * (total - dp)));
         int before = 0, at[kMaxWorkers / 32 + 1];
 #pragma unroll
         for (int j = 0; j <= kMaxWorkers / 32; ++j) {
