@@ -78,7 +78,7 @@ struct Params {
 //   Cutting costs a chain of memory round trips at the end (park, count, read
 // back), about 4 us or 16 k-slices; less gain than that is left alone.
 constexpr int kCutGain = 16;
-constexpr int kMinRange = 6;    // k-slices of a pair's range, at least
+constexpr int kMinRange = 12;   // k-slices of a pair's range, at least
 constexpr int kMaxParts = 4;    // pairs to a tile of the tail, about: each part is 3 us more for whoever finishes it
 struct Sched {
   int np, W, wid;
