@@ -321,7 +321,9 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       sc.tail_off[3] = off;
       if (warp == 2) {
         // a pair's range fills it up to its share; short tails go to fewer pairs
-        const int G = max(1, min(min(W, off / kMinRange), kMaxParts * (total - dp)));
+        int G = max(1, min(min(W, off / kMinRange), kMaxParts * (total - dp)));
+        // (few tiles of one length are cut into equal parts: no pair then has parts of two)
+        if (dp == 0 && 2 * total <= G && off == total * sc.kb[0]) G -= G % total;
         int before = 0, at[kMaxWorkers / 32 + 1];
 #pragma unroll
         for (int j = 0; j <= kMaxWorkers / 32; ++j) {
