@@ -46,13 +46,14 @@ constexpr uint64_t kWaitBudgetNs = 2000000000ull;  // 2 s
 // reads or writes before grid_dep_wait() returns, which happens once those
 // grids have completed and their writes are visible.  Every kernel that may
 // be launched so calls it in every CTA before it exits, so the wait reaches
-// back along the whole stream.  No kernel here lets its dependents be
-// scheduled before it exits (griddepcontrol.launch_dependents): measured on
-// the layer backward, the chain's next kernel then parked on SMs that the
-// side stream's persistent weight-gradient GEMMs were waiting for, and the
-// step was 10% slower; scheduled at exit it is 2% faster than without the
-// attribute.  For a kernel launched without the attribute the wait returns
-// at once.
+// back along the whole stream.  No kernel of the layer and stack backward lets
+// its dependents be scheduled before it exits (griddepcontrol.launch_dependents):
+// measured on the layer backward, the chain's next kernel then parked on SMs
+// that the side stream's persistent weight-gradient GEMMs were waiting for, and
+// the step was 10% slower; scheduled at exit it is 2% faster than without the
+// attribute.  The feed-forward and gradient calls run on one stream, and there
+// an early trigger lets the next kernel set itself up beside the last blocks.
+// For a kernel launched without the attribute the wait returns at once.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------

@@ -10,7 +10,14 @@
 //           y alone): their tiles form one list, whose tail is cut evenly.
 // All three are 2-SM kernels: a pair of CTAs works on a 256 x 256 tile, TMA
 // feeds a ring of 64-deep k-slices, one thread issues the MMAs into one of two
-// accumulators while eight warps empty the other.  Every wait is bounded.
+// accumulators while the epilogue's warps empty the other.  In long lists two
+// pairs form a cluster and stand side by side on a 256 x 512 tile: each of its
+// CTAs loads half of the 128 rows it shares with one of the other pair and
+// multicasts it to both.  Every wait is bounded.
+//   Measured at 8192 x 2048 x 5632, 40% filtered (4916 kept): kUp 200 us (1.89
+// PFLOP/s of bf16), y 112 us (1.69), kDs 97 us (1.17: 1.5 GB through L2 at 15
+// TB/s and 0.35 GB of DRAM), the backward's group 310 us (1.83; 1.95 until its
+// tail).
 #include <algorithm>
 #include <mutex>
 
@@ -61,8 +68,8 @@ struct Params {
   FfnProduct p[3];
   int np;
   uint32_t by_pairs;  // 2^32 / pairs, rounded up
-  float* partial;     // [2 * pairs][2][kBN / 4][kBM][4] f32
-  int* counters;      // [kMaxTail][2], zero on entry and left zero
+  float* partial;     // [2 * pairs][2][kBN / 4][kBM][4] f32 (with two pairs to a cluster: [2 * clusters][4]...)
+  int* counters;      // [kMaxTail][CTAs of a cluster], zero on entry and left zero
   DevStatus* st;
 };
 
@@ -100,11 +107,14 @@ struct Tile {
   int t;
   bool whole;
 };
-__device__ __forceinline__ void place(int units, int n_tiles, int t, int rank, int* m0, int* n0) {
+// NP pairs of a cluster, which stand side by side: pair `pr` has the tile's
+// column NP n + pr
+template <int NP>
+__device__ __forceinline__ void place(int units, int n_tiles, int t, int rank, int pr, int* m0, int* n0) {
   const int per = kGroupRows * n_tiles, g = t / per, r = t % per;
   const int gm = min(kGroupRows, units - g * kGroupRows);
   *m0 = (2 * (g * kGroupRows + r % gm) + rank) * kBM;
-  *n0 = r / gm;
+  *n0 = r / gm * NP + pr;
 }
 
 // the pair's pieces of work in order
@@ -117,7 +127,8 @@ struct Iter {
       end = s.begin[s.wid + 1];
     }
   }
-  __device__ bool next(int rank, Tile* o) {
+  template <int NP>
+  __device__ bool next(int rank, int pr, Tile* o) {
     if (tile < s.dp) {
       o->t = tile;
       tile += s.W;
@@ -136,7 +147,7 @@ struct Iter {
       it += o->k1 - o->k0;
     }
     o->whole = o->k0 == 0 && o->k1 == s.kb[o->p];
-    place(s.units[o->p], s.tiles[o->p] / s.units[o->p], o->t - s.first[o->p], rank, &o->m0, &o->n0);
+    place<NP>(s.units[o->p], s.tiles[o->p] / s.units[o->p], o->t - s.first[o->p], rank, pr, &o->m0, &o->n0);
     return true;
   }
 };
@@ -222,7 +233,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-template <int EPI, int ACT>
+template <int EPI, int ACT, int NP>
 __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   constexpr int S = Cfg<EPI>::kStages, kEpiWarps = Cfg<EPI>::kWarps, kThreads = Cfg<EPI>::kThreads;
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, NP);   // (every pair's MMAs: the rows' operand goes to all of them)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
@@ -262,8 +273,9 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
   // of this one have started) and set itself up: the kept count is none of its
   // predecessors' in the call, the first of which was launched behind all before.
   if (EPI != kGroup) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int W = gridDim.x >> 1, wid = blockIdx.x >> 1;
+  const int crank = static_cast<int>(cluster_ctarank()), rank = crank & 1, pr = crank >> 1;   // in the cluster, in the pair; the pair
+  const int leader_cta = crank & ~1;
+  const int W = gridDim.x / (2 * NP), wid = blockIdx.x / (2 * NP);
   int n = p.M;
   if (p.n_kept) n = min(p.M, max(0, *p.n_kept));
 
@@ -282,7 +294,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       const FfnProduct& q = p.p[i];
       const int m = q.dyn == 1 ? min(q.M, n) : q.M, k = q.dyn == 2 ? min(q.K, n) : q.K;
       sc.units[i] = (m + 2 * kBM - 1) / (2 * kBM);
-      sc.tiles[i] = sc.units[i] * ((q.N + kBN - 1) / kBN);
+      sc.tiles[i] = sc.units[i] * ((q.N + NP * kBN - 1) / (NP * kBN));
       sc.kb[i] = (k + kBK - 1) / kBK;
       total += sc.tiles[i];
       slices += (long long)sc.tiles[i] * sc.kb[i];
@@ -353,7 +365,8 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
   } else {
     sc.np = 1;
     sc.units[0] = (n + 2 * kBM - 1) / (2 * kBM);
-    sc.tiles[0] = sc.units[0] * ((p.F + (EPI == kUp ? 127 : 255)) / (EPI == kUp ? 128 : 256));
+    constexpr int cols = NP * (EPI == kUp ? kBN / 2 : kBN);
+    sc.tiles[0] = sc.units[0] * ((p.F + cols - 1) / cols);
     sc.kb[0] = p.kb;
     sc.first[0] = 0;
     for (int i = 1; i < 4; ++i) sc.first[i] = sc.tiles[0];
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
     uint32_t phase = 0, armed = 0, armed_parity = 0;   // stages with copies issued, and the phase parity armed
     Iter iter(sc);
     Tile t;
-    while (iter.next(rank, &t) && !aborted()) {
+    while (iter.next<NP>(rank, pr, &t) && !aborted()) {
       const CUtensorMap* ma = &maps.m[EPI == kGroup ? 2 * t.p : 0];
       const CUtensorMap* mb = ma + 1;
       const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
@@ -402,8 +415,12 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
           const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
           const int kx = kb * kBK;
           if (rank == 0) mbar_expect_tx(fb, 2 * kStageBytes);   // both CTAs' copies are counted on the even CTA's barrier
-          const uint32_t lb = map_to_rank(fb, 0);
-          if (!a_mn) {
+          const uint32_t lb = map_to_rank(fb, leader_cta);
+          if (NP == 2) {
+            // the two CTAs of the cluster with these rows load a half each, for both
+            const uint16_t both = static_cast<uint16_t>(5u << rank);
+            tma_load_2d_pair_mc(sa + pr * 8192, ma, lb, both, a_mn ? t.m0 + 64 * pr : kx, a_mn ? kx : t.m0 + 64 * pr);
+          } else if (!a_mn) {
             tma_load_2d_pair(sa, ma, lb, kx, t.m0);
           } else {
             tma_load_2d_pair(sa, ma, lb, t.m0, kx);
@@ -451,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       int seg = 0;
       Iter iter(sc);
       Tile t;
-      while (iter.next(rank, &t) && !__any_sync(0xffffffffu, *abort_flag != 0)) {
+      while (iter.next<NP>(rank, pr, &t) && !__any_sync(0xffffffffu, *abort_flag != 0)) {
         const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
         const uint32_t idesc = idesc_bf16(2 * kBM, kBN, a_mn, b_mn);
         const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32, a_lbo = a_mn ? 8192 : 16, b_lbo = b_mn ? 8192 : 16;
@@ -469,20 +486,20 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             for (int kk = 0; kk < kBK / 16; ++kk)
               mma_bf16_pair(d, sdesc(sa + kk * a_step, a_lbo, 1024), sdesc(sb + kk * b_step, b_lbo, 1024), idesc,
                             (kb > t.k0) || (kk > 0));
-            mma_commit_pair_mc(empty0 + 8 * stage, 3);
+            mma_commit_pair_mc(empty0 + 8 * stage, NP == 2 ? 0xf : 3);
           }
           __syncwarp();
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        if (leader) mma_commit_pair_mc(tfull0 + 8 * acc, 3);
+        if (leader) mma_commit_pair_mc(tfull0 + 8 * acc, static_cast<uint16_t>(3u << leader_cta));
         __syncwarp();
         ++seg;
       }
     }
   } else {
     // ---------------- epilogue (warps 2...) ----------------
-    auto release_acc = [&](int acc) { mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8 * acc, 0)); };
+    auto release_acc = [&](int acc) { mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8 * acc, leader_cta)); };
     volatile int no_abort = 0;   // (timeout-only waits: the threads leave together)
     const int q = warp & 3;      // TMEM lane quadrant this warp may access
     const int half = (warp - 2) >> 2;   // its share of the columns: of kUp 64 of g and of u, of kDs 64, else 128
@@ -491,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
     Iter iter(sc);
     Tile t;
     if constexpr (EPI == kUp) {
-      while (iter.next(rank, &t)) {
+      while (iter.next<NP>(rank, pr, &t)) {
         const int acc = seg & 1;
         const int row = t.m0 + rl;
         const Rows4 up_rows(row < n ? row * p.up_ld : -1), s_rows(row < n ? (long long)row * p.F : -1);
@@ -540,7 +557,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       int chunk = 0, slot = 0;
       int src[2];
       auto next_rows = [&] {
-        copying = ahead.next(rank, &ct);
+        copying = ahead.next<NP>(rank, pr, &ct);
         chunk = 0;
         if (!copying) return;
 #pragma unroll
@@ -572,7 +589,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       copy();
       copy();
       int done = 0;          // chunks worked on
-      while (iter.next(rank, &t)) {
+      while (iter.next<NP>(rank, pr, &t)) {
         const int acc = seg & 1;
         const int row = t.m0 + rl;
         // where this lane's stores go: piece (lane & 1) of rows (lane & ~1) + i
@@ -646,7 +663,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       }
       cp_async_wait<0>();
     } else {
-      while (iter.next(rank, &t)) {
+      while (iter.next<NP>(rank, pr, &t)) {
         const FfnProduct& pr = p.p[t.p];
         const int acc = seg & 1;
         const int M = pr.dyn == 1 ? min(pr.M, n) : pr.M;
@@ -684,7 +701,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
           // comes last finishes the tile.  Whoever came has no other tile to
           // wait for, so the last may wait for the others' parts, whichever
           // kernels hold the other SMs.
-          ctr = p.counters + (t.t - sc.dp) * 2 + rank;
+          ctr = p.counters + (t.t - sc.dp) * 2 * NP + crank;
           if (threadIdx.x == 64) {
             int parts = 0;
             for (int w = c_first; w <= c_last; ++w) parts += begin[w] < begin[w + 1];
@@ -714,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
           // begins in, in place 1 of the tile it ends in.
           auto slot_of = [&](int w) {
             const int at = 2 * w + (begin[w] >= x0 && begin[w] < x1 ? 0 : 1);
-            return p.partial + ((long long)at * 2 + rank) * (kBM * kBN);
+            return p.partial + ((long long)at * 2 * NP + crank) * (kBM * kBN);
           };
           named_bar(1, 32 * kEpiWarps);
           const int parts = *last_flag;
@@ -811,53 +828,53 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // host side
-template <int EPI, int ACT>
+template <int EPI, int ACT, int NP>
 cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, long long tiles, long long m, long long n,
                    long long k, int dyn) {
-  auto kern = ffn_kernel<EPI, ACT>;
+  auto kern = ffn_kernel<EPI, ACT, NP>;
   constexpr size_t smem = Cfg<EPI>::kSmem;
   // per device, once: the shared-memory opt-in, and how many pairs run at once
   static std::mutex mu;
   static int known[64] = {0};
-  int dev = 0, pairs = 0;
+  int dev = 0, fit = 0;   // clusters
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   {
     std::lock_guard<std::mutex> lk(mu);
-    if (dev >= 0 && dev < 64) pairs = known[dev];
-    if (pairs == 0) {
+    if (dev >= 0 && dev < 64) fit = known[dev];
+    if (fit == 0) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.x = 2 * NP;
       attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(2 * (c.num_sms / 2));
+      cfg.gridDim = dim3(2 * NP * (c.num_sms / (2 * NP)));
       cfg.blockDim = dim3(Cfg<EPI>::kThreads);
       cfg.dynamicSmemBytes = smem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
       if (e != cudaSuccess) return e;
-      pairs = std::min({pairs, c.num_sms / 2, kMaxWorkers});
-      if (pairs < 1) return cudaErrorNotSupported;
-      if (dev >= 0 && dev < 64) known[dev] = pairs;
+      fit = std::min({fit, c.num_sms / (2 * NP), kMaxWorkers / NP});
+      if (fit < 1) return cudaErrorNotSupported;
+      if (dev >= 0 && dev < 64) known[dev] = fit;
     }
   }
-  // (a group's tail may go to every pair)
-  const int grid = 2 * (EPI == kGroup ? pairs : (int)std::max(1ll, std::min<long long>(tiles, pairs)));
-  p.by_pairs = (uint32_t)(((1ull << 32) + grid / 2 - 1) / (grid / 2));
-  if (grid < 4) p.partial = nullptr;   // (nobody to share with; 2^32 / 1 does not fit)
+  // (a group's tail may go to every cluster)
+  const int workers = EPI == kGroup ? fit : (int)std::max(1ll, std::min<long long>((tiles + NP - 1) / NP, fit));
+  p.by_pairs = (uint32_t)(((1ull << 32) + workers - 1) / workers);
+  if (workers < 2) p.partial = nullptr;   // (nobody to share with; 2^32 / 1 does not fit)
   prof_begin(c, name, m, n, k, dyn);
-  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(grid), dim3(Cfg<EPI>::kThreads), smem, 2, maps, p);
+  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(2 * NP * workers), dim3(Cfg<EPI>::kThreads), smem, 2 * NP, maps, p);
   prof_end(c);
   count_launch();
   return launched(e);
 }
 
-bool k_major(CUtensorMap* m, const void* p, long long inner, long long rows, long long ld) {
-  return make_tensor_map(m, p, false, inner, rows, ld, 64, 128);
+bool k_major(CUtensorMap* m, const void* p, long long inner, long long rows, long long ld, int box_rows = 128) {
+  return make_tensor_map(m, p, false, inner, rows, ld, 64, box_rows);
 }
 bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, long long ld) {
   return make_tensor_map(m, p, false, inner, rows, ld, 64, 64);
@@ -865,26 +882,38 @@ bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, lo
 
 }  // namespace
 
+// Two pairs to a cluster load the rows' operand once for both, so a quarter
+// less comes through L2: for lists of two waves of 256 x 256 tiles at least.
+// One pair and two, us: backward 2403 x 1536 x 8960 272-290 and 265-267, 1229 x
+// 2048 x 5632 139 and 136.5; in a loop of seconds, under the power limit, 8192 x
+// 2048 x 5632 forward 363 and 360, 4916 rows backward 484 and 482 (alone 427 and
+// 431).  Below, the wider tiles fill the SMs worse: 800 x 1024 x 2816 57 and 61.
+static bool side_by_side(const Ctx& c, long long pair_tiles) { return pair_tiles >= c.num_sms; }
+
 size_t ffn_partial_floats() { return (size_t)2 * kMaxWorkers * 2 * kBM * kBN; }
-int ffn_counters() { return 2 * kMaxTail; }
+int ffn_counters() { return 4 * kMaxTail; }
 
 cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
   Maps maps{};
-  if (!k_major(&maps.m[0], a.x, a.D, a.M, a.x_ld) || !mn_major(&maps.m[1], a.w_up, 2ll * a.F, a.D, 2ll * a.F))
+  const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 127) / 128);
+  const bool two = side_by_side(c, tiles);
+  if (!k_major(&maps.m[0], a.x, a.D, a.M, a.x_ld, two ? 64 : 128) || !mn_major(&maps.m[1], a.w_up, 2ll * a.F, a.D, 2ll * a.F))
     return cudaErrorInvalidValue;
   Params p{};
   p.M = a.M; p.F = a.F; p.kb = (a.D + kBK - 1) / kBK;
   p.up = a.up; p.up_ld = a.up_ld; p.s = a.s;
   p.zero = a.counters; p.n_zero = ffn_counters();
   p.st = c.st;
-  const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 127) / 128);
-  return a.act == kGluSilu ? launch<kUp, kGluSilu>(c, "ffn_up", maps, p, tiles, a.M, 2ll * a.F, a.D, 0)
-                           : launch<kUp, kGluGeluTanh>(c, "ffn_up", maps, p, tiles, a.M, 2ll * a.F, a.D, 0);
+  auto go = [&](auto k) { return k(c, "ffn_up", maps, p, tiles, a.M, 2ll * a.F, a.D, 0); };
+  if (a.act == kGluSilu) return two ? go(launch<kUp, kGluSilu, 2>) : go(launch<kUp, kGluSilu, 1>);
+  return two ? go(launch<kUp, kGluGeluTanh, 2>) : go(launch<kUp, kGluGeluTanh, 1>);
 }
 
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a) {
   Maps maps{};
-  const bool ok = k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld) && k_major(&maps.m[1], a.w_down, a.D, a.F, a.D);
+  const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 255) / 256);
+  const bool two = side_by_side(c, tiles);
+  const bool ok = k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld, two ? 64 : 128) && k_major(&maps.m[1], a.w_down, a.D, a.F, a.D);
   if (!ok) return cudaErrorInvalidValue;
   Params p{};
   p.M = a.M; p.F = a.F; p.kb = (a.D + kBK - 1) / kBK;
@@ -893,19 +922,21 @@ cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a) {
   p.dgu = a.dgu; p.s = a.s; p.cap = a.cap;
   p.zero = a.counters; p.n_zero = ffn_counters();
   p.st = c.st;
-  const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 255) / 256);
-  const int dyn = a.n_kept ? 1 : 0;
-  return a.act == kGluSilu ? launch<kDs, kGluSilu>(c, "ffn_ds", maps, p, tiles, a.M, a.F, a.D, dyn)
-                           : launch<kDs, kGluGeluTanh>(c, "ffn_ds", maps, p, tiles, a.M, a.F, a.D, dyn);
+  auto go = [&](auto k) { return k(c, "ffn_ds", maps, p, tiles, a.M, a.F, a.D, a.n_kept ? 1 : 0); };
+  if (a.act == kGluSilu) return two ? go(launch<kDs, kGluSilu, 2>) : go(launch<kDs, kGluSilu, 1>);
+  return two ? go(launch<kDs, kGluGeluTanh, 2>) : go(launch<kDs, kGluGeluTanh, 1>);
 }
 
 cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, const int32_t* idx, const int32_t* n_kept,
                              float* partial, int* counters) {
   Maps maps{};
   Params p{};
+  long long tiles = 0;
+  for (int i = 0; i < np; ++i) tiles += (long long)((q[i].M + 255) / 256) * ((q[i].N + 255) / 256);
+  const bool two = side_by_side(c, tiles);
   for (int i = 0; i < np; ++i) {
     const bool a_ok = q[i].a_mn ? mn_major(&maps.m[2 * i], q[i].A, q[i].M, q[i].a_rows, q[i].lda)
-                                : k_major(&maps.m[2 * i], q[i].A, q[i].K, q[i].a_rows, q[i].lda);
+                                : k_major(&maps.m[2 * i], q[i].A, q[i].K, q[i].a_rows, q[i].lda, two ? 64 : 128);
     const bool b_ok = q[i].b_mn ? mn_major(&maps.m[2 * i + 1], q[i].B, q[i].N, q[i].b_rows, q[i].ldb)
                                 : k_major(&maps.m[2 * i + 1], q[i].B, q[i].K, q[i].b_rows, q[i].ldb);
     if (!a_ok || !b_ok) return cudaErrorInvalidValue;
@@ -915,7 +946,8 @@ cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, c
   p.M = M; p.idx = idx; p.n_kept = n_kept;
   p.partial = partial; p.counters = counters;
   p.st = c.st;
-  return launch<kGroup, 0>(c, "ffn_group", maps, p, 0, q[0].M, q[0].N, q[0].K, q[0].dyn);
+  auto go = [&](auto k) { return k(c, "ffn_group", maps, p, tiles, q[0].M, q[0].N, q[0].K, q[0].dyn); };
+  return two ? go(launch<kGroup, 0, 2>) : go(launch<kGroup, 0, 1>);
 }
 
 }  // namespace collider
