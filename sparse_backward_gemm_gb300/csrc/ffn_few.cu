@@ -1,10 +1,13 @@
-// The gated feed-forward block's forward of a few tokens (M <= 64): its time is
+// The gated feed-forward block's forward of a few tokens (M <= 128): its time is
 // the reading of the weights, so they are the wide operand.  A tile of 128
 // output features (64 gates and the same 64 ups, or 128 columns of y) is the A
-// of 128 x N x 16 MMAs, the tokens, padded to N = 16, 32 or 64, are the B: the
+// of 128 x N x 16 MMAs, the tokens, padded to N = 16, 32, 64 or 128, are the B: the
 // weights pass by TMA from memory to the tensor core, each once, and no thread
 // touches them.  A cluster's CTAs split the reduction, so that all SMs read;
 // their parts meet through distributed shared memory, in CTA order.
+//   Measured at 2048 x 5632 (69 MB of weights; 10.3 us at the copy rate): 1 token
+// 22 us, 64 28, 128 36; as 256-row tiles 65, 56 and 44.  256 x 384, where nothing
+// but launches counts: 33 tokens 12.7 us, 100 17.0 (256-row tiles 16.4).
 #include <algorithm>
 #include <mutex>
 
@@ -38,7 +41,7 @@ constexpr int kUp = 0, kDown = 1;   // the first product with the activation, th
 template <int NT>
 struct FewCfg {
   static constexpr uint32_t kXBytes = NT * 128, kStage = kWBytes + kXBytes;
-  static constexpr int kStages = NT == 64 ? 4 : 5;
+  static constexpr int kStages = NT == 128 ? 3 : NT == 64 ? 4 : 5;
   static constexpr size_t kSmem = 1024 + kStages * kStage + 128;
 };
 
@@ -228,13 +231,14 @@ template <int PHASE, int ACT>
 cudaError_t launch_few_any(const Ctx& c, const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p) {
   if (p.M <= 16) return launch_few<16, PHASE, ACT>(c, mx, mw, p);
   if (p.M <= 32) return launch_few<32, PHASE, ACT>(c, mx, mw, p);
-  return launch_few<64, PHASE, ACT>(c, mx, mw, p);
+  if (p.M <= 64) return launch_few<64, PHASE, ACT>(c, mx, mw, p);
+  return launch_few<128, PHASE, ACT>(c, mx, mw, p);
 }
 
 }  // namespace
 
 cudaError_t launch_ffn_few(const Ctx& c, const FfnFew& a) {
-  const int nt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64;
+  const int nt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
   CUtensorMap mx, mw, ms, md;
   if (!make_tensor_map(&mx, a.x, false, a.D, a.M, a.x_ld, 64, nt) ||
       !make_tensor_map(&mw, a.w_up, false, 2ll * a.F, a.D, 2ll * a.F, 64, 64) ||

@@ -456,7 +456,7 @@ struct FfnDs {
 };
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a);
 // up (may be null), s and y of M <= kFfnFew tokens (ffn_few.cu)
-constexpr int kFfnFew = 64;
+constexpr int kFfnFew = 128;
 struct FfnFew {
   int act, M, D, F;
   const void* x; long long x_ld;
