@@ -44,11 +44,12 @@ constexpr int kMaxTail = 1024;    // tiles of the part that is cut
 // kDs: an epilogue warp's 32 x 16 values of g and u, twice
 constexpr int kDsCols = 16;
 constexpr uint32_t kChunkBytes = 32 * kDsCols * 2, kSlotBytes = 2 * kChunkBytes;
+constexpr int kSlots = 1;
 template <int EPI>
 struct Cfg {
   static constexpr int kWarps = epi_warps(EPI), kThreads = 64 + 32 * kWarps;
-  static constexpr int kStages = EPI == kDs ? 5 : 7;
-  static constexpr uint32_t kEpiBytes = EPI == kDs ? kWarps * 2 * kSlotBytes : 0;
+  static constexpr int kStages = EPI == kDs ? 6 : 7;
+  static constexpr uint32_t kEpiBytes = EPI == kDs ? kWarps * kSlots * kSlotBytes : 0;
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 256 + (EPI == kGroup ? 4 * (kMaxWorkers + 1) + 64 : 0);
 };
 
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       // other four rows, so that the lanes' reads of their own rows meet no bank
       // twice), two chunks ahead of the one in work; a tile's first two before
       // its products are done.
-      const uint32_t slots = smem_u32(epi) + (warp - 2) * 2 * kSlotBytes;
+      const uint32_t slots = smem_u32(epi) + (warp - 2) * kSlots * kSlotBytes;
       const uint32_t sw = ((lane >> 2) & 1) * 16;             // of this thread's row
       const int prow = lane >> 1, piece = lane & 1;           // the copies' rows: prow + 16 i
       // The copies run ahead by an iterator of their own: tile, chunk in it, and
@@ -583,11 +584,10 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
           if (++chunk == 4) next_rows();
         }
         cp_async_commit();      // (an empty group keeps the count)
-        slot ^= 1;
+        slot = (slot + 1) % kSlots;
       };
       next_rows();
-      copy();
-      copy();
+      for (int i = 0; i < kSlots; ++i) copy();
       int done = 0;          // chunks worked on
       while (iter.next<NP>(rank, pr, &t)) {
         const int acc = seg & 1;
@@ -606,9 +606,9 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
         for (int c = 0; c < 4; ++c) {
           uint32_t d[kDsCols];
           tmem_ld16_async(tc0 + c * kDsCols, d);
-          cp_async_wait<1>();
+          cp_async_wait<kSlots - 1>();
           __syncwarp();
-          const uint32_t buf = slots + (done & 1) * kSlotBytes + lane * 32;
+          const uint32_t buf = slots + (done % kSlots) * kSlotBytes + lane * 32;
           uint4 g4[2], u4[2], s4[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
