@@ -1970,7 +1970,8 @@ struct FfnFwdBufs {
 };
 size_t ffn_fwd_carve(Carver& cv, const collider_ffn_desc* d, FfnFwdBufs* b) {
   b->s = cv.take<__nv_bfloat16>((size_t)d->M * d->F);
-  b->partial = cv.take<float>(ffn_partial_floats());
+  if (d->M <= kFfnFew) return cv.used;   // (no tiles that are cut)
+  b->partial = cv.take<float>(ffn_partial_floats(ffn_tiles(d->M, d->D)));
   b->counters = cv.take<int>(ffn_counters());
   return cv.used;
 }
@@ -1986,7 +1987,7 @@ size_t ffn_bwd_carve(Carver& cv, const collider_ffn_desc* d, FfnBwdBufs* b) {
   b->dyk = cv.take<__nv_bfloat16>(Mp * d->D);
   b->dgu = cv.take<__nv_bfloat16>(Mp * 2 * d->F);
   b->s = cv.take<__nv_bfloat16>(Mp * d->F);
-  b->partial = cv.take<float>(ffn_partial_floats());
+  b->partial = cv.take<float>(ffn_partial_floats(ffn_tiles(d->M, d->D) + ffn_tiles(d->D, 2ll * d->F) + ffn_tiles(d->F, d->D)));
   b->counters = cv.take<int>(ffn_counters());
   return cv.used;
 }

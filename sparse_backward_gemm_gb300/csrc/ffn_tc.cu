@@ -890,12 +890,16 @@ bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, lo
 // 431).  Below, the wider tiles fill the SMs worse: 800 x 1024 x 2816 57 and 61.
 static bool side_by_side(const Ctx& c, long long pair_tiles) { return pair_tiles >= c.num_sms; }
 
-size_t ffn_partial_floats() { return (size_t)2 * kMaxWorkers * 2 * kBM * kBN; }
+size_t ffn_partial_floats(long long tiles) {
+  // two parts a pair, of 128 rows in each of its CTAs; at most about kMaxParts pairs work at a tile
+  return (size_t)(2 * std::min<long long>(kMaxWorkers, kMaxParts * tiles) * 2) * kBM * kBN;
+}
+long long ffn_tiles(long long m, long long n) { return (m + 2 * kBM - 1) / (2 * kBM) * ((n + kBN - 1) / kBN); }
 int ffn_counters() { return 4 * kMaxTail; }
 
 cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
   Maps maps{};
-  const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 127) / 128);
+  const long long tiles = ffn_tiles(a.M, 2ll * a.F);
   const bool two = side_by_side(c, tiles);
   if (!k_major(&maps.m[0], a.x, a.D, a.M, a.x_ld, two ? 64 : 128) || !mn_major(&maps.m[1], a.w_up, 2ll * a.F, a.D, 2ll * a.F))
     return cudaErrorInvalidValue;
@@ -911,7 +915,7 @@ cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
 
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a) {
   Maps maps{};
-  const long long tiles = (long long)((a.M + 255) / 256) * ((a.F + 255) / 256);
+  const long long tiles = ffn_tiles(a.M, a.F);
   const bool two = side_by_side(c, tiles);
   const bool ok = k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld, two ? 64 : 128) && k_major(&maps.m[1], a.w_down, a.D, a.F, a.D);
   if (!ok) return cudaErrorInvalidValue;
@@ -932,7 +936,7 @@ cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, c
   Maps maps{};
   Params p{};
   long long tiles = 0;
-  for (int i = 0; i < np; ++i) tiles += (long long)((q[i].M + 255) / 256) * ((q[i].N + 255) / 256);
+  for (int i = 0; i < np; ++i) tiles += ffn_tiles(q[i].M, q[i].N);
   const bool two = side_by_side(c, tiles);
   for (int i = 0; i < np; ++i) {
     const bool a_ok = q[i].a_mn ? mn_major(&maps.m[2 * i], q[i].A, q[i].M, q[i].a_rows, q[i].lda)

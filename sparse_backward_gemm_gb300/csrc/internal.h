@@ -427,8 +427,10 @@ struct FfnPrep {
 cudaError_t launch_ffn_prep(const Ctx& c, const FfnPrep& p);
 // The products (ffn_tc.cu).  counters: ffn_counters() ints that launch_ffn_up
 // and launch_ffn_ds set to 0 for a launch_ffn_group behind them in the stream;
-// partial: ffn_partial_floats() floats of scratch.
-size_t ffn_partial_floats();
+// partial: ffn_partial_floats() floats of scratch, of the group's ffn_tiles()
+// or more.
+long long ffn_tiles(long long m, long long n);
+size_t ffn_partial_floats(long long tiles);
 int ffn_counters();
 // up = bf16(x W_up) (may be null), s = bf16(act(g) u) of the f32 [g | u]
 struct FfnUp {

@@ -91,8 +91,20 @@ def desc(M, D, F, kind, grad=cl.BF16, **ld):
     return cl.FfnDesc(M=M, D=D, F=F, act=ACT[kind], grad_dtype=grad, **ld)
 
 
+GUARDS = []
+
+
 def workspace(size):
-    return torch.full((size,), 0xFF, dtype=torch.uint8, device=gu.DEV)   # NaNs, were anything read before it is written
+    """Filled with NaNs, should anything be read before it is written; the bytes behind it are looked at after the call."""
+    t = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device=gu.DEV)
+    t[size:] = 0xAB
+    GUARDS.append(t[size:])
+    return t[:size]
+
+
+def check_guards():
+    assert all(bool((g == 0xAB).all()) for g in GUARDS)
+    GUARDS.clear()
 
 
 def run_forward(v, kind, pads=(0, 0, 0), want_up=True, stream=None):
@@ -105,6 +117,7 @@ def run_forward(v, kind, pads=(0, 0, 0), want_up=True, stream=None):
     ws = workspace(cl.collider_ffn_fwd_workspace_size(d))
     cl.collider_ffn_fwd(d, x, wu, wd, ut if want_up else None, yt, ws, stream=stream)
     cl.collider_check()
+    check_guards()
     assert bool((ut[:, 2 * F:] == 7).all()) and bool((yt[:, D:] == 7).all())
     return up, y
 
@@ -186,6 +199,7 @@ def run_backward(v, kind, keep, idx, nk, saved=0, dyr=0, dxr=0, grad=cl.BF16, pa
                         saved, dy, dyr, idx, nk, dx if "x" in want else None, dxr, dwu if "u" in want else None,
                         dwd if "d" in want else None, ws, stream=stream)
     cl.collider_check()
+    check_guards()
     assert bool((dx[:, D:] == 7).all())
     if dxr == cl.ROWS_COMPACT and keep is not None and "x" in want:
         end = min(M, -(-n // 128) * 128)
@@ -303,6 +317,7 @@ def test_a_training_step():
 
     def check(v):
         cl.collider_check()
+        assert all(bool((g == 0xAB).all()) for g in GUARDS)
         o, b = forward_bounds(v, "silu")
         within(t["y"], o["y"], b["y"], "y")
         v = dict(v, up=gu.host(t["up"]))
