@@ -1964,12 +1964,12 @@ bool any_overlap(std::initializer_list<Extent> out, std::initializer_list<Extent
 }
 
 struct FfnFwdBufs {
-  __nv_bfloat16* s;    // [M, F]
+  __nv_bfloat16* s;    // [M, F], or [2 M, F]
   float* partial;
   int* counters;
 };
 size_t ffn_fwd_carve(Carver& cv, const collider_ffn_desc* d, FfnFwdBufs* b) {
-  b->s = cv.take<__nv_bfloat16>((size_t)d->M * d->F);
+  b->s = cv.take<__nv_bfloat16>((size_t)d->M * d->F * (d->M <= kFfnSplit ? 2 : 1));
   if (d->M <= kFfnFew) return cv.used;   // (no tiles that are cut)
   b->partial = cv.take<float>(ffn_partial_floats(ffn_tiles(d->M, d->D)));
   b->counters = cv.take<int>(ffn_counters());

@@ -38,6 +38,10 @@ constexpr int kUp = 0, kDown = 1;   // the first product with the activation, th
 // first runs, it fills with weights.  (A deeper one, 8 slices beside 4: one of
 // its clusters finds no 8 SMs with room until the others are gone, 28 us
 // instead of 23 at 1 token x 2048 x 5632.)
+// SPLIT (second product, M <= 64): s as the sum of two bf16 values, rows 0..M-1
+// and M..2M-1 of its buffer, N / 2 columns of the MMAs each.  The products are
+// free here, and y is then off by its own rounding alone (1.7e-3 of its norm; by
+// that of s too 2.4e-3).
 template <int NT>
 struct FewCfg {
   static constexpr uint32_t kXBytes = NT * 128, kStage = kWBytes + kXBytes;
@@ -45,11 +49,12 @@ struct FewCfg {
   static constexpr size_t kSmem = 1024 + kStages * kStage + 128;
 };
 
-template <int NT, int PHASE, int ACT>
+template <int NT, int PHASE, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(kFewThreads)
     ffn_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, FewParams p) {
   using C = FewCfg<NT>;
   constexpr int S = C::kStages;
+  constexpr bool kTwoRows = SPLIT && PHASE == kDown;
   static_assert(S * C::kStage >= NT * kFewRows * 4, "the parts lie where the slices lay");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -88,7 +93,9 @@ __global__ void __launch_bounds__(kFewThreads)
       tma_load_2d(sa + 8192, &mw, fb, PHASE == kUp ? p.N + col0 : col0 + 64, kb * 64);
     };
     auto tokens = [&](int kb, int stage) {
-      tma_load_2d(smem_u32(smem + stage * C::kStage) + kWBytes, &mx, full0 + 8 * stage, kb * 64, 0);
+      const uint32_t sb = smem_u32(smem + stage * C::kStage) + kWBytes;
+      tma_load_2d(sb, &mx, full0 + 8 * stage, kb * 64, 0);
+      if (kTwoRows) tma_load_2d(sb + C::kXBytes / 2, &mx, full0 + 8 * stage, kb * 64, p.M);
     };
     const int first = min(S, k1 - k0);
     if (leader)
@@ -144,14 +151,19 @@ __global__ void __launch_bounds__(kFewThreads)
     if (k1 > k0 && mbar_wait(done, 0, &no_abort, p.st, 23)) {
       fence_after();
       const uint32_t tc0 = tmem + (static_cast<uint32_t>(q * 32) << 16);
+      constexpr int T = kTwoRows ? NT / 2 : NT;   // tokens
 #pragma unroll
-      for (int c = 0; c < NT; c += 16) {
-        uint32_t r[16];
+      for (int c = 0; c < T; c += 16) {
+        uint32_t r[16], lo[16];
         tmem_ld16_async(tc0 + c, r);
+        if (kTwoRows && T >= 16) tmem_ld16_async(tc0 + T + c, lo);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < p.M) mine[(c + i) * kFewRows + row] = __uint_as_float(r[i]);
+        for (int i = 0; i < (T < 16 ? T : 16); ++i) {
+          float v = __uint_as_float(r[i]);
+          if (kTwoRows) v += __uint_as_float(T < 16 ? r[(i + T) & 15] : lo[i]);
+          if (c + i < p.M) mine[(c + i) * kFewRows + row] = v;
+        }
       }
       fence_before();
     }
@@ -177,8 +189,14 @@ __global__ void __launch_bounds__(kFewThreads)
           *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(a.x, a.y);
           *reinterpret_cast<uint32_t*>(o + p.N) = pack_bf16x2(b.x, b.y);
         }
-        *reinterpret_cast<uint32_t*>(p.out + t * p.out_ld + col) =
-            pack_bf16x2(glu_act<ACT>(a.x) * b.x, glu_act<ACT>(a.y) * b.y);
+        const float sx = glu_act<ACT>(a.x) * b.x, sy = glu_act<ACT>(a.y) * b.y;
+        const uint32_t hi = pack_bf16x2(sx, sy);
+        *reinterpret_cast<uint32_t*>(p.out + t * p.out_ld + col) = hi;
+        if (SPLIT) {   // (what an infinity leaves is 0)
+          const float rx = sx - __uint_as_float(hi << 16), ry = sy - __uint_as_float(hi & 0xffff0000u);
+          *reinterpret_cast<uint32_t*>(p.out + (p.M + t) * p.out_ld + col) =
+              pack_bf16x2(isfinite(rx) ? rx : 0.f, isfinite(ry) ? ry : 0.f);
+        }
       } else {
         __nv_bfloat16* o = p.out + t * p.out_ld + col;
         if (col < p.N) *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(a.x, a.y);
@@ -201,9 +219,9 @@ int few_parts(int blocks, int kb, int num_sms) {
   return parts;
 }
 
-template <int NT, int PHASE, int ACT>
+template <int NT, int PHASE, int ACT, bool SPLIT>
 cudaError_t launch_few(const Ctx& c, const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p) {
-  auto k = ffn_few_kernel<NT, PHASE, ACT>;
+  auto k = ffn_few_kernel<NT, PHASE, ACT, SPLIT>;
   constexpr size_t smem = FewCfg<NT>::kSmem;
   static std::mutex mu;
   static bool known[64] = {false};
@@ -227,28 +245,37 @@ cudaError_t launch_few(const Ctx& c, const CUtensorMap& mx, const CUtensorMap& m
   return launched(e);
 }
 
-template <int PHASE, int ACT>
-cudaError_t launch_few_any(const Ctx& c, const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p) {
-  if (p.M <= 16) return launch_few<16, PHASE, ACT>(c, mx, mw, p);
-  if (p.M <= 32) return launch_few<32, PHASE, ACT>(c, mx, mw, p);
-  if (p.M <= 64) return launch_few<64, PHASE, ACT>(c, mx, mw, p);
-  return launch_few<128, PHASE, ACT>(c, mx, mw, p);
+template <int ACT>
+cudaError_t launch_up(const Ctx& c, const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p) {
+  if (p.M <= 16) return launch_few<16, kUp, ACT, true>(c, mx, mw, p);
+  if (p.M <= 32) return launch_few<32, kUp, ACT, true>(c, mx, mw, p);
+  if (p.M <= 64) return launch_few<64, kUp, ACT, true>(c, mx, mw, p);
+  return launch_few<128, kUp, ACT, false>(c, mx, mw, p);
+}
+cudaError_t launch_down(const Ctx& c, const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p) {
+  if (p.M <= 8) return launch_few<16, kDown, 0, true>(c, mx, mw, p);
+  if (p.M <= 16) return launch_few<32, kDown, 0, true>(c, mx, mw, p);
+  if (p.M <= 32) return launch_few<64, kDown, 0, true>(c, mx, mw, p);
+  if (p.M <= 64) return launch_few<128, kDown, 0, true>(c, mx, mw, p);
+  return launch_few<128, kDown, 0, false>(c, mx, mw, p);
 }
 
 }  // namespace
 
 cudaError_t launch_ffn_few(const Ctx& c, const FfnFew& a) {
   const int nt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+  const bool split = a.M <= kFfnSplit;
   CUtensorMap mx, mw, ms, md;
   if (!make_tensor_map(&mx, a.x, false, a.D, a.M, a.x_ld, 64, nt) ||
       !make_tensor_map(&mw, a.w_up, false, 2ll * a.F, a.D, 2ll * a.F, 64, 64) ||
-      !make_tensor_map(&ms, a.s, false, a.F, a.M, a.F, 64, nt) || !make_tensor_map(&md, a.w_down, false, a.D, a.F, a.D, 64, 64))
+      !make_tensor_map(&ms, a.s, false, a.F, split ? 2 * a.M : a.M, a.F, 64, a.M <= 8 ? 8 : nt) ||
+      !make_tensor_map(&md, a.w_down, false, a.D, a.F, a.D, 64, 64))
     return cudaErrorInvalidValue;
   FewParams p{a.M, a.F, (a.D + 63) / 64, a.up, a.s, a.up_ld, a.F, c.st};
-  cudaError_t e = a.act == kGluSilu ? launch_few_any<kUp, kGluSilu>(c, mx, mw, p) : launch_few_any<kUp, kGluGeluTanh>(c, mx, mw, p);
+  cudaError_t e = a.act == kGluSilu ? launch_up<kGluSilu>(c, mx, mw, p) : launch_up<kGluGeluTanh>(c, mx, mw, p);
   if (e != cudaSuccess) return e;
   p = FewParams{a.M, a.D, (a.F + 63) / 64, nullptr, a.y, 0, a.y_ld, c.st};
-  return launch_few_any<kDown, kGluSilu>(c, ms, md, p);
+  return launch_down(c, ms, md, p);
 }
 
 }  // namespace collider

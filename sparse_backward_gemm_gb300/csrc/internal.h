@@ -459,12 +459,13 @@ struct FfnDs {
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a);
 // up (may be null), s and y of M <= kFfnFew tokens (ffn_few.cu)
 constexpr int kFfnFew = 128;
+constexpr int kFfnSplit = 64;   // up to so many tokens s has [2 M, F]: two bf16 values of each
 struct FfnFew {
   int act, M, D, F;
   const void* x; long long x_ld;
   const void *w_up, *w_down;
   __nv_bfloat16* up; long long up_ld;
-  __nv_bfloat16* s;   // [M, F]
+  __nv_bfloat16* s;   // [M, F], or [2 M, F]
   __nv_bfloat16* y; long long y_ld;
 };
 cudaError_t launch_ffn_few(const Ctx& c, const FfnFew& a);

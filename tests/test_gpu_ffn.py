@@ -1,6 +1,6 @@
 """Gated feed-forward block on the GPU against the float64 oracle, element by element.
 
-Every bound counts roundings: H is half a step of bf16; a sum of K products in f32 is off by at most K 2^-23 of the sum
+Every bound counts roundings: H is half a step of bf16 (s of up to 64 tokens is kept as two bf16 values, H of H); a sum of K products in f32 is off by at most K 2^-23 of the sum
 of their magnitudes (E of that sum below); the activation and its slope by 2^-18 (1 + |g|) of the magnitudes that meet
 there (one exponential and one reciprocal, of arguments that f32 rounds)."""
 import threading
@@ -40,7 +40,7 @@ def forward_bounds(v, kind):
     g, u = np.split(np.abs(o["up"]), 2, axis=1)
     eg, eu = np.split(e_up, 2, axis=1)
     ds = 1.2 * eg * (u + eu) + g * eu + 2.0 ** -18 * (1 + g) * g * u      # |a'| < 1.2, |a| <= |g|
-    ds = ds + H * (np.abs(o["s"]) + ds)
+    ds = ds + (H if len(v["x"]) > 64 else H * H) * (np.abs(o["s"]) + ds)
     wd = np.abs(v["w_down"])
     ey = ds @ wd + E(F) * ((np.abs(o["s"]) + ds) @ wd)
     return o, dict(up=H * (np.abs(o["up"]) + e_up) + e_up, y=H * (np.abs(o["y"]) + ey) + ey)
@@ -160,6 +160,19 @@ def test_forward_keeps_infinities_in_their_rows():
     for g, w in zip(got, want):
         assert np.array_equal(g[rest], w[rest]) and not np.isfinite(g[[17, 200]]).any(axis=1).all()
         assert np.isnan(g[200]).all()
+
+
+def test_forward_of_few_tokens_keeps_infinities():
+    """An s that bf16 takes for infinity gives y what one infinity gives, in its row alone."""
+    v = inputs(5, 64, 128, 6)
+    v["x"][:], v["w_up"][:] = 1.0, 0.0
+    v["w_up"][0, :2], v["w_up"][0, 128:130] = 2.0 ** 60, 1.0
+    v["x"][2, 0] = 2.0 ** 34                               # s = 2^94 * 2^34 = 2^128 there, at columns 0 and 1
+    v["w_down"][0], v["w_down"][1] = 1.0, 0.5
+    up, y = run_forward(v, "silu")
+    y = gu.host(y)
+    assert (y[2] == np.inf).all()
+    assert np.array_equal(y[[0, 1, 3, 4]], np.full((4, 64), 1.5 * 2.0 ** 60))
 
 
 def index(M, f, seed):
