@@ -41,15 +41,14 @@ constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + 128 * kBK * 
 constexpr int kGroupRows = 16;    // 256-row units that follow each other down a column of tiles
 constexpr int kMaxWorkers = 80;   // CTA pairs of a launch, at most
 constexpr int kMaxTail = 1024;    // tiles of the part that is cut
-// kDs: an epilogue warp's 32 x 16 values of g and u, twice
+// kDs: an epilogue warp's chunk, 32 x 16 values of g and of u
 constexpr int kDsCols = 16;
-constexpr uint32_t kChunkBytes = 32 * kDsCols * 2, kSlotBytes = 2 * kChunkBytes;
-constexpr int kSlots = 1;
+constexpr uint32_t kChunkBytes = 32 * kDsCols * 2;
 template <int EPI>
 struct Cfg {
   static constexpr int kWarps = epi_warps(EPI), kThreads = 64 + 32 * kWarps;
   static constexpr int kStages = EPI == kDs ? 6 : 7;
-  static constexpr uint32_t kEpiBytes = EPI == kDs ? kWarps * kSlots * kSlotBytes : 0;
+  static constexpr uint32_t kEpiBytes = EPI == kDs ? kWarps * 2 * kChunkBytes : 0;
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 256 + (EPI == kGroup ? 4 * (kMaxWorkers + 1) + 64 : 0);
 };
 
@@ -84,10 +83,13 @@ struct Params {
 // parts that the others parked in memory and its own accumulator, in the order
 // of the pairs: the same sum whoever that is.
 //   Cutting costs a chain of memory round trips at the end (park, count, read
-// back), about 4 us or 16 k-slices; less gain than that is left alone.
-constexpr int kCutGain = 16;
-constexpr int kMinRange = 12;   // k-slices of a pair's range, at least
-constexpr int kMaxParts = 4;    // pairs to a tile of the tail, about: each part is 3 us more for whoever finishes it
+// back), 6 to 10 us; a k-slice is 0.3 us.  Measured bounds: a gain of 16
+// k-slices (with 8 the forward of 3003 x 1536 x 8960 is 160 us instead of 145,
+// with 28 the unfiltered backward of 4096 x 2048 x 5632 is 344 instead of 338);
+// ranges of 12 k-slices (with 6: 47 us instead of 41 for the backward of 240 x
+// 512 x 1408); about 4 pairs to a tile (with no bound 63 us instead of 36 for
+// the forward of 200 x 256 x 8192: whoever finishes reads 2 to 3 us a part).
+constexpr int kCutGain = 16, kMinRange = 12, kMaxParts = 4;
 struct Sched {
   int np, W, wid;
   int units[3], tiles[3], kb[3];   // 256-row units, tiles, k-slices of each product
@@ -104,7 +106,7 @@ __device__ __forceinline__ int count_mod(int a, int b, int w, uint32_t magic) {
 
 struct Tile {
   int p, k0, k1;
-  int m0, n0;     // this CTA's first row, the tile's first column
+  int m0, n0;     // this CTA's first row, the tile's place among the columns of tiles
   int t;
   bool whole;
 };
@@ -224,11 +226,7 @@ __device__ __forceinline__ void store32(const FfnProduct& p, const Rows4& rows, 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -544,9 +542,10 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       // A chunk is 32 rows x 16 columns of this warp.  Its g and u are copied to
       // shared memory (16-byte pieces, the two of a 32-byte row swapped in every
       // other four rows, so that the lanes' reads of their own rows meet no bank
-      // twice), two chunks ahead of the one in work; a tile's first two before
-      // its products are done.
-      const uint32_t slots = smem_u32(epi) + (warp - 2) * kSlots * kSlotBytes;
+      // twice) as soon as those of the chunk before are read; a tile's first
+      // before its products are done.  (A second chunk's room costs a stage of
+      // the ring: 430 us instead of 425 for the backward above.)
+      const uint32_t room = smem_u32(epi) + (warp - 2) * 2 * kChunkBytes;
       const uint32_t sw = ((lane >> 2) & 1) * 16;             // of this thread's row
       const int prow = lane >> 1, piece = lane & 1;           // the copies' rows: prow + 16 i
       // The copies run ahead by an iterator of their own: tile, chunk in it, and
@@ -555,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       Iter ahead(sc);
       Tile ct;
       bool copying;
-      int chunk = 0, slot = 0;
+      int chunk = 0;
       int src[2];
       auto next_rows = [&] {
         copying = ahead.next<NP>(rank, pr, &ct);
@@ -569,7 +568,6 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       };
       auto copy = [&] {
         if (copying) {
-          const uint32_t dst = slots + slot * kSlotBytes;
           const int col = ct.n0 * kBN + half * 64 + chunk * kDsCols + piece * 8;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -577,18 +575,15 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             const bool there = (unsigned)src[i] < (unsigned)p.M && col < p.F;
             if (chunk == 0 && !there && src[i] != kNoRow && col < p.F) report_error(p.st, kErrBadIndex, 702);
             const __nv_bfloat16* g = p.up + (there ? src[i] * p.up_ld + col : 0);
-            const uint32_t at = dst + r * 32 + ((piece ^ ((r >> 2) & 1)) * 16);
+            const uint32_t at = room + r * 32 + ((piece ^ ((r >> 2) & 1)) * 16);
             cp_async16(at, g, there);
             cp_async16(at + kChunkBytes, g + (there ? p.F : 0), there);
           }
           if (++chunk == 4) next_rows();
         }
-        cp_async_commit();      // (an empty group keeps the count)
-        slot = (slot + 1) % kSlots;
       };
       next_rows();
-      for (int i = 0; i < kSlots; ++i) copy();
-      int done = 0;          // chunks worked on
+      copy();
       while (iter.next<NP>(rank, pr, &t)) {
         const int acc = seg & 1;
         const int row = t.m0 + rl;
@@ -606,17 +601,16 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
         for (int c = 0; c < 4; ++c) {
           uint32_t d[kDsCols];
           tmem_ld16_async(tc0 + c * kDsCols, d);
-          cp_async_wait<kSlots - 1>();
+          cp_async_wait_all();
           __syncwarp();
-          const uint32_t buf = slots + (done % kSlots) * kSlotBytes + lane * 32;
+          const uint32_t buf = room + lane * 32;
           uint4 g4[2], u4[2], s4[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             g4[j] = lds128(buf + ((j * 16) ^ sw));
             u4[j] = lds128(buf + kChunkBytes + ((j * 16) ^ sw));
           }
-          __syncwarp();     // the slot is read: the chunk after the next may come
-          ++done;
+          __syncwarp();     // the room is read: the next chunk may come
           copy();
           tmem_wait_ld();
           if (c == 3) {
@@ -661,7 +655,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
         }
         ++seg;
       }
-      cp_async_wait<0>();
+      cp_async_wait_all();
     } else {
       while (iter.next<NP>(rank, pr, &t)) {
         const FfnProduct& pr = p.p[t.p];
