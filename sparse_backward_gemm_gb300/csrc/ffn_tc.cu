@@ -36,16 +36,17 @@ constexpr int kUp = 0, kDs = 1, kGroup = 2;
 // chains (copy, accumulator, activation, three stores), which twice the warps
 // hide better.
 constexpr int epi_warps(int epi) { return epi == kDs ? 16 : 8; }
-constexpr int kBM = 128, kBN = 256, kBK = 64;   // a CTA's rows, the pair's columns, a k-slice
-constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + 128 * kBK * 2;
+constexpr int kBM = 128, kBK = 64;   // a CTA's rows, a k-slice; a pair's columns: NB, 256 or 128
+constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr int kGroupRows = 16;    // 256-row units that follow each other down a column of tiles
 constexpr int kMaxWorkers = 80;   // CTA pairs of a launch, at most
 constexpr int kMaxTail = 1024;    // tiles of the part that is cut
 // kDs: an epilogue warp's chunk, 32 x 16 values of g and of u
 constexpr int kDsCols = 16;
 constexpr uint32_t kChunkBytes = 32 * kDsCols * 2;
-template <int EPI>
+template <int EPI, int NB>
 struct Cfg {
+  static constexpr uint32_t kStageBytes = kABytes + NB / 2 * kBK * 2;
   static constexpr int kWarps = epi_warps(EPI), kThreads = 64 + 32 * kWarps;
   static constexpr int kStages = EPI == kDs ? 6 : 7;
   static constexpr uint32_t kEpiBytes = EPI == kDs ? kWarps * 2 * kChunkBytes : 0;
@@ -68,7 +69,7 @@ struct Params {
   FfnProduct p[3];
   int np;
   uint32_t by_pairs;  // 2^32 / pairs, rounded up
-  float* partial;     // [2 * pairs][2][kBN / 4][kBM][4] f32 (with two pairs to a cluster: [2 * clusters][4]...)
+  float* partial;     // [2 * pairs][2][NB / 4][kBM][4] f32 (with two pairs to a cluster: [2 * clusters][4]...)
   int* counters;      // [kMaxTail][CTAs of a cluster], zero on entry and left zero
   DevStatus* st;
 };
@@ -232,14 +233,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-template <int EPI, int ACT, int NP>
-__global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
+template <int EPI, int ACT, int NP, int NB>
+__global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-  constexpr int S = Cfg<EPI>::kStages, kEpiWarps = Cfg<EPI>::kWarps, kThreads = Cfg<EPI>::kThreads;
+  using C = Cfg<EPI, NB>;
+  constexpr int S = C::kStages, kEpiWarps = C::kWarps, kThreads = C::kThreads;
+  constexpr uint32_t kStageBytes = C::kStageBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* epi = smem + S * kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + Cfg<EPI>::kEpiBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + C::kEpiBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
   }
   if (warp == 0 && lane < (EPI == kGroup ? 2 * p.np : 2))
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.m[lane])) : "memory");
-  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 2 * kBN);
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 2 * NB);
   fence_before();
   __syncthreads();
   cluster_sync();   // the peer's barriers exist before any copy or commit reaches them
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       const FfnProduct& q = p.p[i];
       const int m = q.dyn == 1 ? min(q.M, n) : q.M, k = q.dyn == 2 ? min(q.K, n) : q.K;
       sc.units[i] = (m + 2 * kBM - 1) / (2 * kBM);
-      sc.tiles[i] = sc.units[i] * ((q.N + NP * kBN - 1) / (NP * kBN));
+      sc.tiles[i] = sc.units[i] * ((q.N + NP * NB - 1) / (NP * NB));
       sc.kb[i] = (k + kBK - 1) / kBK;
       total += sc.tiles[i];
       slices += (long long)sc.tiles[i] * sc.kb[i];
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
   } else {
     sc.np = 1;
     sc.units[0] = (n + 2 * kBM - 1) / (2 * kBM);
-    constexpr int cols = NP * (EPI == kUp ? kBN / 2 : kBN);
+    constexpr int cols = NP * (EPI == kUp ? NB / 2 : NB);
     sc.tiles[0] = sc.units[0] * ((p.F + cols - 1) / cols);
     sc.kb[0] = p.kb;
     sc.first[0] = 0;
@@ -402,8 +405,8 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       const CUtensorMap* ma = &maps.m[EPI == kGroup ? 2 * t.p : 0];
       const CUtensorMap* mb = ma + 1;
       const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
-      // this CTA's half of the tile's columns: of kUp, all 128 of g or of u
-      const int nb = EPI == kUp ? t.n0 * 128 + rank * p.F : t.n0 * kBN + rank * 128;
+      // this CTA's half of the tile's columns: of kUp, all of g or of u
+      const int nb = EPI == kUp ? t.n0 * (NB / 2) + rank * p.F : t.n0 * NB + rank * (NB / 2);
       bool ok = true;
       for (int kb = t.k0; kb < t.k1; ++kb) {
         if (!wait(empty0 + 8 * stage, phase ^ 1u, 1)) { ok = false; break; }
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             tma_load_2d_pair(sb, mb, lb, kx, nb);
           } else {
             tma_load_2d_pair(sb, mb, lb, nb, kx);
-            tma_load_2d_pair(sb + 8192, mb, lb, nb + 64, kx);
+            if (NB == 256) tma_load_2d_pair(sb + 8192, mb, lb, nb + 64, kx);
           }
         }
         __syncwarp();
@@ -469,12 +472,12 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       Tile t;
       while (iter.next<NP>(rank, pr, &t) && !__any_sync(0xffffffffu, *abort_flag != 0)) {
         const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
-        const uint32_t idesc = idesc_bf16(2 * kBM, kBN, a_mn, b_mn);
+        const uint32_t idesc = idesc_bf16(2 * kBM, NB, a_mn, b_mn);
         const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32, a_lbo = a_mn ? 8192 : 16, b_lbo = b_mn ? 8192 : 16;
         const int acc = seg & 1;
         if (!wait(tempty0 + 8 * acc, ((seg >> 1) & 1) ^ 1u, 2)) break;
         fence_after();
-        const uint32_t d = tmem_base + acc * kBN;
+        const uint32_t d = tmem_base + acc * NB;
         bool ok = true;
         for (int kb = t.k0; kb < t.k1; ++kb) {
           if (!wait(full0 + 8 * stage, phase, 3)) { ok = false; break; }
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
     auto release_acc = [&](int acc) { mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8 * acc, leader_cta)); };
     volatile int no_abort = 0;   // (timeout-only waits: the threads leave together)
     const int q = warp & 3;      // TMEM lane quadrant this warp may access
-    const int half = (warp - 2) >> 2;   // its share of the columns: of kUp 64 of g and of u, of kDs 64, else 128
+    const int half = (warp - 2) >> 2;   // its share of the columns: of kUp a quarter of NB of g and of u, of kDs a quarter, else half
     const int rl = q * 32 + lane;
     int seg = 0;
     Iter iter(sc);
@@ -513,17 +516,17 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
         const Rows4 up_rows(row < n ? row * p.up_ld : -1), s_rows(row < n ? (long long)row * p.F : -1);
         if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
         fence_after();
-        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 64;
+        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NB + half * (NB / 4);
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
+        for (int c = 0; c < NB / 4; c += 32) {
           float g[32], u[32];
           tmem_ld32(tc0 + c, g);
-          tmem_ld32(tc0 + 128 + c, u);
-          if (c == 32) {
+          tmem_ld32(tc0 + NB / 2 + c, u);
+          if (c == NB / 4 - 32) {
             fence_before();
             release_acc(acc);
           }
-          const int col = t.n0 * 128 + half * 64 + c;
+          const int col = t.n0 * (NB / 2) + half * (NB / 4) + c;
           uint4 w[4];
           if (p.up) {
             pack32(g, w);
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       const int prow = lane >> 1, piece = lane & 1;           // the copies' rows: prow + 16 i
       // The copies run ahead by an iterator of their own: tile, chunk in it, and
       // the rows of `up` of the tile (row prow + 16 i of the warp's 32).
-      constexpr int kNoRow = INT32_MIN;
+      constexpr int kNoRow = INT32_MIN, kChunks = NB / 4 / kDsCols;   // (chunks of a warp's share of a tile)
       Iter ahead(sc);
       Tile ct;
       bool copying;
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       };
       auto copy = [&] {
         if (copying) {
-          const int col = ct.n0 * kBN + half * 64 + chunk * kDsCols + piece * 8;
+          const int col = ct.n0 * NB + half * (NB / 4) + chunk * kDsCols + piece * 8;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r = prow + 16 * i;
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             cp_async16(at, g, there);
             cp_async16(at + kChunkBytes, g + (there ? p.F : 0), there);
           }
-          if (++chunk == 4) next_rows();
+          if (++chunk == kChunks) next_rows();
         }
       };
       next_rows();
@@ -596,9 +599,9 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
         }
         if (!mbar_wait(tfull0 + 8 * acc, (seg >> 1) & 1, &no_abort, p.st, 4)) break;
         fence_after();
-        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 64;
+        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NB + half * (NB / 4);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kChunks; ++c) {
           uint32_t d[kDsCols];
           tmem_ld16_async(tc0 + c * kDsCols, d);
           cp_async_wait_all();
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
           __syncwarp();     // the room is read: the next chunk may come
           copy();
           tmem_wait_ld();
-          if (c == 3) {
+          if (c == kChunks - 1) {
             fence_before();
             release_acc(acc);
           }
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
           transpose2(g4);
           transpose2(u4);
           transpose2(s4);
-          const int col = t.n0 * kBN + half * 64 + c * kDsCols + 8 * (lane & 1);
+          const int col = t.n0 * NB + half * (NB / 4) + c * kDsCols + 8 * (lane & 1);
           if (col < p.F) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -657,6 +660,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
       }
       cp_async_wait_all();
     } else {
+      constexpr int kHalf = NB / 2;   // columns of a warp
       while (iter.next<NP>(rank, pr, &t)) {
         const FfnProduct& pr = p.p[t.p];
         const int acc = seg & 1;
@@ -703,14 +707,14 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             last_flag[0] = (old & 0xffff) == parts - 1 ? parts : 0;
           }
         }
-        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN + half * 128;
-        const int col0 = t.n0 * kBN + half * 128;
+        const uint32_t tc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NB + half * kHalf;
+        const int col0 = t.n0 * NB + half * kHalf;
         if (t.whole) {
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < kHalf; c += 32) {
             float v[32];
             tmem_ld32(tc0 + c, v);
-            if (c == 96) {
+            if (c == kHalf - 32) {
               fence_before();
               release_acc(acc);
             }
@@ -725,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
           // begins in, in place 1 of the tile it ends in.
           auto slot_of = [&](int w) {
             const int at = 2 * w + (begin[w] >= x0 && begin[w] < x1 ? 0 : 1);
-            return p.partial + ((long long)at * 2 * NP + crank) * (kBM * kBN);
+            return p.partial + ((long long)at * 2 * NP + crank) * (kBM * NB);
           };
           named_bar(1, 32 * kEpiWarps);
           const int parts = *last_flag;
@@ -733,13 +737,13 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
           if (!parts) {
             float* own = slot_of(wid);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
+            for (int c = 0; c < kHalf; c += 32) {
               float v[32];
               tmem_ld32(tc0 + c, v);
               if (!live) continue;
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                __stcg(reinterpret_cast<float4*>(own + ((long long)((half * 128 + c + i) >> 2) * kBM + rl) * 4),
+                __stcg(reinterpret_cast<float4*>(own + ((long long)((half * kHalf + c + i) >> 2) * kBM + rl) * 4),
                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
             }
             fence_before();
@@ -759,7 +763,7 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             const int other = parts == 2 ? (c_first == wid ? c_last : c_first) : -1;
             auto load_part = [&](int w, int c, float* x) {
               if (live) {
-                const float* from = slot_of(w) + ((long long)((half * 128 + c) >> 2) * kBM + rl) * 4;
+                const float* from = slot_of(w) + ((long long)((half * kHalf + c) >> 2) * kBM + rl) * 4;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   const float4 y = __ldcg(reinterpret_cast<const float4*>(from + i * kBM * 4));
@@ -773,14 +777,14 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
             float next[32];
             if (other >= 0) load_part(other, 0, next);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
+            for (int c = 0; c < kHalf; c += 32) {
               float v[32];
               if (other >= 0) {
                 float x[32];
                 tmem_ld32(tc0 + c, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = next[i];
-                if (c < 96) load_part(other, c + 32, next);
+                if (c < kHalf - 32) load_part(other, c + 32, next);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += x[i];   // (of two, either order is the same)
               } else {
@@ -816,17 +820,17 @@ __global__ void __launch_bounds__(Cfg<EPI>::kThreads, 1)
   cluster_sync();
   if (warp == 1) {
     fence_after();
-    tmem_dealloc_pair(tmem_base, 2 * kBN);
+    tmem_dealloc_pair(tmem_base, 2 * NB);
   }
 }
 
 // ---------------------------------------------------------------------------
 // host side
-template <int EPI, int ACT, int NP>
+template <int EPI, int ACT, int NP, int NB>
 cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, long long tiles, long long m, long long n,
-                   long long k, int dyn) {
-  auto kern = ffn_kernel<EPI, ACT, NP>;
-  constexpr size_t smem = Cfg<EPI>::kSmem;
+                   long long k, int dyn) {   // tiles: of a pair
+  auto kern = ffn_kernel<EPI, ACT, NP, NB>;
+  constexpr size_t smem = Cfg<EPI, NB>::kSmem;
   // per device, once: the shared-memory opt-in, and how many pairs run at once
   static std::mutex mu;
   static int known[64] = {0};
@@ -845,7 +849,7 @@ cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, l
       attr[0].val.clusterDim.x = 2 * NP;
       attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3(2 * NP * (c.num_sms / (2 * NP)));
-      cfg.blockDim = dim3(Cfg<EPI>::kThreads);
+      cfg.blockDim = dim3(Cfg<EPI, NB>::kThreads);
       cfg.dynamicSmemBytes = smem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
@@ -861,13 +865,13 @@ cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, l
   p.by_pairs = (uint32_t)(((1ull << 32) + workers - 1) / workers);
   if (workers < 2) p.partial = nullptr;   // (nobody to share with; 2^32 / 1 does not fit)
   prof_begin(c, name, m, n, k, dyn);
-  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(2 * NP * workers), dim3(Cfg<EPI>::kThreads), smem, 2 * NP, maps, p);
+  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(2 * NP * workers), dim3(Cfg<EPI, NB>::kThreads), smem, 2 * NP, maps, p);
   prof_end(c);
   count_launch();
   return launched(e);
 }
 
-bool k_major(CUtensorMap* m, const void* p, long long inner, long long rows, long long ld, int box_rows = 128) {
+bool k_major(CUtensorMap* m, const void* p, long long inner, long long rows, long long ld, int box_rows) {
   return make_tensor_map(m, p, false, inner, rows, ld, 64, box_rows);
 }
 bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, long long ld) {
@@ -876,43 +880,61 @@ bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, lo
 
 }  // namespace
 
-// Two pairs to a cluster load the rows' operand once for both, so a quarter
-// less comes through L2: for lists of two waves of 256 x 256 tiles at least.
-// One pair and two, us: backward 2403 x 1536 x 8960 272-290 and 265-267, 1229 x
-// 2048 x 5632 139 and 136.5; in a loop of seconds, under the power limit, 8192 x
-// 2048 x 5632 forward 363 and 360, 4916 rows backward 484 and 482 (alone 427 and
-// 431).  Below, the wider tiles fill the SMs worse: 800 x 1024 x 2816 57 and 61.
-static bool side_by_side(const Ctx& c, long long pair_tiles) { return pair_tiles >= c.num_sms; }
+// The form of a list of so many 256 x 256 tiles.
+//   Two waves or more: two pairs to a cluster load the rows' operand once for
+// both, so a quarter less comes through L2.  One pair and two, us: backward 2403
+// x 1536 x 8960 272-290 and 265-267, 1229 x 2048 x 5632 139 and 136.5; in a loop
+// of seconds, under the power limit, 8192 x 2048 x 5632 forward 363 and 360, 4916
+// rows backward 484 and 482 (alone 427 and 431).  Below, the wider tiles fill the
+// SMs worse: 800 x 1024 x 2816 57 and 61.
+//   At most a quarter of a wave of SMs: tiles of 128 columns, so that twice the SMs
+// share the epilogues.
+enum class Form { kNarrow, kPair, kPairs };
+static Form form_of(const Ctx& c, long long tiles) {
+  return tiles >= c.num_sms ? Form::kPairs : 4 * tiles <= c.num_sms ? Form::kNarrow : Form::kPair;
+}
+static int rows_box(Form f) { return f == Form::kPairs ? 64 : 128; }       // of the rows' operand, K-major
+static int cols_box(Form f) { return f == Form::kNarrow ? 64 : 128; }      // of the columns'
+template <int EPI, int ACT, typename... A>
+static cudaError_t launch_form(Form f, A... args) {
+  return f == Form::kPairs    ? launch<EPI, ACT, 2, 256>(args...)
+         : f == Form::kNarrow ? launch<EPI, ACT, 1, 128>(args...)
+                              : launch<EPI, ACT, 1, 256>(args...);
+}
+static long long tiles_of(Form f, long long m, long long n) {
+  const int nb = f == Form::kNarrow ? 128 : 256;
+  return (m + 2 * kBM - 1) / (2 * kBM) * ((n + nb - 1) / nb);
+}
 
 size_t ffn_partial_floats(long long tiles) {
   // two parts a pair, of 128 rows in each of its CTAs; at most about kMaxParts pairs work at a tile
-  return (size_t)(2 * std::min<long long>(kMaxWorkers, kMaxParts * tiles) * 2) * kBM * kBN;
+  // (of 128-column tiles there are twice as many at most, of half the size)
+  return (size_t)(2 * std::min<long long>(kMaxWorkers, kMaxParts * tiles) * 2) * kBM * 256;
 }
-long long ffn_tiles(long long m, long long n) { return (m + 2 * kBM - 1) / (2 * kBM) * ((n + kBN - 1) / kBN); }
+long long ffn_tiles(long long m, long long n) { return tiles_of(Form::kPair, m, n); }
 int ffn_counters() { return 4 * kMaxTail; }
 
 cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
   Maps maps{};
-  const long long tiles = ffn_tiles(a.M, 2ll * a.F);
-  const bool two = side_by_side(c, tiles);
-  if (!k_major(&maps.m[0], a.x, a.D, a.M, a.x_ld, two ? 64 : 128) || !mn_major(&maps.m[1], a.w_up, 2ll * a.F, a.D, 2ll * a.F))
+  const Form f = form_of(c, ffn_tiles(a.M, 2ll * a.F));
+  if (!k_major(&maps.m[0], a.x, a.D, a.M, a.x_ld, rows_box(f)) || !mn_major(&maps.m[1], a.w_up, 2ll * a.F, a.D, 2ll * a.F))
     return cudaErrorInvalidValue;
   Params p{};
   p.M = a.M; p.F = a.F; p.kb = (a.D + kBK - 1) / kBK;
   p.up = a.up; p.up_ld = a.up_ld; p.s = a.s;
   p.zero = a.counters; p.n_zero = ffn_counters();
   p.st = c.st;
-  auto go = [&](auto k) { return k(c, "ffn_up", maps, p, tiles, a.M, 2ll * a.F, a.D, 0); };
-  if (a.act == kGluSilu) return two ? go(launch<kUp, kGluSilu, 2>) : go(launch<kUp, kGluSilu, 1>);
-  return two ? go(launch<kUp, kGluGeluTanh, 2>) : go(launch<kUp, kGluGeluTanh, 1>);
+  const long long tiles = tiles_of(f, a.M, 2ll * a.F);
+  return a.act == kGluSilu ? launch_form<kUp, kGluSilu>(f, c, "ffn_up", maps, p, tiles, a.M, 2ll * a.F, a.D, 0)
+                           : launch_form<kUp, kGluGeluTanh>(f, c, "ffn_up", maps, p, tiles, a.M, 2ll * a.F, a.D, 0);
 }
 
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a) {
   Maps maps{};
-  const long long tiles = ffn_tiles(a.M, a.F);
-  const bool two = side_by_side(c, tiles);
-  const bool ok = k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld, two ? 64 : 128) && k_major(&maps.m[1], a.w_down, a.D, a.F, a.D);
-  if (!ok) return cudaErrorInvalidValue;
+  const Form f = form_of(c, ffn_tiles(a.M, a.F));
+  if (!k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld, rows_box(f)) ||
+      !k_major(&maps.m[1], a.w_down, a.D, a.F, a.D, cols_box(f)))
+    return cudaErrorInvalidValue;
   Params p{};
   p.M = a.M; p.F = a.F; p.kb = (a.D + kBK - 1) / kBK;
   p.n_kept = a.n_kept; p.idx = a.up_full ? a.idx : nullptr;
@@ -920,9 +942,10 @@ cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a) {
   p.dgu = a.dgu; p.s = a.s; p.cap = a.cap;
   p.zero = a.counters; p.n_zero = ffn_counters();
   p.st = c.st;
-  auto go = [&](auto k) { return k(c, "ffn_ds", maps, p, tiles, a.M, a.F, a.D, a.n_kept ? 1 : 0); };
-  if (a.act == kGluSilu) return two ? go(launch<kDs, kGluSilu, 2>) : go(launch<kDs, kGluSilu, 1>);
-  return two ? go(launch<kDs, kGluGeluTanh, 2>) : go(launch<kDs, kGluGeluTanh, 1>);
+  const long long tiles = tiles_of(f, a.M, a.F);
+  const int dyn = a.n_kept ? 1 : 0;
+  return a.act == kGluSilu ? launch_form<kDs, kGluSilu>(f, c, "ffn_ds", maps, p, tiles, a.M, a.F, a.D, dyn)
+                           : launch_form<kDs, kGluGeluTanh>(f, c, "ffn_ds", maps, p, tiles, a.M, a.F, a.D, dyn);
 }
 
 cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, const int32_t* idx, const int32_t* n_kept,
@@ -931,12 +954,12 @@ cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, c
   Params p{};
   long long tiles = 0;
   for (int i = 0; i < np; ++i) tiles += ffn_tiles(q[i].M, q[i].N);
-  const bool two = side_by_side(c, tiles);
+  const Form f = form_of(c, tiles);
   for (int i = 0; i < np; ++i) {
     const bool a_ok = q[i].a_mn ? mn_major(&maps.m[2 * i], q[i].A, q[i].M, q[i].a_rows, q[i].lda)
-                                : k_major(&maps.m[2 * i], q[i].A, q[i].K, q[i].a_rows, q[i].lda, two ? 64 : 128);
+                                : k_major(&maps.m[2 * i], q[i].A, q[i].K, q[i].a_rows, q[i].lda, rows_box(f));
     const bool b_ok = q[i].b_mn ? mn_major(&maps.m[2 * i + 1], q[i].B, q[i].N, q[i].b_rows, q[i].ldb)
-                                : k_major(&maps.m[2 * i + 1], q[i].B, q[i].K, q[i].b_rows, q[i].ldb);
+                                : k_major(&maps.m[2 * i + 1], q[i].B, q[i].K, q[i].b_rows, q[i].ldb, cols_box(f));
     if (!a_ok || !b_ok) return cudaErrorInvalidValue;
     p.p[i] = q[i];
   }
@@ -944,8 +967,7 @@ cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, c
   p.M = M; p.idx = idx; p.n_kept = n_kept;
   p.partial = partial; p.counters = counters;
   p.st = c.st;
-  auto go = [&](auto k) { return k(c, "ffn_group", maps, p, tiles, q[0].M, q[0].N, q[0].K, q[0].dyn); };
-  return two ? go(launch<kGroup, 0, 2>) : go(launch<kGroup, 0, 1>);
+  return launch_form<kGroup, 0>(f, c, "ffn_group", maps, p, tiles, q[0].M, q[0].N, q[0].K, q[0].dyn);
 }
 
 }  // namespace collider

@@ -124,7 +124,7 @@ def run_forward(v, kind, pads=(0, 0, 0), want_up=True, stream=None):
 
 SIZES = [(1, 8, 8), (1, 256, 1024), (3, 1024, 2048), (17, 520, 648), (32, 64, 64), (64, 2048, 264), (65, 264, 520), (2, 64, 136), (5, 200, 72), (16, 512, 264), (33, 1536, 96), (127, 72, 136), (128, 128, 256),
          (129, 256, 384), (192, 256, 384), (300, 200, 1000), (513, 64, 8), (700, 8, 640), (200, 256, 8192), (1025, 384, 1096),
-         (2300, 1024, 2816)]
+         (1300, 512, 2048), (2300, 1024, 2816)]
 
 
 @pytest.mark.parametrize("M,D,F", SIZES)
