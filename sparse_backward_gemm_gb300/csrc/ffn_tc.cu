@@ -83,14 +83,15 @@ struct Params {
 // cut between pairs is finished by whichever comes last, which adds the
 // parts that the others parked in memory and its own accumulator, in the order
 // of the pairs: the same sum whoever that is.
-//   Cutting costs a chain of memory round trips at the end (park, count, read
-// back), 6 to 10 us; a k-slice is 0.3 us.  Measured bounds: a gain of 16
-// k-slices (with 8 the forward of 3003 x 1536 x 8960 is 160 us instead of 145,
-// with 28 the unfiltered backward of 4096 x 2048 x 5632 is 344 instead of 338);
-// ranges of 12 k-slices (with 6: 47 us instead of 41 for the backward of 240 x
-// 512 x 1408); about 4 pairs to a tile (with no bound 63 us instead of 36 for
-// the forward of 200 x 256 x 8192: whoever finishes reads 2 to 3 us a part).
-constexpr int kCutGain = 16, kMinRange = 12, kMaxParts = 4;
+//   Cutting costs a chain of memory round trips at the end: counting, parking,
+// and the finisher's reading of every part.  Measured, in k-slices of 0.3 us: 14
+// and 8 for every part but one (6.6 us with two pairs to a tile, 11.4 with four).
+// So of ranges long enough for 2, 3, 4 or 5 pairs to a tile the best is taken,
+// or none.  (Cut wherever 16 k-slices were gained: 560 x 768 x 1496 backward 44
+// us, so 40; with any number of pairs to a tile the forward of 200 x 256 x 8192
+// 63 us, so 29; never cut, the backward's group of 4916 x 2048 x 5632 20 us
+// more.)
+constexpr int kCutCost = 14, kPartCost = 8, kMaxParts = 4;
 struct Sched {
   int np, W, wid;
   int units[3], tiles[3], kb[3];   // 256-row units, tiles, k-slices of each product
@@ -324,18 +325,32 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
     // (ranges shorter than a tile would cut tiles into more than two: a wave more for them)
     if (waves > 0 && share - fit < left) --waves;
     const int dp = min(total, waves * W);
-    if (p.partial && share > 0 && load0 >= share + kCutGain && total - dp <= kMaxTail) {
-      sc.dp = dp;
-      int off = 0;
-      for (int i = 0; i < 3; ++i) {
-        sc.tail_first[i] = max(sc.first[i], dp);
-        sc.tail_off[i] = off;
-        if (i < p.np) off += max(0, sc.first[i] + sc.tiles[i] - sc.tail_first[i]) * sc.kb[i];
+    int off = 0, longest = 0;
+    for (int i = 0; i < 3; ++i) {
+      sc.tail_first[i] = max(sc.first[i], dp);
+      sc.tail_off[i] = off;
+      const int tail = i < p.np ? max(0, sc.first[i] + sc.tiles[i] - sc.tail_first[i]) : 0;
+      if (total - dp <= kMaxTail) off += tail * sc.kb[i];
+      if (tail) longest = max(longest, sc.kb[i]);
+    }
+    sc.tail_off[3] = off;
+    // k-slices of a range (on average: the pairs with less work before take
+    // more), and of a pair's whole work with what cutting costs
+    int range = 0, best = load0;
+    const int even = (int)__umulhi((uint32_t)off, magic) + 1;
+    for (int parts = 2; parts <= kMaxParts + 1; ++parts) {
+      const int r = max(even, (longest + parts - 2) / (parts - 1));
+      const int all = share + r - even + kCutCost + kPartCost * (parts - 1);
+      if (all < best) {
+        best = all;
+        range = r;
       }
-      sc.tail_off[3] = off;
+    }
+    if (p.partial && share > 0 && range > 0 && total - dp <= kMaxTail) {
+      sc.dp = dp;
       if (warp == 2) {
         // a pair's range fills it up to its share; short tails go to fewer pairs
-        int G = max(1, min(min(W, off / kMinRange), kMaxParts * (total - dp)));
+        int G = max(1, min(min(W, (off + range - 1) / range), kMaxParts * (total - dp)));
         // (few tiles of one length are cut into equal parts: no pair then has parts of two)
         if (dp == 0 && 2 * total <= G && off == total * sc.kb[0]) G -= G % total;
         int before = 0, at[kMaxWorkers / 32 + 1];
