@@ -390,12 +390,15 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
     sc.dp = sc.tiles[0];
     if (sc.units[0] == 0) sc.units[0] = 1;
   }
-  grid_dep_wait();   // the operands, the counters and the outputs are the kernels' ahead until here
+  // What the kernel ahead in the call writes is read by the producer and by
+  // kGroup's epilogue alone, which wait for it (kDs: the kept rows of dy; kGroup:
+  // its operands and counters).
   if (EPI != kGroup && p.zero && blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.n_zero; i += kThreads) p.zero[i] = 0;
 
   if (EPI == kGroup && p.n_kept && n == 0) {
     // nothing kept: sums over the kept rows are 0
+    grid_dep_wait();
     if (warp >= 2)
       for (int i = 0; i < p.np; ++i) {
         const FfnProduct& q = p.p[i];
@@ -416,7 +419,9 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
     uint32_t phase = 0, armed = 0, armed_parity = 0;   // stages with copies issued, and the phase parity armed
     Iter iter(sc);
     Tile t;
-    while (iter.next<NP>(rank, pr, &t) && !aborted()) {
+    bool more = iter.next<NP>(rank, pr, &t);
+    grid_dep_wait();
+    for (; more && !aborted(); more = iter.next<NP>(rank, pr, &t)) {
       const CUtensorMap* ma = &maps.m[EPI == kGroup ? 2 * t.p : 0];
       const CUtensorMap* mb = ma + 1;
       const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
@@ -676,6 +681,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
       cp_async_wait_all();
     } else {
       constexpr int kHalf = NB / 2;   // columns of a warp
+      grid_dep_wait();
       while (iter.next<NP>(rank, pr, &t)) {
         const FfnProduct& pr = p.p[t.p];
         const int acc = seg & 1;
