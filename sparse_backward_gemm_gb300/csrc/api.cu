@@ -1969,8 +1969,9 @@ struct FfnFwdBufs {
   int* counters;
 };
 size_t ffn_fwd_carve(Carver& cv, const collider_ffn_desc* d, FfnFwdBufs* b) {
-  b->s = cv.take<__nv_bfloat16>((size_t)d->M * d->F * (d->M <= kFfnSplit ? 2 : 1));
-  if (d->M <= kFfnFew) return cv.used;   // (no tiles that are cut)
+  const bool few = ffn_few(d->M, d->D, d->F);
+  b->s = cv.take<__nv_bfloat16>((size_t)d->M * d->F * (few && d->M <= kFfnSplit ? 2 : 1));
+  if (few) return cv.used;   // (no tiles that are cut)
   b->partial = cv.take<float>(ffn_partial_floats(ffn_tiles(d->M, d->D)));
   b->counters = cv.take<int>(ffn_counters());
   return cv.used;
@@ -2025,7 +2026,7 @@ extern "C" collider_status collider_ffn_fwd(const collider_ffn_desc* d, const vo
   Carver cv{static_cast<char*>(ws), ws_bytes, 0, false};
   FfnFwdBufs b;
   ffn_fwd_carve(cv, d, &b);
-  if (M <= kFfnFew) {
+  if (ffn_few(M, D, F)) {
     FfnFew f{};
     f.act = d->act; f.M = M; f.D = D; f.F = F;
     f.x = x; f.x_ld = ld.x; f.w_up = w_up; f.w_down = w_down;

@@ -1,4 +1,4 @@
-// The gated feed-forward block's forward of a few tokens (M <= 128): its time is
+// The gated feed-forward block's forward of a few tokens (M <= 128, ffn_few): its time is
 // the reading of the weights, so they are the wide operand.  A tile of 128
 // output features (64 gates and the same 64 ups, or 128 columns of y) is the A
 // of 128 x N x 16 MMAs, the tokens, padded to N = 16, 32, 64 or 128, are the B: the
@@ -6,8 +6,7 @@
 // touches them.  A cluster's CTAs split the reduction, so that all SMs read;
 // their parts meet through distributed shared memory, in CTA order.
 //   Measured at 2048 x 5632 (69 MB of weights; 10.3 us at the copy rate): 1 token
-// 22 us, 64 28, 128 36; as 256-row tiles 65, 56 and 44.  256 x 384, where nothing
-// but launches counts: 33 tokens 12.7 us, 100 17.0 (256-row tiles 16.4).
+// 22 us, 64 29, 128 36; as 256-row tiles 65 (of 256 columns), 37 and 38.
 #include <algorithm>
 #include <mutex>
 

@@ -1,6 +1,6 @@
 """Gated feed-forward block on the GPU against the float64 oracle, element by element.
 
-Every bound counts roundings: H is half a step of bf16 (s of up to 64 tokens is kept as two bf16 values, H of H); a sum of K products in f32 is off by at most K 2^-23 of the sum
+Every bound counts roundings: H is half a step of bf16 (s of up to 32 tokens is kept as two bf16 values, H of H); a sum of K products in f32 is off by at most K 2^-23 of the sum
 of their magnitudes (E of that sum below); the activation and its slope by 2^-18 (1 + |g|) of the magnitudes that meet
 there (one exponential and one reciprocal, of arguments that f32 rounds)."""
 import threading
@@ -40,7 +40,7 @@ def forward_bounds(v, kind):
     g, u = np.split(np.abs(o["up"]), 2, axis=1)
     eg, eu = np.split(e_up, 2, axis=1)
     ds = 1.2 * eg * (u + eu) + g * eu + 2.0 ** -18 * (1 + g) * g * u      # |a'| < 1.2, |a| <= |g|
-    ds = ds + (H if len(v["x"]) > 64 else H * H) * (np.abs(o["s"]) + ds)
+    ds = ds + (H if len(v["x"]) > 32 else H * H) * (np.abs(o["s"]) + ds)
     wd = np.abs(v["w_down"])
     ey = ds @ wd + E(F) * ((np.abs(o["s"]) + ds) @ wd)
     return o, dict(up=H * (np.abs(o["up"]) + e_up) + e_up, y=H * (np.abs(o["y"]) + ey) + ey)
@@ -122,7 +122,7 @@ def run_forward(v, kind, pads=(0, 0, 0), want_up=True, stream=None):
     return up, y
 
 
-SIZES = [(1, 8, 8), (1, 256, 1024), (3, 1024, 2048), (17, 520, 648), (32, 64, 64), (64, 2048, 264), (65, 264, 520), (2, 64, 136), (5, 200, 72), (16, 512, 264), (33, 1536, 96), (127, 72, 136), (128, 128, 256),
+SIZES = [(1, 8, 8), (1, 256, 1024), (3, 1024, 2048), (17, 520, 648), (32, 64, 64), (64, 2048, 264), (65, 264, 520), (40, 520, 1032), (100, 1032, 2056), (2, 64, 136), (5, 200, 72), (16, 512, 264), (33, 1536, 96), (127, 72, 136), (128, 128, 256),
          (129, 256, 384), (192, 256, 384), (300, 200, 1000), (513, 64, 8), (700, 8, 640), (200, 256, 8192), (1025, 384, 1096),
          (1300, 512, 2048), (2300, 1024, 2816)]
 
