@@ -15,9 +15,10 @@
 // CTAs loads half of the 128 rows it shares with one of the other pair and
 // multicasts it to both.  Every wait is bounded.
 //   Measured at 8192 x 2048 x 5632, 40% filtered (4916 kept): kUp 200 us (1.89
-// PFLOP/s of bf16), y 112 us (1.69), kDs 97 us (1.17: 1.5 GB through L2 at 15
-// TB/s and 0.35 GB of DRAM), the backward's group 310 us (1.83; 1.95 until its
-// tail).
+// PFLOP/s of bf16, the tensor pipe 84% busy), y 110 us (1.72), kDs 95 us (1.19),
+// the backward's group 308 us (1.84; 1.95 until its tail).  kDs's MMAs wait half
+// of their time for operands: six slices in flight, beside an epilogue that moves
+// 0.28 GB (0.35 GB of DRAM in 95 us, 1.4 GB through L2).
 #include <algorithm>
 #include <mutex>
 
