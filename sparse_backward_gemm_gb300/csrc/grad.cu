@@ -6,13 +6,13 @@
 // HBM-bound: the norm reads every value once; clipping needs the whole norm
 // before it writes the first value, so it reads a second time.
 //   Measured: the norm of 1.1 G f32 values (135 tensors, 4.4 GB) 604 us, 7.3 TB/s;
-// of 44 M 35 us (29 of them reading at 6 TB/s); of 492 K, in one cluster, 8.7 us.
+// of 44 M 35 us (29 of them reading at 6 TB/s); of 492 K 7.7 us.  (A set of up to
+// 4 MB in one launch, as a cluster of 16 CTAs with the partials in its shared
+// memory: 8.7 us, and 12 instead of 8 for clipping 2 MB: too few SMs read.)
 // Clipping them 1965 us (three passes at 6.7 TB/s) and 74 us, 88 from memory.
 #include <algorithm>
-#include <mutex>
 
 #include "internal.h"
-#include "tc_ptx.cuh"
 
 namespace collider {
 
@@ -22,6 +22,7 @@ constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 8;             // 16-byte vectors a thread has in flight
 constexpr int kGradChunk = kGradThreads * kGradVecs;   // vectors of a chunk: 32 KB
 constexpr int kGradTable = 1024;         // tensors of a launch (20 KB of its 32 KB of parameters)
+constexpr int kShortTable = 32;          // tensors of a short list
 constexpr int kGradBlocksPerSm = 4;
 constexpr size_t kGradKeep = 96 << 20;   // bytes that the norm leaves in L2 for the clipping pass (176 MB: 88 us, with none left 93)
 
@@ -119,11 +120,6 @@ __device__ __forceinline__ bool whole_vec(const Span& s, long long v) {
 // 1/64 of the f32 rate).  Where the largest magnitude leaves [2^-50, 2^60],
 // and squares of f32 could overflow or vanish, the same values are squared in
 // f64.
-// A block of kGradThreads threads (a quarter of a CTA in the small form below):
-// the thread's place in it, and its barrier
-__device__ __forceinline__ int block_thread() { return threadIdx.x & (kGradThreads - 1); }
-__device__ __forceinline__ void block_sync() { tc::named_bar(1 + threadIdx.x / kGradThreads, kGradThreads); }
-
 // The vectors of a chunk that this thread takes: v0 + thread + k * kGradThreads.
 // keep: what is loaded is read again soon (clipping).  Inside a tensor they are loaded without a question, all at once; only a
 // tensor's first and last chunk ask for each vector.
@@ -136,7 +132,7 @@ template <bool BF>
 __device__ __forceinline__ void load_chunk(const Span& s, long long v0, bool keep, uint4* u) {
   constexpr int per = BF ? 8 : 4;
   if (inner_chunk<BF>(s, v0)) {
-    const uint4* p = s.base + v0 + block_thread();
+    const uint4* p = s.base + v0 + threadIdx.x;
     if (keep) {
 #pragma unroll
       for (int k = 0; k < kGradVecs; ++k) u[k] = p[k * kGradThreads];
@@ -148,7 +144,7 @@ __device__ __forceinline__ void load_chunk(const Span& s, long long v0, bool kee
     const long long vend = (s.end + per - 1) / per;
 #pragma unroll
     for (int k = 0; k < kGradVecs; ++k) {
-      const long long v = v0 + block_thread() + k * kGradThreads;
+      const long long v = v0 + threadIdx.x + k * kGradThreads;
       u[k] = make_uint4(0, 0, 0, 0);
       if (v < vend) u[k] = whole_vec<BF>(s, v) ? s.base[v] : load_edge<BF>(s, v);
     }
@@ -211,13 +207,13 @@ __device__ __forceinline__ double max_nan(double a, double b) { return (a > b ||
 // warps that each reduced their own and then each other's values would take
 // eight times as long (3 us an SM with four blocks).
 __device__ __forceinline__ double block_reduce(double v, int max_kind, double* red) {
-  block_sync();
-  red[block_thread()] = v;
-  block_sync();
-  if (block_thread() < 32) {
+  __syncthreads();
+  red[threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
 #pragma unroll
     for (int i = 1; i < kGradThreads / 32; ++i) {
-      const double w = red[block_thread() + 32 * i];
+      const double w = red[threadIdx.x + 32 * i];
       v = max_kind ? max_nan(v, w) : v + w;
     }
 #pragma unroll
@@ -225,9 +221,9 @@ __device__ __forceinline__ double block_reduce(double v, int max_kind, double* r
       const double w = __shfl_xor_sync(0xffffffffu, v, o);
       v = max_kind ? max_nan(v, w) : v + w;
     }
-    if (block_thread() == 0) red[0] = v;
+    if (threadIdx.x == 0) red[0] = v;
   }
-  block_sync();
+  __syncthreads();
   return red[0];
 }
 
@@ -256,7 +252,7 @@ __device__ __forceinline__ void part_block(const Tab& t, int b, int blocks, int 
       c = kend;
       v = block_reduce(max_kind ? max_value(big) : sum, max_kind, red);
     }
-    if (block_thread() == 0) part[b + k] = v;
+    if (threadIdx.x == 0) part[b + k] = v;
   }
 }
 
@@ -269,7 +265,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
   part_block(t, blockIdx.x, gridDim.x, keep, max_kind, part, red);
 }
 
-// a partial, in global memory or in the cluster's shared memory
+// a partial that another kernel left (no copy of L1's)
 __device__ __forceinline__ double load_part(const double* p) { return *static_cast<const volatile double*>(p); }
 
 // the root of a sum, in f32 (a root of an f64 is about 1 us here) where the sum is well inside f32
@@ -304,7 +300,7 @@ __device__ __forceinline__ double tensor_norm(const Tab& t, int k, int blocks, i
 // the norm of everything, from all slots; every thread of the block gets it
 __device__ __forceinline__ float total_norm(const double* part, int slots, int max_kind, float scale, double* red) {
   double v = 0.0;
-  for (int i = block_thread(); i < slots; i += 4 * kGradThreads) {
+  for (int i = threadIdx.x; i < slots; i += 4 * kGradThreads) {
     double w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = i + j * kGradThreads < slots ? load_part(part + i + j * kGradThreads) : 0.0;
@@ -313,8 +309,8 @@ __device__ __forceinline__ float total_norm(const double* part, int slots, int m
   }
   v = block_reduce(v, max_kind, red);
   float* out = reinterpret_cast<float*>(red + 1);
-  if (block_thread() == 0) *out = (float)((max_kind ? v : root(v)) * (double)scale);
-  block_sync();
+  if (threadIdx.x == 0) *out = (float)((max_kind ? v : root(v)) * (double)scale);
+  __syncthreads();
   return *out;
 }
 
@@ -323,7 +319,7 @@ template <typename Tab>
 __device__ __forceinline__ void write_norms(const Tab& t, int b, int blocks, int max_kind, float scale, int part_blocks,
                                             const double* part, float* norms) {
   constexpr int warps = kGradThreads / 32;
-  for (int k = b * warps + (block_thread() >> 5); k < t.count; k += blocks * warps) {
+  for (int k = b * warps + (threadIdx.x >> 5); k < t.count; k += blocks * warps) {
     const double v = tensor_norm(t, k, part_blocks, max_kind, part);
     if ((threadIdx.x & 31) == 0) norms[k] = (float)(v * (double)scale);
   }
@@ -339,7 +335,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_finish_kernel(const __grid_
   if (norms) write_norms(t, blockIdx.x, gridDim.x, max_kind, scale, blocks, part, norms);
   if (blockIdx.x == gridDim.x - 1 && norm) {
     const float v = total_norm(all, slots, max_kind, scale, red);
-    if (block_thread() == 0) *norm = v;
+    if (threadIdx.x == 0) *norm = v;
   }
 }
 
@@ -360,7 +356,7 @@ __device__ __forceinline__ void scale_chunk(const Span& s, long long v0, float c
   uint4 u[kGradVecs];
   load_chunk<BF>(s, v0, false, u);
   if (inner_chunk<BF>(s, v0)) {
-    out += v0 + block_thread();
+    out += v0 + threadIdx.x;
 #pragma unroll
     for (int k = 0; k < kGradVecs; ++k) __stcs(out + k * kGradThreads, scaled<BF>(u[k], coef));
     return;
@@ -368,7 +364,7 @@ __device__ __forceinline__ void scale_chunk(const Span& s, long long v0, float c
   const long long vend = (s.end + per - 1) / per;
 #pragma unroll
   for (int k = 0; k < kGradVecs; ++k) {
-    const long long v = v0 + block_thread() + k * kGradThreads;
+    const long long v = v0 + threadIdx.x + k * kGradThreads;
     if (v >= vend) continue;
     const uint4 w = scaled<BF>(u[k], coef);
     if (whole_vec<BF>(s, v)) {
@@ -396,7 +392,7 @@ __device__ __forceinline__ void scale_block(const Tab& t, int b, int blocks, int
   const bool fine = isfinite(nv);
   const float clip = fminf(1.f, __fdiv_rn(max_norm, __fadd_rn(nv, 1e-6f)));
   const float coef = fine ? __fmul_rn(scale, clip) : 0.f;
-  if (b == 0 && block_thread() == 0) {
+  if (b == 0 && threadIdx.x == 0) {
     if (norm) *norm = nv;
     if (coef_out) *coef_out = coef;
   }
@@ -423,35 +419,6 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
   grid_dep_wait();
   scale_block(t, blockIdx.x, gridDim.x, max_kind, scale, max_norm, all, slots, norm, coef_out, red);
   if (norms) write_norms(t, blockIdx.x, gridDim.x, max_kind, scale, gridDim.x, part, norms);
-}
-
-// A small set in one launch: one cluster of 16 CTAs of four blocks each, whose
-// barrier stands between the partials, which lie in the first CTA's shared
-// memory, and what is made of them.
-constexpr int kSmallCtas = 16, kSmallPerCta = 4, kSmallBlocks = kSmallCtas * kSmallPerCta;
-constexpr int kSmallChunks = 128, kSmallTensors = 32;
-__global__ void __launch_bounds__(kGradThreads* kSmallPerCta)
-    grad_small_kernel(const __grid_constant__ GradTable<kSmallTensors> t, int blocks, int max_kind, int clip, float scale,
-                      float max_norm, float* norm, float* norms, float* coef_out) {
-  __shared__ double red_all[kSmallPerCta][kGradThreads];
-  __shared__ double part_all[kSmallBlocks + kSmallTensors];
-  grid_dep_wait();
-  tc::cluster_sync();   // the first CTA's shared memory is there
-  double* part = tc::peer_generic(part_all, 0);
-  const int b = blockIdx.x * kSmallPerCta + threadIdx.x / kGradThreads;
-  double* red = red_all[threadIdx.x / kGradThreads];
-  if (b < blocks) part_block(t, b, blocks, 1 << 28, max_kind, part, red);
-  tc::cluster_sync();
-  const int slots = blocks + t.count;
-  if (clip) {
-    if (b < blocks) scale_block(t, b, blocks, max_kind, scale, max_norm, part, slots, norm, coef_out, red);
-  } else if (b == 0 && norm) {
-    const float v = total_norm(part, slots, max_kind, scale, red);
-    if (block_thread() == 0) *norm = v;
-  }
-  // (the other CTAs' warps first: block 0 has the total to do)
-  if (norms) write_norms(t, kSmallBlocks - 1 - b, kSmallBlocks, max_kind, scale, blocks, part, norms);
-  tc::cluster_sync();   // the first CTA stays until its partials are read
 }
 
 int chunks_of(const GradItem& g) {
@@ -517,49 +484,7 @@ size_t grad_part_doubles(int count) {
   return pieces * kGradMaxBlocks + (size_t)(count < 0 ? 0 : count);
 }
 
-// whether the device takes a cluster of kSmallCtas CTAs of the small form
-static bool small_fits() {
-  static std::mutex mu;
-  static signed char known[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  std::lock_guard<std::mutex> lk(mu);
-  if (!known[dev]) {
-    auto k = grad_small_kernel;
-    int n = 0;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kSmallCtas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(kSmallCtas);
-    cfg.blockDim = dim3(kGradThreads * kSmallPerCta);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const bool ok = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                    cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0;
-    if (!ok) cudaGetLastError();
-    known[dev] = ok ? 1 : -1;
-  }
-  return known[dev] > 0;
-}
-
 cudaError_t launch_grad(const Ctx& c, const GradJob& j) {
-  if (j.count <= kSmallTensors && small_fits()) {
-    long long chunks = 0;
-    for (int i = 0; i < j.count; ++i) chunks += chunks_of(j.items[i]);
-    if (chunks <= kSmallChunks) {
-      GradTable<kSmallTensors> t;
-      fill(&t, j.items, j.count);
-      const int blocks = t.chunks < 1 ? 1 : t.chunks < kSmallBlocks ? t.chunks : kSmallBlocks;
-      prof_begin(c, "grad_small");
-      const cudaError_t e = launch_k(c, false, grad_small_kernel, dim3(kSmallCtas), dim3(kGradThreads * kSmallPerCta), 0,
-                                     kSmallCtas, t, blocks, j.max_kind, j.clip, j.scale, j.max_norm, j.norm, j.norms, j.coef);
-      prof_end(c);
-      count_launch();
-      return launched(e);
-    }
-  }
   const int pieces = j.count <= 0 ? 1 : (j.count + kGradTable - 1) / kGradTable;
   if (c.num_sms * kGradBlocksPerSm > kGradMaxBlocks) return cudaErrorNotSupported;
   int slots = 0;
@@ -570,7 +495,7 @@ cudaError_t launch_grad(const Ctx& c, const GradJob& j) {
       int used = 0;
       float* norms = j.norms ? j.norms + i0 : nullptr;
       // (a short list's table is a few hundred bytes of parameters instead of 20 KB)
-      const cudaError_t e = n <= kSmallTensors ? run_piece<kSmallTensors>(c, j, stage, j.items + i0, n, j.part + at, &used, slots, norms, p == 0)
+      const cudaError_t e = n <= kShortTable ? run_piece<kShortTable>(c, j, stage, j.items + i0, n, j.part + at, &used, slots, norms, p == 0)
                                     : run_piece<kGradTable>(c, j, stage, j.items + i0, n, j.part + at, &used, slots, norms, p == 0);
       if (e != cudaSuccess) return e;
       at += used;

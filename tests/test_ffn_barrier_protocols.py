@@ -1,5 +1,5 @@
 """Models of the barrier protocols of the feed-forward kernels (sparse_backward_gemm_gb300/csrc/ffn_tc.cu, ffn_few.cu),
-checked on the CPU with the checker of test_barrier_protocols.py: no deadlock, no missed phase, no early arrival."""
+checked on the CPU as in test_barrier_protocols.py: no deadlock, no missed phase, no early arrival."""
 import pytest
 
 from test_barrier_protocols import check, ring
