@@ -10,10 +10,8 @@
 //           y alone): their tiles form one list, whose tail is cut evenly.
 // All three are 2-SM kernels: a pair of CTAs works on a 256 x 256 tile, TMA
 // feeds a ring of 64-deep k-slices, one thread issues the MMAs into one of two
-// accumulators while the epilogue's warps empty the other.  In long lists two
-// pairs form a cluster and stand side by side on a 256 x 512 tile: each of its
-// CTAs loads half of the 128 rows it shares with one of the other pair and
-// multicasts it to both.  Every wait is bounded.
+// accumulators while the epilogue's warps empty the other.  Each CTA loads its own
+// rows and its own half of the columns.  Every wait is bounded.
 //   Measured at 8192 x 2048 x 5632, 40% filtered (4916 kept): kUp 200 us (1.89
 // PFLOP/s of bf16, the tensor pipe 84% busy), y 110 us (1.72), kDs 95 us (1.19),
 // the backward's group 308 us (1.84; 1.95 until its tail).  kDs's MMAs wait half
@@ -70,8 +68,8 @@ struct Params {
   FfnProduct p[3];
   int np;
   uint32_t by_pairs;  // 2^32 / pairs, rounded up
-  float* partial;     // [2 * pairs][2][NB / 4][kBM][4] f32 (with two pairs to a cluster: [2 * clusters][4]...)
-  int* counters;      // [kMaxTail][CTAs of a cluster], zero on entry and left zero
+  float* partial;     // [2 * pairs][2][NB / 4][kBM][4] f32
+  int* counters;      // [kMaxTail][2], zero on entry and left zero
   DevStatus* st;
 };
 
@@ -109,18 +107,15 @@ __device__ __forceinline__ int count_mod(int a, int b, int w, uint32_t magic) {
 
 struct Tile {
   int p, k0, k1;
-  int m0, n0;     // this CTA's first row, the tile's place among the columns of tiles
+  int m0, n0;     // this CTA's first row, the tile's column of tiles
   int t;
   bool whole;
 };
-// NP pairs of a cluster, which stand side by side: pair `pr` has the tile's
-// column NP n + pr
-template <int NP>
-__device__ __forceinline__ void place(int units, int n_tiles, int t, int rank, int pr, int* m0, int* n0) {
+__device__ __forceinline__ void place(int units, int n_tiles, int t, int rank, int* m0, int* n0) {
   const int per = kGroupRows * n_tiles, g = t / per, r = t % per;
   const int gm = min(kGroupRows, units - g * kGroupRows);
   *m0 = (2 * (g * kGroupRows + r % gm) + rank) * kBM;
-  *n0 = r / gm * NP + pr;
+  *n0 = r / gm;
 }
 
 // the pair's pieces of work in order
@@ -133,8 +128,7 @@ struct Iter {
       end = s.begin[s.wid + 1];
     }
   }
-  template <int NP>
-  __device__ bool next(int rank, int pr, Tile* o) {
+  __device__ bool next(int rank, Tile* o) {
     if (tile < s.dp) {
       o->t = tile;
       tile += s.W;
@@ -153,7 +147,7 @@ struct Iter {
       it += o->k1 - o->k0;
     }
     o->whole = o->k0 == 0 && o->k1 == s.kb[o->p];
-    place<NP>(s.units[o->p], s.tiles[o->p] / s.units[o->p], o->t - s.first[o->p], rank, pr, &o->m0, &o->n0);
+    place(s.units[o->p], s.tiles[o->p] / s.units[o->p], o->t - s.first[o->p], rank, &o->m0, &o->n0);
     return true;
   }
 };
@@ -235,7 +229,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-template <int EPI, int ACT, int NP, int NB>
+template <int EPI, int ACT, int NB>
 __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using C = Cfg<EPI, NB>;
@@ -256,7 +250,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, NP);   // (every pair's MMAs: the rows' operand goes to all of them)
+      mbar_init(empty0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
@@ -277,9 +271,8 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
   // of this one have started) and set itself up: the kept count is none of its
   // predecessors' in the call, the first of which was launched behind all before.
   if (EPI != kGroup) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int crank = static_cast<int>(cluster_ctarank()), rank = crank & 1, pr = crank >> 1;   // in the cluster, in the pair; the pair
-  const int leader_cta = crank & ~1;
-  const int W = gridDim.x / (2 * NP), wid = blockIdx.x / (2 * NP);
+  const int rank = static_cast<int>(cluster_ctarank());   // in the pair
+  const int W = gridDim.x / 2, wid = blockIdx.x / 2;
   int n = p.M;
   if (p.n_kept) n = min(p.M, max(0, *p.n_kept));
 
@@ -298,7 +291,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
       const FfnProduct& q = p.p[i];
       const int m = q.dyn == 1 ? min(q.M, n) : q.M, k = q.dyn == 2 ? min(q.K, n) : q.K;
       sc.units[i] = (m + 2 * kBM - 1) / (2 * kBM);
-      sc.tiles[i] = sc.units[i] * ((q.N + NP * NB - 1) / (NP * NB));
+      sc.tiles[i] = sc.units[i] * ((q.N + NB - 1) / NB);
       sc.kb[i] = (k + kBK - 1) / kBK;
       total += sc.tiles[i];
       slices += (long long)sc.tiles[i] * sc.kb[i];
@@ -383,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
   } else {
     sc.np = 1;
     sc.units[0] = (n + 2 * kBM - 1) / (2 * kBM);
-    constexpr int cols = NP * (EPI == kUp ? NB / 2 : NB);
+    constexpr int cols = EPI == kUp ? NB / 2 : NB;
     sc.tiles[0] = sc.units[0] * ((p.F + cols - 1) / cols);
     sc.kb[0] = p.kb;
     sc.first[0] = 0;
@@ -420,9 +413,9 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
     uint32_t phase = 0, armed = 0, armed_parity = 0;   // stages with copies issued, and the phase parity armed
     Iter iter(sc);
     Tile t;
-    bool more = iter.next<NP>(rank, pr, &t);
+    bool more = iter.next(rank, &t);
     grid_dep_wait();
-    for (; more && !aborted(); more = iter.next<NP>(rank, pr, &t)) {
+    for (; more && !aborted(); more = iter.next(rank, &t)) {
       const CUtensorMap* ma = &maps.m[EPI == kGroup ? 2 * t.p : 0];
       const CUtensorMap* mb = ma + 1;
       const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
@@ -438,12 +431,8 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
           const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
           const int kx = kb * kBK;
           if (rank == 0) mbar_expect_tx(fb, 2 * kStageBytes);   // both CTAs' copies are counted on the even CTA's barrier
-          const uint32_t lb = map_to_rank(fb, leader_cta);
-          if (NP == 2) {
-            // the two CTAs of the cluster with these rows load a half each, for both
-            const uint16_t both = static_cast<uint16_t>(5u << rank);
-            tma_load_2d_pair_mc(sa + pr * 8192, ma, lb, both, a_mn ? t.m0 + 64 * pr : kx, a_mn ? kx : t.m0 + 64 * pr);
-          } else if (!a_mn) {
+          const uint32_t lb = map_to_rank(fb, 0);
+          if (!a_mn) {
             tma_load_2d_pair(sa, ma, lb, kx, t.m0);
           } else {
             tma_load_2d_pair(sa, ma, lb, t.m0, kx);
@@ -462,7 +451,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
       if (!ok) break;
     }
     if (!aborted()) {
-      // both MMAs release every stage (their commits land in this CTA's empty
+      // the MMAs release every stage (their commits land in this CTA's empty
       // barriers) before this CTA may leave the cluster
       for (int i = 0; i < S; ++i) {
         if (!wait(empty0 + 8 * stage, phase ^ 1u, 5)) break;
@@ -491,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
       int seg = 0;
       Iter iter(sc);
       Tile t;
-      while (iter.next<NP>(rank, pr, &t) && !__any_sync(0xffffffffu, *abort_flag != 0)) {
+      while (iter.next(rank, &t) && !__any_sync(0xffffffffu, *abort_flag != 0)) {
         const bool a_mn = EPI == kGroup ? p.p[t.p].a_mn != 0 : false, b_mn = EPI == kGroup ? p.p[t.p].b_mn != 0 : EPI == kUp;
         const uint32_t idesc = idesc_bf16(2 * kBM, NB, a_mn, b_mn);
         const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32, a_lbo = a_mn ? 8192 : 16, b_lbo = b_mn ? 8192 : 16;
@@ -509,20 +498,20 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
             for (int kk = 0; kk < kBK / 16; ++kk)
               mma_bf16_pair(d, sdesc(sa + kk * a_step, a_lbo, 1024), sdesc(sb + kk * b_step, b_lbo, 1024), idesc,
                             (kb > t.k0) || (kk > 0));
-            mma_commit_pair_mc(empty0 + 8 * stage, NP == 2 ? 0xf : 3);
+            mma_commit_pair_mc(empty0 + 8 * stage, 3);
           }
           __syncwarp();
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        if (leader) mma_commit_pair_mc(tfull0 + 8 * acc, static_cast<uint16_t>(3u << leader_cta));
+        if (leader) mma_commit_pair_mc(tfull0 + 8 * acc, 3);
         __syncwarp();
         ++seg;
       }
     }
   } else {
     // ---------------- epilogue (warps 2...) ----------------
-    auto release_acc = [&](int acc) { mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8 * acc, leader_cta)); };
+    auto release_acc = [&](int acc) { mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8 * acc, 0)); };
     volatile int no_abort = 0;   // (timeout-only waits: the threads leave together)
     const int q = warp & 3;      // TMEM lane quadrant this warp may access
     const int half = (warp - 2) >> 2;   // its share of the columns: of kUp a quarter of NB of g and of u, of kDs a quarter, else half
@@ -531,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
     Iter iter(sc);
     Tile t;
     if constexpr (EPI == kUp) {
-      while (iter.next<NP>(rank, pr, &t)) {
+      while (iter.next(rank, &t)) {
         const int acc = seg & 1;
         const int row = t.m0 + rl;
         const Rows4 up_rows(row < n ? row * p.up_ld : -1), s_rows(row < n ? (long long)row * p.F : -1);
@@ -581,7 +570,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
       int chunk = 0;
       int src[2];
       auto next_rows = [&] {
-        copying = ahead.next<NP>(rank, pr, &ct);
+        copying = ahead.next(rank, &ct);
         chunk = 0;
         if (!copying) return;
 #pragma unroll
@@ -608,7 +597,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
       };
       next_rows();
       copy();
-      while (iter.next<NP>(rank, pr, &t)) {
+      while (iter.next(rank, &t)) {
         const int acc = seg & 1;
         const int row = t.m0 + rl;
         // where this lane's stores go: piece (lane & 1) of rows (lane & ~1) + i
@@ -683,7 +672,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
     } else {
       constexpr int kHalf = NB / 2;   // columns of a warp
       grid_dep_wait();
-      while (iter.next<NP>(rank, pr, &t)) {
+      while (iter.next(rank, &t)) {
         const FfnProduct& pr = p.p[t.p];
         const int acc = seg & 1;
         const int M = pr.dyn == 1 ? min(pr.M, n) : pr.M;
@@ -721,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
           // comes last finishes the tile.  Whoever came has no other tile to
           // wait for, so the last may wait for the others' parts, whichever
           // kernels hold the other SMs.
-          ctr = p.counters + (t.t - sc.dp) * 2 * NP + crank;
+          ctr = p.counters + (t.t - sc.dp) * 2 + rank;
           if (threadIdx.x == 64) {
             int parts = 0;
             for (int w = c_first; w <= c_last; ++w) parts += begin[w] < begin[w + 1];
@@ -751,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
           // begins in, in place 1 of the tile it ends in.
           auto slot_of = [&](int w) {
             const int at = 2 * w + (begin[w] >= x0 && begin[w] < x1 ? 0 : 1);
-            return p.partial + ((long long)at * 2 * NP + crank) * (kBM * NB);
+            return p.partial + ((long long)at * 2 + rank) * (kBM * NB);
           };
           named_bar(1, 32 * kEpiWarps);
           const int parts = *last_flag;
@@ -848,15 +837,15 @@ __global__ void __launch_bounds__(Cfg<EPI, NB>::kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // host side
-template <int EPI, int ACT, int NP, int NB>
+template <int EPI, int ACT, int NB>
 cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, long long tiles, long long m, long long n,
-                   long long k, int dyn) {   // tiles: of a pair
-  auto kern = ffn_kernel<EPI, ACT, NP, NB>;
+                   long long k, int dyn) {
+  auto kern = ffn_kernel<EPI, ACT, NB>;
   constexpr size_t smem = Cfg<EPI, NB>::kSmem;
   // per device, once: the shared-memory opt-in, and how many pairs run at once
   static std::mutex mu;
   static int known[64] = {0};
-  int dev = 0, fit = 0;   // clusters
+  int dev = 0, fit = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   {
@@ -868,26 +857,26 @@ cudaError_t launch(const Ctx& c, const char* name, const Maps& maps, Params p, l
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2 * NP;
+      attr[0].val.clusterDim.x = 2;
       attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(2 * NP * (c.num_sms / (2 * NP)));
+      cfg.gridDim = dim3(c.num_sms / 2 * 2);
       cfg.blockDim = dim3(Cfg<EPI, NB>::kThreads);
       cfg.dynamicSmemBytes = smem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
       if (e != cudaSuccess) return e;
-      fit = std::min({fit, c.num_sms / (2 * NP), kMaxWorkers / NP});
+      fit = std::min({fit, c.num_sms / 2, kMaxWorkers});
       if (fit < 1) return cudaErrorNotSupported;
       if (dev >= 0 && dev < 64) known[dev] = fit;
     }
   }
-  // (a group's tail may go to every cluster)
-  const int workers = EPI == kGroup ? fit : (int)std::max(1ll, std::min<long long>((tiles + NP - 1) / NP, fit));
+  // (a group's tail may go to every pair)
+  const int workers = EPI == kGroup ? fit : (int)std::max(1ll, std::min<long long>(tiles, fit));
   p.by_pairs = (uint32_t)(((1ull << 32) + workers - 1) / workers);
   if (workers < 2) p.partial = nullptr;   // (nobody to share with; 2^32 / 1 does not fit)
   prof_begin(c, name, m, n, k, dyn);
-  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(2 * NP * workers), dim3(Cfg<EPI, NB>::kThreads), smem, 2 * NP, maps, p);
+  e = launch_k(c, pdl_allowed() && c.pdl, kern, dim3(2 * workers), dim3(Cfg<EPI, NB>::kThreads), smem, 2, maps, p);
   prof_end(c);
   count_launch();
   return launched(e);
@@ -902,26 +891,14 @@ bool mn_major(CUtensorMap* m, const void* p, long long inner, long long rows, lo
 
 }  // namespace
 
-// The form of a list of so many 256 x 256 tiles.
-//   Two waves or more: two pairs to a cluster load the rows' operand once for
-// both, so a quarter less comes through L2.  One pair and two, us: backward 2403
-// x 1536 x 8960 272-290 and 265-267, 1229 x 2048 x 5632 139 and 136.5; in a loop
-// of seconds, under the power limit, 8192 x 2048 x 5632 forward 363 and 360, 4916
-// rows backward 484 and 482 (alone 427 and 431).  Below, the wider tiles fill the
-// SMs worse: 800 x 1024 x 2816 57 and 61.
-//   At most a quarter of a wave of SMs: tiles of 128 columns, so that twice the SMs
-// share the epilogues.
-enum class Form { kNarrow, kPair, kPairs };
-static Form form_of(const Ctx& c, long long tiles) {
-  return tiles >= c.num_sms ? Form::kPairs : 4 * tiles <= c.num_sms ? Form::kNarrow : Form::kPair;
-}
-static int rows_box(Form f) { return f == Form::kPairs ? 64 : 128; }       // of the rows' operand, K-major
-static int cols_box(Form f) { return f == Form::kNarrow ? 64 : 128; }      // of the columns'
+// The form of a list of so many 256 x 256 tiles: at most a quarter of a wave of
+// SMs takes tiles of 128 columns, so that twice the SMs share the epilogues.
+enum class Form { kNarrow, kPair };
+static Form form_of(const Ctx& c, long long tiles) { return 4 * tiles <= c.num_sms ? Form::kNarrow : Form::kPair; }
+static int cols_box(Form f) { return f == Form::kNarrow ? 64 : 128; }   // of the columns' operand, K-major
 template <int EPI, int ACT, typename... A>
 static cudaError_t launch_form(Form f, A... args) {
-  return f == Form::kPairs    ? launch<EPI, ACT, 2, 256>(args...)
-         : f == Form::kNarrow ? launch<EPI, ACT, 1, 128>(args...)
-                              : launch<EPI, ACT, 1, 256>(args...);
+  return f == Form::kNarrow ? launch<EPI, ACT, 128>(args...) : launch<EPI, ACT, 256>(args...);
 }
 static long long tiles_of(Form f, long long m, long long n) {
   const int nb = f == Form::kNarrow ? 128 : 256;
@@ -934,12 +911,12 @@ size_t ffn_partial_floats(long long tiles) {
   return (size_t)(2 * std::min<long long>(kMaxWorkers, kMaxParts * tiles) * 2) * kBM * 256;
 }
 long long ffn_tiles(long long m, long long n) { return tiles_of(Form::kPair, m, n); }
-int ffn_counters() { return 4 * kMaxTail; }
+int ffn_counters() { return 2 * kMaxTail; }
 
 cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
   Maps maps{};
   const Form f = form_of(c, ffn_tiles(a.M, 2ll * a.F));
-  if (!k_major(&maps.m[0], a.x, a.D, a.M, a.x_ld, rows_box(f)) || !mn_major(&maps.m[1], a.w_up, 2ll * a.F, a.D, 2ll * a.F))
+  if (!k_major(&maps.m[0], a.x, a.D, a.M, a.x_ld, kBM) || !mn_major(&maps.m[1], a.w_up, 2ll * a.F, a.D, 2ll * a.F))
     return cudaErrorInvalidValue;
   Params p{};
   p.M = a.M; p.F = a.F; p.kb = (a.D + kBK - 1) / kBK;
@@ -954,7 +931,7 @@ cudaError_t launch_ffn_up(const Ctx& c, const FfnUp& a) {
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a) {
   Maps maps{};
   const Form f = form_of(c, ffn_tiles(a.M, a.F));
-  if (!k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld, rows_box(f)) ||
+  if (!k_major(&maps.m[0], a.dy, a.D, a.dy_rows, a.dy_ld, kBM) ||
       !k_major(&maps.m[1], a.w_down, a.D, a.F, a.D, cols_box(f)))
     return cudaErrorInvalidValue;
   Params p{};
@@ -979,7 +956,7 @@ cudaError_t launch_ffn_group(const Ctx& c, const FfnProduct* q, int np, int M, c
   const Form f = form_of(c, tiles);
   for (int i = 0; i < np; ++i) {
     const bool a_ok = q[i].a_mn ? mn_major(&maps.m[2 * i], q[i].A, q[i].M, q[i].a_rows, q[i].lda)
-                                : k_major(&maps.m[2 * i], q[i].A, q[i].K, q[i].a_rows, q[i].lda, rows_box(f));
+                                : k_major(&maps.m[2 * i], q[i].A, q[i].K, q[i].a_rows, q[i].lda, kBM);
     const bool b_ok = q[i].b_mn ? mn_major(&maps.m[2 * i + 1], q[i].B, q[i].N, q[i].b_rows, q[i].ldb)
                                 : k_major(&maps.m[2 * i + 1], q[i].B, q[i].K, q[i].b_rows, q[i].ldb, cols_box(f));
     if (!a_ok || !b_ok) return cudaErrorInvalidValue;

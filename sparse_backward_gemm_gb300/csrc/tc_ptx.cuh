@@ -80,17 +80,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
-// The same copy into the shared memory of every CTA of the cluster in cta_mask,
-// at this offset; in each it is counted on the barrier at bar's offset in the
-// even CTA of its pair (bar: an even CTA's).
-__device__ __forceinline__ void tma_load_2d_pair_mc(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint16_t cta_mask, int x,
-                                                    int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
-      " [%0], [%1, {%4, %5}], [%2], %3;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "h"(cta_mask), "r"(x), "r"(y)
-      : "memory");
-}
 // the shared::cluster address of this CTA's shared location `a` in CTA `rank`
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t a, uint32_t rank) {
   uint32_t r;
