@@ -42,7 +42,9 @@ __device__ __forceinline__ void glu_both(float g, float* a, float* da) {
     *da = p * fmaf(g, 1.f - p, 1.f);
   } else {
     constexpr float c2 = 2.f * 0.7978845608028654f, k3 = 3.f * 0.044715f;
-    *da = fmaf(*a * (1.f - p), c2 * fmaf(k3 * g, g, 1.f), p);
+    // (|g| up to 64: from 20 on p is 0 or 1 and the term 0, and its square must not become an infinity)
+    const float h = fminf(fabsf(g), 64.f);
+    *da = fmaf(*a * (1.f - p), c2 * fmaf(k3 * h, h, 1.f), p);
   }
 }
 
