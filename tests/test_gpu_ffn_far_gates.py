@@ -55,3 +55,14 @@ def test_far_gates(kind, far):
     v["dy"] *= 2.0 ** -10                        # (and du = ds g)
     v["w_up"][:, F + 5] = v["w_up"][:, F + 129] = 0.0
     check(v, kind)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+def test_a_slope_of_0_beside_a_large_product(kind):
+    """ds u beyond f32 where the slope is 0: the gate's gradient is 0, not 0 times infinity."""
+    M, D, F = 20, 64, 64
+    v = t.inputs(M, D, F, 32)
+    big = 2.0 ** 70
+    v["dy"][7] *= big
+    v["up"][7, 9], v["up"][7, F + 9] = -200.0, big
+    check(v, kind)
