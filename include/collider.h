@@ -688,9 +688,10 @@ typedef struct {
 /* norm[0] = scale (sum of g^2 over all gradients)^(1/2), or scale max |g|
  * (kind); norms[i] (may be NULL, as may norm): the same of gradient i alone; f32, device.
  * scale (finite, > 0) stands for what the gradients are still to be multiplied
- * by, such as one over the number of summed micro-batches.  Sums are held in
- * f64, and squares too where f32's would overflow or vanish: the norm is finite
- * wherever it fits f32.  A NaN gives NaN.  Bit-identical from run to run.
+ * by, such as one over the number of summed micro-batches.  Squares are added at
+ * most 16 at a time in f32 and those sums in f64 (the squares too where f32's would
+ * overflow or vanish); the root and its product with scale are rounded to f32 once:
+ * within 10 2^-24, and finite wherever it fits f32.  A NaN gives NaN.  Bit-identical from run to run.
  * grads is a host array of count (0 <= count <= 2^20) gradients, read during
  * the call only; at most 2^40 values in all.  A gradient listed twice counts
  * twice.  Workspace: collider_grad_norm_workspace_size(). */

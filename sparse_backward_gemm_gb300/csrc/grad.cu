@@ -268,9 +268,13 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
 // a partial that another kernel left (no copy of L1's)
 __device__ __forceinline__ double load_part(const double* p) { return *static_cast<const volatile double*>(p); }
 
-// the root of a sum, in f32 (a root of an f64 is about 1 us here) where the sum is well inside f32
+// The root of a sum.  sqrt of an f64 costs about 1 us here; where the sum is
+// well inside f32, its root r there (off by 2^-24) and one step of Newton's
+// method in f64, r + (v - r^2) / (2 r), whose quotient may be an f32: off by 2^-46.
 __device__ __forceinline__ double root(double v) {
-  return v > 1e-30 && v < 1e30 ? (double)__fsqrt_rn((float)v) : sqrt(v);
+  if (!(v > 1e-30 && v < 1e30)) return sqrt(v);
+  const float r = __fsqrt_rn((float)v);
+  return fma(fma(-(double)r, (double)r, v), (double)__fdividef(0.5f, r), (double)r);
 }
 
 // tensor k's norm (before scale) from the partials of the blocks that met it; by one warp
