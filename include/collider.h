@@ -644,7 +644,7 @@ typedef struct {
 /* All M rows (the forward stays dense).  up [M, 2F] = [g | u] is what the
  * backward reads; NULL: not kept.  g and u are f32 until s is formed; s is
  * rounded to bf16 for the second product, which the tensor cores take in bf16
- * (of up to 32 tokens to the sum of two bf16 values), and each output is
+ * (of up to 64 tokens to the sum of two bf16 values), and each output is
  * rounded once.  The outputs overlap each other and the
  * inputs nowhere.  Workspace: collider_ffn_fwd_workspace_size(). */
 size_t collider_ffn_fwd_workspace_size(const collider_ffn_desc* desc);

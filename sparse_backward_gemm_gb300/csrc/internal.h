@@ -457,16 +457,16 @@ struct FfnDs {
   int* counters;
 };
 cudaError_t launch_ffn_ds(const Ctx& c, const FfnDs& a);
-// up (may be null), s and y of few tokens (ffn_few.cu).  Few: what its kernels
-// are the faster at.  Theirs and those of 256-row tiles, us: 48 and 64 tokens x
+// up (may be null), s and y of few tokens (ffn_few.cu): up to 64, where s is kept
+// as two bf16 values, [2 M, F], whatever the weights' sizes, and to 128 where its
+// kernels are the faster.  Theirs and those of 256-row tiles, us: 48 and 64 tokens x
 // 256 x 384 13.5, 14.6 and 12.8, 12.5, x 512 x 1408 14.7, 16.0 and 17; 96 and 128
 // tokens x 768 x 2048 18.8, 20.7 and 19.5, x 1024 x 2816 19.0, 20.9 and 23.5, x
 // 2048 x 5632 33.3, 35.7 and 37.5; 24 tokens 11 to 25 and 13 to 37.
+constexpr int kFfnSplit = 64;
 inline bool ffn_few(int M, int D, int F) {
-  const long long w = (long long)D * F;
-  return M <= 32 || (M <= 64 && w >= 1 << 18) || (M <= 128 && w >= 1 << 21);
+  return M <= kFfnSplit || (M <= 128 && (long long)D * F >= 1 << 21);
 }
-constexpr int kFfnSplit = 64;   // up to so many tokens s has [2 M, F] there: two bf16 values of each
 struct FfnFew {
   int act, M, D, F;
   const void* x; long long x_ld;
