@@ -509,11 +509,18 @@ def collider_grad_norm_workspace_size(grads, count) -> int:
     return lib().collider_grad_norm_workspace_size(grads, count)
 
 
+def _listed(grads, count):
+    if isinstance(grads, C.Array) and count > len(grads):
+        raise ColliderError(ERR_INVALID_ARG, f"a count of {count} gradients beyond a list of {len(grads)}")
+
+
 def collider_grad_norm(grads, count, kind, scale, norm, norms, ws, stream=None) -> None:
+    _listed(grads, count)
     _check(lib().collider_grad_norm(grads, count, kind, scale, _ptr(norm), _ptr(norms), _ptr(ws), _nbytes(ws),
                                     _stream(stream)))
 
 
 def collider_grad_clip(grads, count, kind, scale, max_norm, norm, norms, coef, ws, stream=None) -> None:
+    _listed(grads, count)
     _check(lib().collider_grad_clip(grads, count, kind, scale, max_norm, _ptr(norm), _ptr(norms), _ptr(coef), _ptr(ws),
                                     _nbytes(ws), _stream(stream)))
