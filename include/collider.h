@@ -659,12 +659,13 @@ collider_status collider_ffn_fwd(const collider_ffn_desc* desc, const void* x, c
  * products; ds stays f32.  So f32 weight gradients carry the rounding of bf16
  * factors too.  saved_rows: x and up hold M (FULL, read through idx) or n_kept
  * (COMPACT) rows; dy_rows and dx_rows likewise; the filtered rows of a FULL dx
- * are written 0.  idx (ascending) and n_kept both NULL: every token is kept.
- * dx NULL, dw_up NULL, dw_down NULL: not wanted (x may then be NULL without
- * dw_up, w_up without dx).  Outputs are overwritten, and overlap each other and
- * the inputs nowhere.  Every sum has a fixed order: bit-identical from run to
- * run.  A kept index outside the tokens is reported by collider_check; its row
- * counts as zeros.  Workspace: collider_ffn_bwd_workspace_size(). */
+ * are written 0.  idx (ascending, a token once) and n_kept both NULL: every
+ * token is kept.  dx NULL, dw_up NULL, dw_down NULL: not wanted (x may then be
+ * NULL without dw_up, w_up without dx); with dw_up or dw_down, M is at most
+ * 2^27.  Outputs are overwritten, and overlap each other and the inputs
+ * nowhere.  Every sum has a fixed order: bit-identical from run to run.  A kept
+ * index outside the tokens is reported by collider_check; its row counts as
+ * zeros.  Workspace: collider_ffn_bwd_workspace_size(). */
 size_t collider_ffn_bwd_workspace_size(const collider_ffn_desc* desc);
 collider_status collider_ffn_bwd(const collider_ffn_desc* desc, const void* w_up, const void* w_down,
                                  const void* x, const void* up, collider_rows saved_rows, const void* dy,

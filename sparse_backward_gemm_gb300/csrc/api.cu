@@ -2080,6 +2080,10 @@ extern "C" collider_status collider_ffn_bwd(const collider_ffn_desc* d, const vo
     if (!al16(p)) return fail(COLLIDER_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
   if (!al4({idx, n_kept})) return fail(COLLIDER_ERR_INVALID_ARG, "%s: a misaligned index", fn);
   const int M = d->M, D = d->D, F = d->F, gsz = d->grad_dtype == COLLIDER_F32 ? 4 : 2;
+  // (one pair of CTAs may add all rows of a weight gradient: 2^21 k-slices of up
+  // to 0.3 us, and its epilogue waits kWaitBudgetNs, 2 s, for them)
+  if ((dw_up || dw_down) && M > (1 << 27))
+    return fail(COLLIDER_ERR_UNSUPPORTED, "%s: weight gradients of at most 2^27 tokens", fn);
   const bool kept = idx != nullptr;
   // (of COMPACT rows, whose number the host does not know, the first)
   auto rows = [&](collider_rows r) { return kept && r == COLLIDER_ROWS_COMPACT ? 1 : M; };
