@@ -113,16 +113,10 @@ __device__ __forceinline__ bool whole_vec(const Span& s, long long v) {
   return v * per >= s.lead && (v + 1) * per <= s.end;
 }
 
-// Adds a thread's values of one chunk to its sum of squares (in f64), or takes
-// its largest magnitude (as the bits of |v|: a NaN is above infinity).
-// Squares are added in f32, at most 64 of them, and the sum in f64: one f64
-// operation a chunk and thread (an f64 multiply-add a value would bind, at
-// 1/64 of the f32 rate).  Where the largest magnitude leaves [2^-50, 2^60],
-// and squares of f32 could overflow or vanish, the same values are squared in
-// f64.
 // The vectors of a chunk that this thread takes: v0 + thread + k * kGradThreads.
-// keep: what is loaded is read again soon (clipping).  Inside a tensor they are loaded without a question, all at once; only a
-// tensor's first and last chunk ask for each vector.
+// keep: what is loaded is read again soon (clipping).  Inside a tensor they are
+// loaded without a question, all at once; only a tensor's first and last chunk
+// ask for each vector.
 template <bool BF>
 __device__ __forceinline__ bool inner_chunk(const Span& s, long long v0) {
   constexpr int per = BF ? 8 : 4;
