@@ -12,11 +12,11 @@
 // feeds a ring of 64-deep k-slices, one thread issues the MMAs into one of two
 // accumulators while the epilogue's warps empty the other.  Each CTA loads its own
 // rows and its own half of the columns.  Every wait is bounded.
-//   Measured at 8192 x 2048 x 5632, 40% filtered (4916 kept): kUp 200 us (1.89
-// PFLOP/s of bf16, the tensor pipe 84% busy), y 110 us (1.72), kDs 95 us (1.19),
-// the backward's group 308 us (1.84; 1.95 until its tail).  kDs's MMAs wait half
-// of their time for operands: six slices in flight, beside an epilogue that moves
-// 0.28 GB (0.35 GB of DRAM in 95 us, 1.4 GB through L2).
+//   Measured at 8192 x 2048 x 5632, 40% filtered (4916 kept), from memory: kUp 202
+// us (1.87 PFLOP/s of bf16, the tensor pipe 84% busy), y 110 us (1.72), kDs 100 us
+// (1.14), the backward's group 315 us (1.80).  kDs's MMAs wait half of their time
+// for operands: six slices in flight, beside an epilogue that moves 0.28 GB (0.35
+// GB of DRAM in 100 us, 1.5 GB through L2).
 #include <algorithm>
 #include <mutex>
 
@@ -87,8 +87,8 @@ struct Params {
 // and 8 for every part but one (6.6 us with two pairs to a tile, 11.4 with four).
 // So of ranges long enough for 2, 3, 4 or 5 pairs to a tile the best is taken,
 // or none.  (Cut wherever 16 k-slices were gained: 560 x 768 x 1496 backward 44
-// us, so 40; with any number of pairs to a tile the forward of 200 x 256 x 8192
-// 63 us, so 29; never cut, the backward's group of 4916 x 2048 x 5632 20 us
+// us, 36 so; with any number of pairs to a tile the forward of 200 x 256 x 8192
+// 63 us, 29 so; never cut, the backward's group of 4916 x 2048 x 5632 20 us
 // more.)
 constexpr int kCutCost = 14, kPartCost = 8, kMaxParts = 4;
 struct Sched {

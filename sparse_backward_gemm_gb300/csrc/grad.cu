@@ -5,11 +5,11 @@
 //   g <- coef g, coef = scale min(1, max_norm / (norm + 1e-6)).
 // HBM-bound: the norm reads every value once; clipping needs the whole norm
 // before it writes the first value, so it reads a second time.
-//   Measured: the norm of 1.1 G f32 values (135 tensors, 4.4 GB) 604 us, 7.3 TB/s;
-// of 44 M 35 us (29 of them reading at 6 TB/s); of 492 K 7.7 us.  (A set of up to
+//   Measured: the norm of 1.1 G f32 values (135 tensors, 4.4 GB) 615 us, 7.2 TB/s;
+// of 44 M 35 us (29 of them reading at 6 TB/s); of 492 K 8.2 us.  (A set of up to
 // 4 MB in one launch, as a cluster of 16 CTAs with the partials in its shared
 // memory: 8.7 us, and 12 instead of 8 for clipping 2 MB: too few SMs read.)
-// Clipping them 1965 us (three passes at 6.7 TB/s) and 74 us, 88 from memory.
+// Clipping them 1988 us (three passes at 6.6 TB/s) and 75 us, 89 from memory.
 #include <algorithm>
 
 #include "internal.h"
