@@ -644,9 +644,8 @@ typedef struct {
 /* All M rows (the forward stays dense).  up [M, 2F] = [g | u] is what the
  * backward reads; NULL: not kept.  g and u are f32 until s is formed; s is
  * rounded to bf16 for the second product, which the tensor cores take in bf16
- * (of up to 64 tokens to the sum of two bf16 values), and each output is
- * rounded once.  The outputs overlap each other and the
- * inputs nowhere.  Workspace: collider_ffn_fwd_workspace_size(). */
+ * (of up to 64 tokens to the sum of two bf16 values), and each output is rounded
+ * once.  The outputs overlap each other and the inputs nowhere.  Workspace: collider_ffn_fwd_workspace_size(). */
 size_t collider_ffn_fwd_workspace_size(const collider_ffn_desc* desc);
 collider_status collider_ffn_fwd(const collider_ffn_desc* desc, const void* x, const void* w_up,
                                  const void* w_down, void* up, void* y, void* ws, size_t ws_bytes,
@@ -690,9 +689,10 @@ typedef struct {
  * (kind); norms[i] (may be NULL, as may norm): the same of gradient i alone; f32, device.
  * scale (finite, > 0) stands for what the gradients are still to be multiplied
  * by, such as one over the number of summed micro-batches.  Squares are added at
- * most 16 at a time in f32 and those sums in f64 (the squares too where f32's would
- * overflow or vanish); the root and its product with scale are rounded to f32 once:
- * within 10 2^-24, and finite wherever it fits f32.  A NaN gives NaN.  Bit-identical from run to run.
+ * most 16 at a time in f32 and those sums in f64 (the squares too where f32's
+ * would overflow or vanish); the root times scale is rounded to f32 once: off by
+ * 10 2^-24 of its value at most, and finite wherever it fits f32.  A NaN gives
+ * NaN.  Bit-identical from run to run.
  * grads is a host array of count (0 <= count <= 2^20) gradients, read during
  * the call only; at most 2^40 values in all.  A gradient listed twice counts
  * twice.  Workspace: collider_grad_norm_workspace_size(). */
